@@ -260,8 +260,7 @@ def _headers(ids, seg, n, P, Hkv, tip):
     u, t = seg // 3, seg % 3
     inseg = torch.arange(seg.numel(), device=seg.device) - tip[seg].long()
     rows = (n.view(-1)[seg] - inseg * P).clamp(max=P)
-    w = torch.stack([rows | (t << 16) | (0x5A << 24), u // Hkv, u % Hkv,
-                     inseg + tip[seg].long() - tip[3 * u].long()], 1)
+    w = torch.stack([rows | (t << 16) | (0x5A << 24), u // Hkv, u % Hkv, inseg], 1)
     return w.to(torch.int32)
 
 
