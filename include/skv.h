@@ -477,6 +477,107 @@ int skv_decode_attention_static(skv_ctx* ctx, const void* q, int q_dtype, int B,
                                 const skv_pools* pools, float* out, float* lse,
                                 int32_t* err_word, int num_splits, void* stream);
 
+/* skv_tree_attention -- attention of N drafted tokens a sequence over the
+   paged store (the step that verifies a speculated continuation; with N = 1
+   and no drafted keys it is a single-token decode whose scores may be capped
+   or biased).  The paper has no counterpart; keys, values and logits of the
+   store are those of skv_decode_attention.  For every sequence b, drafted
+   token i < count[b] and query head hq (kv head h = hq / (Hq/Hkv)):
+     out[b][i][hq] = sum_t softmax_t(s_t) v_t,  lse[b][i][hq] = log sum_t exp(s_t)
+   over the resident tokens of (b, h) and the drafted tokens j < count[b]
+   whose bit j of mask[b][i] is set, with x = q . k_t / sqrt d and
+     s = x                            by default
+     s = softcap tanh(x / softcap)    with softcap > 0
+     s <- s - slopes[hq] (q_pos[b][i] - pos_t)   with slopes,
+   pos_t the position of a resident token (by row_of) or q_pos[b][j] of a
+   drafted one.  A row that sees nothing gives out 0 and lse -inf; rows
+   i >= count[b] are left as they were.  Keys and values that a row's mask
+   hides never reach it, whatever they hold (infinities, NaN).  Sums and
+   softmax statistics are fp32; store keys (as decoded), store values and
+   softmax weights enter the tensor cores as fp16. */
+typedef struct skv_tree {
+  int32_t N;              /* drafted tokens a sequence, 1..64 */
+  int32_t kv_dtype;       /* SKV_Q_FP16 / SKV_Q_BF16: type of K and V */
+  const int32_t* count;   /* int32 [B] device or NULL (N each); taken within 0..N */
+  const void* K;          /* [B][N][Hkv][128] device, or NULL with V: the store alone */
+  const void* V;
+  const uint64_t* mask;   /* [B][N] device, or NULL: each drafted token sees itself
+                             and those before it (a chain).  Bits j >= count[b]
+                             are ignored */
+  int64_t q_stride;       /* elements from a token's q to the next's (the batch stride is
+                             N of them); 0: Hq * 128.  A multiple of 8 */
+  int64_t kv_stride;      /* the same for K and V; 0: Hkv * 128 */
+} skv_tree;
+
+typedef struct skv_score {
+  float softcap;            /* finite, >= 0 (0: none) */
+  int32_t reserved;         /* zero */
+  const float* slopes;      /* fp32 [Hq] device, or NULL: no bias; the rest is then unused */
+  const int32_t* q_pos;     /* int32 [B][N] device: positions of the drafted tokens */
+  const int32_t* row_of;    /* the store's row map [B][Hkv][Tmax] */
+  const int32_t* seq_lens;  /* int32 [B] device */
+  int64_t Tmax;
+} skv_score;
+
+/* Bytes of workspace of skv_tree_attention; page_cap: capacity of page_ids;
+   positions: nonzero when slopes are given. */
+int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, int64_t page_cap,
+                            int positions, int num_splits, size_t* bytes);
+/* q, out: [B][N][Hq][128] in q_dtype (out dense); lse: fp32 [B][N][Hq] or
+   NULL; score: NULL for plain scores.  Hq/Hkv in {1, 2, 4}.  page_tier_indptr
+   may be NULL.  q, K, V and out must be 16-byte aligned.  The workspace needs
+   no initialisation; calls that overlap in time must not share one.  Stream
+   order: as any kernel launch (no early start).  A context with t0_bf16 is
+   refused.  Device errors: SKV_ERR_CORRUPT (bad page id, header or row: the
+   page or row is skipped), SKV_ERR_TIMEOUT. */
+int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, int Hkv,
+                       const skv_tree* tree, const skv_score* score, const int32_t* page_indptr,
+                       const int32_t* page_tier_indptr, const uint32_t* page_ids,
+                       int64_t page_cap, const skv_pools* pools, void* out, float* lse,
+                       int32_t* err_word, void* workspace, size_t ws_bytes, int num_splits,
+                       void* stream);
+
+/* skv_evict -- eviction by accumulated attention weight (technical summary
+   2.2: keep or drop per token and head; the utility that decides is this
+   library's attention mass, see skv_decode_utility).  Of the resident tokens
+   of every (b, h) these stay:
+     - those at positions < sink or >= seq_lens[b] - recent, and those with
+       protect != 0 (whatever keep[b] says);
+     - of the others the highest scores, until keep[b] tokens stay in all;
+       equal scores go by position, the lower first; NaN is the lowest score.
+   A kept token stays in its tier, its stored bytes unchanged; the others
+   become SKV_TIER_DROP.  The result is a new page table in the layout of
+   skv_allocate: per unit the T0, T1, T2 pages, rows in position order, in
+   slots free->ids[t][free_cursor[t] + k] (k in unit order).  The store before
+   the call is only read, so all its pages may go back to the caller's free
+   lists once nothing reads it any more.
+     seq_lens   int32 [B] device
+     score      fp32 [B][Hkv][Tmax] device (skv_decode_utility's utility)
+     protect    uint8 [B][Hkv][Tmax] device or NULL
+     keep       int32 [B] device: tokens to keep per kv head (negative: 0)
+     sink, recent  >= 0
+     tier ... page_ids, page_cap  the store (page_cap: capacity of page_ids)
+     free, free_cursor  device free lists and int32 [3] cursors (read only);
+                free_cursor_out: int32 [3] device or NULL, the cursors after the call
+     pools      holds the old and the new pages
+     tier_out, row_of_out, page_indptr_out, page_tier_indptr_out (or NULL),
+     page_ids_out (capacity out_cap)   the store after the call; must not
+                overlap the store's own arrays
+     workspace  skv_evict_workspace_size bytes
+   Tmax is at most 2^20.  Device errors: SKV_ERR_POOL (free list or page
+   capacity exhausted; the outputs are then unspecified, the old store is
+   intact), SKV_ERR_CORRUPT (a kept token's row lies outside the store; its
+   new row is zero). */
+int skv_evict_workspace_size(const skv_ctx* ctx, int B, int Hkv, int64_t Tmax, size_t* bytes);
+int skv_evict(skv_ctx* ctx, int B, int Hkv, int64_t Tmax, const int32_t* seq_lens,
+              const float* score, const uint8_t* protect, const int32_t* keep, int sink,
+              int recent, const uint8_t* tier, const int32_t* row_of, const int32_t* page_indptr,
+              const uint32_t* page_ids, int64_t page_cap, const skv_free_lists* free,
+              const int32_t* free_cursor, const skv_pools* pools, uint8_t* tier_out,
+              int32_t* row_of_out, int32_t* page_indptr_out, int32_t* page_tier_indptr_out,
+              uint32_t* page_ids_out, int64_t out_cap, int32_t* free_cursor_out,
+              int32_t* err_word, void* workspace, size_t ws_bytes, void* stream);
+
 /* skv_dense_pack_bf16 -- the dense baseline's store: every token of every
    (b, h) kept as bf16 K/V (fp16 inputs rounded to nearest even) in pages of
    P rows with the T0 page layout.  Slots come from free_ids in (b, h, page)

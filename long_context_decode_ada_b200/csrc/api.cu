@@ -1004,6 +1004,215 @@ int skv_decode_attention_static(skv_ctx* ctx, const void* q, int q_dtype, int B,
                        stream, name);
 }
 
+// The context's device current for the duration of a call.
+struct DeviceScope {
+  int before = -1;
+  cudaError_t status;
+  explicit DeviceScope(int device) {
+    status = cudaGetDevice(&before);
+    if (status == cudaSuccess && before != device) status = cudaSetDevice(device);
+    if (before == device) before = -1;
+  }
+  ~DeviceScope() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+static bool tree_sizes_ok(int B, int N, int Hq, int Hkv, int64_t page_cap) {
+  return B >= 0 && N >= 1 && N <= 64 && Hkv > 0 && Hkv <= 1024 && Hq > 0 && Hq % Hkv == 0 &&
+         (Hq / Hkv == 1 || Hq / Hkv == 2 || Hq / Hkv == 4) && page_cap >= 0 &&
+         page_cap <= (1LL << 25) && (long long)B * Hkv <= (1LL << 20);
+}
+
+int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, int64_t page_cap,
+                            int positions, int num_splits, size_t* bytes) {
+  if (!ctx || !bytes) return fail(SKV_ERR_ARG, "skv_tree_workspace_size: null argument");
+  if (!tree_sizes_ok(B, N, Hq, Hkv, page_cap) || num_splits < 0)
+    return fail(SKV_ERR_ARG, "skv_tree_workspace_size: bad sizes");
+  *bytes = positions ? (size_t)page_cap * ctx->P * 4 : 0;
+  return ok();
+}
+
+int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, int Hkv,
+                       const skv_tree* tree, const skv_score* score, const int32_t* page_indptr,
+                       const int32_t* page_tier_indptr, const uint32_t* page_ids,
+                       int64_t page_cap, const skv_pools* pools, void* out, float* lse,
+                       int32_t* err_word, void* workspace, size_t ws_bytes, int num_splits,
+                       void* stream) {
+  const char* name = "skv_tree_attention";
+  if (!ctx || !tree) return fail(SKV_ERR_ARG, "%s: null argument", name);
+  if (ctx->t0_bf16) return fail(SKV_ERR_ARG, "%s: not for bf16 T0 pages", name);
+  if (!tree_sizes_ok(B, tree->N, Hq, Hkv, page_cap) || num_splits < 0)
+    return fail(SKV_ERR_ARG,
+                "%s: need B >= 0, 1 <= N <= 64, Hq/Hkv in {1, 2, 4}, B * Hkv <= 2^20, "
+                "0 <= page_cap <= 2^25, num_splits >= 0",
+                name);
+  if ((q_dtype != SKV_Q_BF16 && q_dtype != SKV_Q_FP16) ||
+      (tree->kv_dtype != SKV_Q_BF16 && tree->kv_dtype != SKV_Q_FP16))
+    return fail(SKV_ERR_ARG, "%s: unknown dtype", name);
+  if (!tree->K != !tree->V) return fail(SKV_ERR_ARG, "%s: K and V go together", name);
+  const int64_t qs = tree->q_stride ? tree->q_stride : (int64_t)Hq * 128;
+  const int64_t ks = tree->kv_stride ? tree->kv_stride : (int64_t)Hkv * 128;
+  if (qs < (int64_t)Hq * 128 || ks < (int64_t)Hkv * 128 || qs % 8 || ks % 8 ||
+      qs > (1LL << 31) || ks > (1LL << 31))
+    return fail(SKV_ERR_ARG, "%s: strides must cover a token and be multiples of 8", name);
+  const float cap = score ? score->softcap : 0.0f;
+  if (!(cap >= 0.0f) || std::isinf(cap))
+    return fail(SKV_ERR_ARG, "%s: softcap must be finite and not negative", name);
+  const bool bias = score && score->slopes;
+  if (bias && (!score->q_pos || !score->row_of || !score->seq_lens || score->Tmax < 0 ||
+               score->Tmax > (1LL << 23)))
+    return fail(SKV_ERR_ARG, "%s: slopes need q_pos, row_of, seq_lens and Tmax", name);
+  if (!valid_pools(pools, 3)) return fail(SKV_ERR_ARG, "%s: bad pools", name);
+  if (B == 0) return ok();
+  if (!q || !page_indptr || !out || !err_word || (page_cap > 0 && !page_ids))
+    return fail(SKV_ERR_ARG, "%s: null argument", name);
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(tree->K) | reinterpret_cast<uintptr_t>(tree->V)) & 15)
+    return fail(SKV_ERR_ARG, "%s: q, K, V and out must be 16-byte aligned", name);
+  size_t need = 0;
+  const int rc = skv_tree_workspace_size(ctx, B, tree->N, Hq, Hkv, page_cap, bias, num_splits, &need);
+  if (rc != SKV_OK) return rc;
+  if (need > 0 && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15)))
+    return fail(SKV_ERR_ARG, "%s: a 16-byte aligned workspace of %zu bytes needed", name, need);
+  skv::TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.q_bf16 = q_dtype == SKV_Q_BF16;
+  p.q_stride = qs;
+  p.B = B;
+  p.N = tree->N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.count = tree->count;
+  p.K = tree->K;
+  p.V = tree->V;
+  p.kv_bf16 = tree->kv_dtype == SKV_Q_BF16;
+  p.kv_stride = ks;
+  p.mask = reinterpret_cast<const unsigned long long*>(tree->mask);
+  p.softcap = cap;
+  if (bias) {
+    p.slopes = score->slopes;
+    p.q_pos = score->q_pos;
+    p.row_of = score->row_of;
+    p.seq_lens = score->seq_lens;
+    p.Tmax = score->Tmax;
+    p.row_pos = static_cast<int32_t*>(workspace);
+  }
+  p.indptr = page_indptr;
+  p.tier_indptr = page_tier_indptr;
+  p.ids = page_ids;
+  p.page_cap = page_cap;
+  for (int t = 0; t < 3; ++t) {
+    p.pool[t] = static_cast<const uint8_t*>(pools->base[t]);
+    p.slots[t] = pools->slots[t];
+    p.stride[t] = ctx->stride[t];
+  }
+  p.out = out;
+  p.lse = lse;
+  p.err = err_word;
+  p.P = ctx->P;
+  p.qk_scale = (float)(1.0 / std::sqrt(128.0));
+  p.t1_scheme = ctx->t1_scheme;
+  std::memcpy(p.rho, ctx->rho_levels, sizeof(p.rho));
+  std::memcpy(p.cos6, ctx->cos6, sizeof(p.cos6));
+  std::memcpy(p.sin6, ctx->sin6, sizeof(p.sin6));
+  std::memcpy(p.cos4, ctx->cos4, sizeof(p.cos4));
+  std::memcpy(p.sin4, ctx->sin4, sizeof(p.sin4));
+  std::memcpy(p.cos5, ctx->cos5, sizeof(p.cos5));
+  std::memcpy(p.sin5, ctx->sin5, sizeof(p.sin5));
+  DeviceScope dev(ctx->device);
+  if (dev.status != cudaSuccess) return cuda_fail(dev.status, name);
+  const cudaError_t e = skv::launch_tree(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return ok();
+}
+
+static bool evict_sizes_ok(int B, int Hkv, int64_t Tmax) {
+  return B >= 0 && Hkv > 0 && Hkv <= 1024 && Tmax >= 0 && Tmax <= skv::kEvictTmax &&
+         (long long)B * Hkv <= (1LL << 20);
+}
+
+int skv_evict_workspace_size(const skv_ctx* ctx, int B, int Hkv, int64_t Tmax, size_t* bytes) {
+  if (!ctx || !bytes) return fail(SKV_ERR_ARG, "skv_evict_workspace_size: null argument");
+  if (!evict_sizes_ok(B, Hkv, Tmax))
+    return fail(SKV_ERR_ARG, "skv_evict_workspace_size: bad sizes (Tmax is at most 2^20)");
+  *bytes = skv::evict_workspace_bytes(B, Hkv, Tmax, ctx->P);
+  return ok();
+}
+
+int skv_evict(skv_ctx* ctx, int B, int Hkv, int64_t Tmax, const int32_t* seq_lens,
+              const float* score, const uint8_t* protect, const int32_t* keep, int sink,
+              int recent, const uint8_t* tier, const int32_t* row_of, const int32_t* page_indptr,
+              const uint32_t* page_ids, int64_t page_cap, const skv_free_lists* free,
+              const int32_t* free_cursor, const skv_pools* pools, uint8_t* tier_out,
+              int32_t* row_of_out, int32_t* page_indptr_out, int32_t* page_tier_indptr_out,
+              uint32_t* page_ids_out, int64_t out_cap, int32_t* free_cursor_out,
+              int32_t* err_word, void* workspace, size_t ws_bytes, void* stream) {
+  const char* name = "skv_evict";
+  if (!ctx) return fail(SKV_ERR_ARG, "%s: null ctx", name);
+  if (!evict_sizes_ok(B, Hkv, Tmax) || page_cap < 0 || page_cap > 0x7FFFFFFFLL || out_cap < 0 ||
+      out_cap > 0x7FFFFFFFLL)
+    return fail(SKV_ERR_ARG, "%s: bad sizes (Tmax is at most 2^20, B * Hkv at most 2^20)", name);
+  if (sink < 0 || recent < 0) return fail(SKV_ERR_ARG, "%s: sink and recent are not negative", name);
+  if (!valid_pools(pools, 3))
+    return fail(SKV_ERR_ARG, "%s: pools need 128-byte aligned bases", name);
+  if (!free) return fail(SKV_ERR_ARG, "%s: null argument", name);
+  for (int t = 0; t < 3; ++t)
+    if (free->len[t] < 0 || (free->len[t] > 0 && !free->ids[t]))
+      return fail(SKV_ERR_ARG, "%s: bad free list %d", name, t);
+  if (B == 0) return ok();
+  if (!seq_lens || !keep || !page_indptr || !free_cursor || !page_indptr_out || !err_word ||
+      (Tmax > 0 && (!score || !tier || !row_of || !tier_out || !row_of_out)) ||
+      (page_cap > 0 && !page_ids) || (out_cap > 0 && !page_ids_out))
+    return fail(SKV_ERR_ARG, "%s: null argument", name);
+  if (tier == tier_out || row_of == row_of_out || page_indptr == page_indptr_out ||
+      page_ids == page_ids_out)
+    return fail(SKV_ERR_ARG, "%s: the new store's arrays must not be the old one's", name);
+  const size_t need = skv::evict_workspace_bytes(B, Hkv, Tmax, ctx->P);
+  if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return fail(SKV_ERR_ARG, "%s: a 16-byte aligned workspace of %zu bytes needed", name, need);
+  skv::EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Tmax = Tmax;
+  p.P = ctx->P;
+  p.seq_lens = seq_lens;
+  p.score = score;
+  p.protect = protect;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.tier = tier;
+  p.row_of = row_of;
+  p.indptr = page_indptr;
+  p.ids = page_ids;
+  p.page_cap = page_cap;
+  for (int t = 0; t < 3; ++t) {
+    p.free_ids[t] = free->ids[t];
+    p.free_len[t] = free->len[t];
+    p.pool[t] = static_cast<uint8_t*>(pools->base[t]);
+    p.slots[t] = pools->slots[t];
+    p.stride[t] = ctx->stride[t];
+  }
+  p.cursor = free_cursor;
+  p.tier_out = tier_out;
+  p.row_of_out = row_of_out;
+  p.indptr_out = page_indptr_out;
+  p.tier_indptr_out = page_tier_indptr_out;
+  p.ids_out = page_ids_out;
+  p.out_cap = out_cap;
+  p.cursor_out = free_cursor_out;
+  p.err = err_word;
+  skv::evict_carve(p, workspace);
+  DeviceScope dev(ctx->device);
+  if (dev.status != cudaSuccess) return cuda_fail(dev.status, name);
+  const cudaError_t e = skv::launch_evict(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return ok();
+}
+
 int skv_set_profile_event(skv_ctx* ctx, void* event) {
   if (!ctx) return fail(SKV_ERR_ARG, "skv_set_profile_event: null ctx");
   ctx->profile_event = static_cast<cudaEvent_t>(event);

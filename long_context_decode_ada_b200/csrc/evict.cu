@@ -1,0 +1,521 @@
+// evict.cu -- eviction by accumulated attention weight: per (sequence, kv
+// head) the sink, the recent window, the protected tokens and the highest
+// scores stay resident, in their tier and with their bytes; the others are
+// dropped and the kept rows packed into new tier-homogeneous pages.
+//
+// Three kernels.  Select: a cluster of C blocks per unit holds the unit's
+// scores in shared memory and finds the cut by a radix select (three digits
+// of 11, 11 and 10 bits, most significant first, the blocks' histograms
+// summed over distributed shared memory), then ranks the kept tokens per tier
+// in position order: tiers, row map and, per new row, its old row.  Plan: one
+// block turns the units' counts into the page table's offsets.  Move: the
+// pages' ids and headers, and every new row's bytes from its old page.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace skv {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr uint32_t kGone = 3;      // state: not resident
+constexpr uint32_t kHeld = 4;      // state bit: stays whatever its score
+constexpr uint32_t kStay = 8;      // state bit: stays
+
+// Scores as unsigned integers of the same order (-0 equals +0, NaN lowest).
+__device__ __forceinline__ uint32_t score_key(float x) {
+  x += 0.0f;
+  const uint32_t b = __float_as_uint(x);
+  if (x != x) return 0u;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+struct SelShared {
+  uint32_t hist[3][kBins];
+  uint32_t scan[kSelWarps];
+  uint32_t part[4];             // this block's totals, read by the cluster
+  uint32_t part2[4];
+  uint32_t warp[3][kSelWarps];
+  uint32_t bin, above;
+  int live;                     // candidates of the unit
+};
+
+__device__ __forceinline__ uint32_t warp_sum(uint32_t x) {
+  return __reduce_add_sync(0xFFFFFFFFu, x);
+}
+
+// Sum over the cluster of word `k` of part / part2, and the sum before this block.
+template <class Cluster>
+__device__ __forceinline__ void cluster_sum(Cluster& cl, uint32_t* word, uint32_t& before,
+                                            uint32_t& total) {
+  before = total = 0;
+  const unsigned me = cl.block_rank(), n = cl.num_blocks();
+  for (unsigned r = 0; r < n; ++r) {
+    const uint32_t x = *cl.map_shared_rank(word, r);
+    if (r < me) before += x;
+    total += x;
+  }
+}
+
+__global__ void __launch_bounds__(kSelThreads)
+    evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ SelShared sm;
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const long long u = blockIdx.x / p.clusters;
+  const int b = (int)(u / p.Hkv);
+  const long long T = min(max((long long)p.seq_lens[b], 0ll), p.Tmax);
+  const long long lo = (long long)cl.block_rank() * p.chunk;
+  const int len = (int)max(0ll, min((long long)p.chunk, p.Tmax - lo));
+  uint32_t* const keys = reinterpret_cast<uint32_t*>(raw);
+  uint8_t* const smst = raw + (p.cached ? 4 * (size_t)p.chunk : 0);
+  const long long base = u * p.Tmax + lo;
+
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
+  __syncthreads();
+
+  // states (one byte a position) and keys; the first digit's histogram
+  uint32_t n_cand = 0, n_held = 0;
+  for (int i = tid; i < len; i += kSelThreads) {
+    const long long t = lo + i;
+    uint32_t st = t < T ? p.tier[base + i] : kGone;
+    if (st >= kGone) st = kGone;
+    if (st != kGone && (t < p.sink || t >= T - p.recent || (p.protect && p.protect[base + i])))
+      st |= kHeld;
+    smst[i] = (uint8_t)st;
+    if (st < kGone) {
+      const uint32_t k = score_key(p.score[base + i]);
+      if (p.cached) keys[i] = k;
+      atomicAdd(&sm.hist[0][k >> 21], 1u);
+      ++n_cand;
+    } else if (st & kHeld) {
+      ++n_held;
+    }
+  }
+  n_cand = warp_sum(n_cand);
+  n_held = warp_sum(n_held);
+  if (lane == 0) {
+    sm.warp[0][w] = n_cand;
+    sm.warp[1][w] = n_held;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t a = 0, c = 0;
+    for (int k = 0; k < kSelWarps; ++k) {
+      a += sm.warp[0][k];
+      c += sm.warp[1][k];
+    }
+    sm.part[0] = a;
+    sm.part[1] = c;
+  }
+  cl.sync();
+  uint32_t before, cand, held;
+  cluster_sum(cl, &sm.part[0], before, cand);
+  cluster_sum(cl, &sm.part[1], before, held);
+  const long long want = (long long)p.keep[b] - held;
+  // all candidates stay, none does, or the `need` highest
+  const uint32_t need = want <= 0 ? 0u : (uint32_t)min(want, (long long)cand);
+  uint32_t cut = 0, ties = 0;  // keys above `cut` stay, and the first `ties` equal to it
+  const bool some = need > 0 && need < cand;
+  if (some) {
+    uint32_t left = need, prefix = 0;
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
+      const int up = d == 1 ? 21 : 10;   // bits of the prefix from here
+      if (d > 0) {
+        for (int i = tid; i < len; i += kSelThreads) {
+          if (smst[i] >= kGone) continue;
+          const uint32_t k = p.cached ? keys[i] : score_key(p.score[base + i]);
+          if ((k >> up) == (prefix >> up))
+            atomicAdd(&sm.hist[d][(k >> shift) & (d == 2 ? 1023u : 2047u)], 1u);
+        }
+        cl.sync();
+      }
+      // bins from the highest: thread t holds bins 4 t' .. 4 t' + 3, t' from the top
+      uint32_t c[4], tot = 0;
+      const int b0 = kBins - 4 - 4 * tid;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = 0;
+      for (unsigned r = 0; r < cl.num_blocks(); ++r) {
+        const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(&sm.hist[d][b0], r));
+        c[3] += x.x;
+        c[2] += x.y;
+        c[1] += x.z;
+        c[0] += x.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tot += c[e];
+      uint32_t inc = tot;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sm.scan[w] = inc;
+      __syncthreads();
+      uint32_t ex = inc - tot;
+      for (int k = 0; k < w; ++k) ex += sm.scan[k];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (ex < left && left <= ex + c[e]) {
+          sm.bin = (uint32_t)(b0 + 3 - e);
+          sm.above = ex;
+        }
+        ex += c[e];
+      }
+      __syncthreads();
+      prefix |= sm.bin << shift;
+      left -= sm.above;
+      __syncthreads();
+    }
+    cut = prefix;
+    ties = left;
+  }
+
+  // ties in position order: warp w takes the w-th part of the block's span
+  const int span = (((len + kSelWarps - 1) / kSelWarps) + 31) / 32 * 32;
+  const int i0 = min(len, w * span), i1 = min(len, i0 + span);
+  uint32_t tie_at = 0;
+  if (some) {
+    uint32_t cnt = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+      if (smst[i] >= kGone) continue;
+      cnt += (p.cached ? keys[i] : score_key(p.score[base + i])) == cut;
+    }
+    cnt = warp_sum(cnt);
+    if (lane == 0) sm.warp[0][w] = cnt;
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t a = 0;
+      for (int k = 0; k < kSelWarps; ++k) a += sm.warp[0][k];
+      sm.part2[3] = a;
+    }
+    cl.sync();
+    uint32_t total;
+    cluster_sum(cl, &sm.part2[3], tie_at, total);
+    for (int k = 0; k < w; ++k) tie_at += sm.warp[0][k];
+  }
+
+  // who stays, and how many of each tier
+  uint32_t n[3] = {0, 0, 0};
+  const uint32_t lt = (1u << lane) - 1;
+  for (int i = i0; i < i1; i += 32) {
+    const int k = i + lane;
+    uint32_t st = k < i1 ? smst[k] : kGone;
+    bool stay = (st & kHeld) != 0;
+    if (some) {
+      const uint32_t key = st < kGone ? (p.cached ? keys[k] : score_key(p.score[base + k])) : 0u;
+      const bool tie = st < kGone && key == cut;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, tie);
+      if (st < kGone) stay = key > cut || (tie && tie_at + __popc(m & lt) < ties);
+      tie_at += __popc(m);
+    } else if (st < kGone) {
+      stay = need > 0;
+    }
+    if (k < i1 && stay) smst[k] = (uint8_t)(st | kStay);
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+      n[t] += __popc(__ballot_sync(0xFFFFFFFFu, stay && (st & 3u) == (uint32_t)t));
+  }
+  __syncthreads();  // the tie counts of sm.warp are read above
+  if (lane == 0)
+    for (int t = 0; t < 3; ++t) sm.warp[t][w] = n[t];
+  __syncthreads();
+  if (tid < 3) {
+    uint32_t a = 0;
+    for (int k = 0; k < kSelWarps; ++k) a += sm.warp[tid][k];
+    sm.part2[tid] = a;
+  }
+  cl.sync();
+  uint32_t at[3], total[3];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) cluster_sum(cl, &sm.part2[t], at[t], total[t]);
+  const uint32_t P = (uint32_t)p.P;
+  uint32_t first[3];  // the tier's first row in the unit's page list
+  first[0] = 0;
+  first[1] = (total[0] + P - 1) / P * P;
+  first[2] = first[1] + (total[1] + P - 1) / P * P;
+  if (tid == 0 && cl.block_rank() == 0)
+    for (int t = 0; t < 3; ++t) p.counts[3 * u + t] = (int32_t)total[t];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    for (int k = 0; k < w; ++k) at[t] += sm.warp[t][k];
+    at[t] += first[t];
+  }
+  int32_t* const src = p.src + u * p.src_stride;
+  for (int i = i0; i < i1; i += 32) {
+    const int k = i + lane;
+    const uint32_t st = k < i1 ? smst[k] : 0u;
+    const bool stay = (st & kStay) != 0;
+    int row = -1;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      const bool mine = stay && (st & 3u) == (uint32_t)t;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
+      if (mine) row = (int)(at[t] + __popc(m & lt));
+      at[t] += __popc(m);
+    }
+    if (k < i1) {
+      p.tier_out[base + k] = (uint8_t)(stay ? st & 3u : (uint32_t)SKV_TIER_DROP);
+      p.row_of_out[base + k] = row;
+      if (stay) src[row] = p.row_of[base + k];
+    }
+  }
+  cl.sync();  // no block leaves while another reads its shared memory
+}
+
+// One block: the page offsets of every (unit, tier) and its first free-list
+// entry, by a scan of the units' page counts.
+__global__ void __launch_bounds__(1024) evict_plan_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ long long sc[32][4];
+  const int U = p.B * p.Hkv, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (U + 1023) / 1024;
+  const int a = min(U, tid * per), z = min(U, a + per);
+  long long n[4] = {0, 0, 0, 0};
+  for (int u = a; u < z; ++u)
+    for (int t = 0; t < 3; ++t) n[t] += (p.counts[3 * u + t] + p.P - 1) / p.P;
+  n[3] = n[0] + n[1] + n[2];
+  long long ex[4];
+  for (int k = 0; k < 4; ++k) {
+    long long x = n[k];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sc[w][k] = x;
+    ex[k] = x - n[k];
+  }
+  __syncthreads();
+  long long tot[4];
+  for (int k = 0; k < 4; ++k) {
+    tot[k] = 0;
+    for (int j = 0; j < 32; ++j) {
+      if (j < w) ex[k] += sc[j][k];
+      tot[k] += sc[j][k];
+    }
+  }
+  for (int u = a; u < z; ++u) {
+    p.indptr_out[u] = (int32_t)ex[3];
+    for (int t = 0; t < 3; ++t) {
+      const long long c = (p.counts[3 * u + t] + p.P - 1) / p.P;
+      if (p.tier_indptr_out) p.tier_indptr_out[3 * u + t] = (int32_t)ex[3];
+      p.tbase[3 * u + t] = (int32_t)ex[t];
+      ex[3] += c;
+      ex[t] += c;
+    }
+  }
+  if (tid == 0) {
+    p.indptr_out[U] = (int32_t)tot[3];
+    if (p.tier_indptr_out) p.tier_indptr_out[3 * U] = (int32_t)tot[3];
+    if (tot[3] > p.out_cap) report(p.err, SKV_ERR_POOL);
+    for (int t = 0; t < 3; ++t) {
+      const int c = p.cursor[t];
+      if (c < 0 || c + tot[t] > p.free_len[t]) report(p.err, SKV_ERR_POOL);
+      if (p.cursor_out) p.cursor_out[t] = (int32_t)min(c + tot[t], 0x7FFFFFFFll);
+    }
+  }
+}
+
+// the old page of local row `loc` of unit u, or null when the table does not
+// hold it as a page of tier t
+__device__ __forceinline__ const uint8_t* old_page(const EvictParams& p, long long u, int t,
+                                                   int loc) {
+  if (loc < 0) return nullptr;
+  const long long g = (long long)p.indptr[u] + loc / p.P;
+  if (g < 0 || g >= p.indptr[u + 1] || g >= p.page_cap) return nullptr;
+  const uint32_t id = p.ids[g], slot = id & 0x3FFFFFFFu;
+  if ((int)(id >> 30) != t || (long long)slot >= p.slots[t]) return nullptr;
+  return p.pool[t] + (long long)slot * p.stride[t];
+}
+
+__device__ __forceinline__ uint4 load4(const uint8_t* at) {
+  return at ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+}
+
+// A warp per 8 rows of a new page.  A row's values lie in 16-byte chunks
+// shared with its pair row (the matrix-fragment order): a new chunk is the
+// byte (T1 / T2) or half-word (T0) interleave of two old ones.
+__global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
+  const int U = p.B * p.Hkv, P = p.P, lane = threadIdx.x & 31;
+  const int oct = P >> 3, lo3 = __ffs(oct) - 1;
+  const long long total = min((long long)p.indptr_out[U], p.out_cap) << lo3;
+  const long long nw = ((long long)gridDim.x * blockDim.x) >> 5;
+  const long long me = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const long long per = (total + nw - 1) / nw;
+  long long task = me * per;
+  const long long end = min(total, task + per);
+  if (task >= end) return;
+  int u = 0, hi = U;
+  while (hi - u > 1) {  // the unit of the first page
+    const int mid = (u + hi) >> 1;
+    if (p.indptr_out[mid] <= (task >> lo3)) u = mid; else hi = mid;
+  }
+  for (; task < end; ++task) {
+    const long long g = task >> lo3;
+    const int blk = (int)(task & (oct - 1));
+    while (g >= p.indptr_out[u + 1]) ++u;
+    int pg = (int)(g - p.indptr_out[u]);
+    const int local = pg;
+    const int n0 = p.counts[3 * u], n1 = p.counts[3 * u + 1], n2 = p.counts[3 * u + 2];
+    const int p0 = (n0 + P - 1) / P, p1 = (n1 + P - 1) / P;
+    int t = 0, n = n0;
+    if (pg >= p0 + p1) {
+      t = 2;
+      n = n2;
+      pg -= p0 + p1;
+    } else if (pg >= p0) {
+      t = 1;
+      n = n1;
+      pg -= p0;
+    }
+    const long long fi = (long long)p.cursor[t] + p.tbase[3 * u + t] + pg;
+    const uint32_t slot = fi >= 0 && fi < p.free_len[t] ? p.free_ids[t][fi] : 0xFFFFFFFFu;
+    if (slot > 0x3FFFFFFFu || (long long)slot >= p.slots[t]) {
+      if (lane == 0) report(p.err, SKV_ERR_POOL);
+      continue;
+    }
+    uint8_t* const page = p.pool[t] + (long long)slot * p.stride[t];
+    const int rows = min(P, n - pg * P);
+    if (blk == 0 && lane == 0) {
+      p.ids_out[g] = ((uint32_t)t << 30) | slot;
+      *reinterpret_cast<uint4*>(page) =
+          make_uint4((uint32_t)rows | ((uint32_t)t << 16) | ((uint32_t)kPageMagic << 24),
+                     (uint32_t)(u / p.Hkv), (uint32_t)(u % p.Hkv), (uint32_t)pg);
+    }
+    // lane r < 8: the old page and row of new row 8 blk + r
+    const int rn = 8 * blk + (lane & 7);
+    const uint8_t* op = nullptr;
+    int ro = 0;
+    if (rn < rows) {
+      const int loc = p.src[(long long)u * p.src_stride + (long long)local * P + rn];
+      op = old_page(p, u, t, loc);
+      if (!op && lane < 8) report(p.err, SKV_ERR_CORRUPT);
+      ro = loc & (P - 1);
+    }
+    const auto page_of = [&](int r) {
+      return reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(op), r));
+    };
+    const auto row_of = [&](int r) { return __shfl_sync(0xFFFFFFFFu, ro, r); };
+    const int t4 = lane & 3;  // values: lane (g, t4) holds rows 2 t4, 2 t4 + 1
+    const uint8_t *pa = page_of(2 * t4), *pb = page_of(2 * t4 + 1);
+    const int ra = row_of(2 * t4), rb = row_of(2 * t4 + 1);
+    const int la = 16 * ((lane & ~3) + ((ra & 7) >> 1)), lb = 16 * ((lane & ~3) + ((rb & 7) >> 1));
+    if (t == SKV_TIER_T0) {
+      // keys: 16 chunks a row, two rows at a time
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 2 * k + (lane >> 4), c = lane & 15;
+        const uint8_t* o = page_of(r);
+        const int q = row_of(r);
+        const uint4 x = load4(o ? o + kHdrBytes + q * 256 + (c ^ (4 * (q & 1))) * 16 : nullptr);
+        *reinterpret_cast<uint4*>(page + kHdrBytes + (8 * blk + r) * 256 + (c ^ (4 * (r & 1))) * 16) = x;
+      }
+      const int vs = kHdrBytes + 256 * P;
+      const uint32_t sel = (ra & 1 ? 0x32u : 0x10u) | (rb & 1 ? 0x7600u : 0x5400u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = load4(pa ? pa + vs + (ra >> 3) * 2048 + 512 * k + la : nullptr);
+        const uint4 y = load4(pb ? pb + vs + (rb >> 3) * 2048 + 512 * k + lb : nullptr);
+        *reinterpret_cast<uint4*>(page + vs + blk * 2048 + 512 * k + 16 * lane) =
+            make_uint4(__byte_perm(x.x, y.x, sel), __byte_perm(x.y, y.y, sel),
+                       __byte_perm(x.z, y.z, sel), __byte_perm(x.w, y.w, sel));
+      }
+      continue;
+    }
+    const int cb = t == SKV_TIER_T1 ? 64 : 48;
+    if (lane < 16) {  // radius (lanes 0-7) and scale (lanes 8-15)
+      const int sec = kHdrBytes + (lane >= 8 ? (2 + cb) * P : 0);
+      const uint16_t x = op ? *reinterpret_cast<const uint16_t*>(op + sec + 2 * ro) : (uint16_t)0;
+      *reinterpret_cast<uint16_t*>(page + sec + 2 * rn) = x;
+    }
+    {  // codes: cb / 16 chunks a row
+      const int ch = cb / 16, r = lane / ch, c = lane - r * ch;
+      const uint8_t* o = page_of(r & 7);
+      const int q = row_of(r & 7);
+      if (r < 8) {
+        const uint4 x = load4(o ? o + kHdrBytes + 2 * P + cb * q + 16 * c : nullptr);
+        *reinterpret_cast<uint4*>(page + kHdrBytes + 2 * P + cb * (8 * blk + r) + 16 * c) = x;
+      }
+    }
+    const int vs = kHdrBytes + (4 + cb) * P;
+    // bytes (row 2 t4, row 2 t4 + 1) x (dims d, d + 8) of each word
+    const uint32_t sel = ra & 1 ? (rb & 1 ? 0x7351u : 0x6341u) : (rb & 1 ? 0x7250u : 0x6240u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 x = load4(pa ? pa + vs + (ra >> 3) * 1024 + 512 * k + la : nullptr);
+      const uint4 y = load4(pb ? pb + vs + (rb >> 3) * 1024 + 512 * k + lb : nullptr);
+      *reinterpret_cast<uint4*>(page + vs + blk * 1024 + 512 * k + 16 * lane) =
+          make_uint4(__byte_perm(x.x, y.x, sel), __byte_perm(x.y, y.y, sel),
+                     __byte_perm(x.z, y.z, sel), __byte_perm(x.w, y.w, sel));
+    }
+  }
+}
+
+// Blocks per unit: chunks of about 16384 positions, at most 8 (the portable
+// cluster size).  The keys stay in shared memory while they fit.
+int evict_clusters(long long Tmax) {
+  int c = 1;
+  while (c < 8 && Tmax > 16384ll * c) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+size_t evict_workspace_bytes(int B, int Hkv, long long Tmax, int P) {
+  const size_t U = (size_t)B * Hkv;
+  return 4 * (6 * U + U * (size_t)(Tmax + 3 * P));
+}
+
+void evict_carve(EvictParams& p, void* ws) {
+  const size_t U = (size_t)p.B * p.Hkv;
+  int32_t* w = static_cast<int32_t*>(ws);
+  p.counts = w;
+  p.tbase = w + 3 * U;
+  p.src = w + 6 * U;
+  p.src_stride = p.Tmax + 3 * p.P;
+}
+
+cudaError_t launch_evict(EvictParams& p, cudaStream_t stream) {
+  const long long U = (long long)p.B * p.Hkv;
+  if (U == 0) return cudaSuccess;
+  p.clusters = evict_clusters(p.Tmax);
+  p.chunk = (int)((p.Tmax + p.clusters - 1) / p.clusters + 15) / 16 * 16;
+  constexpr int kMaxSmem = 160 * 1024;
+  p.cached = 5ll * p.chunk <= kMaxSmem;
+  const long long smem = (p.cached ? 5ll : 1ll) * p.chunk;
+  if (smem > 200 * 1024) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(U * p.clusters));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.clusters;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  if (e != cudaSuccess) return e;
+  evict_plan_kernel<<<1, 1024, 0, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  evict_move_kernel<<<148 * 8, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace skv

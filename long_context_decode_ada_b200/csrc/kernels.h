@@ -254,4 +254,81 @@ struct TranscodeParams {
 cudaError_t launch_transcode(const TranscodeParams& p, cudaStream_t stream);
 cudaError_t launch_dense_plan(AllocParams& p, cudaStream_t stream);
 
+// Attention of drafted tokens over the store (tree.cu).
+struct TreeParams {
+  const void* q;              // [B][N][Hq][128], token stride q_stride elements
+  int q_bf16;
+  long long q_stride;
+  int B, N, Hq, Hkv;
+  const int32_t* count;       // [B] drafted tokens of each sequence, or NULL (N)
+  const void* K;              // drafted keys / values [B][N][Hkv][128], or NULL
+  const void* V;
+  int kv_bf16;
+  long long kv_stride;
+  const unsigned long long* mask;  // [B][N] or NULL (a chain)
+  float softcap;              // 0: none
+  const float* slopes;        // [Hq] or NULL
+  const int32_t* q_pos;       // [B][N]
+  const int32_t* row_of;      // [B][Hkv][Tmax] (with slopes)
+  const int32_t* seq_lens;    // [B]
+  long long Tmax;
+  int32_t* row_pos;           // [page_cap * P] (workspace, with slopes)
+  const int32_t* indptr;
+  const int32_t* tier_indptr; // [3U + 1] or NULL
+  const uint32_t* ids;
+  long long page_cap;
+  const uint8_t* pool[3];
+  long long slots[3];
+  long long stride[3];
+  void* out;                  // [B][N][Hq][128] in q's type
+  float* lse;                 // [B][N][Hq] or NULL
+  int32_t* err;
+  int P;
+  float qk_scale;
+  int t1_scheme;
+  float rho[4];               // decoded 2-bit shares
+  float cos6[64], sin6[64], cos4[16], sin4[16], cos5[32], sin5[32];
+};
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
+
+// Eviction by score (evict.cu).
+struct EvictParams {
+  int B, Hkv;
+  long long Tmax;
+  int P;
+  const int32_t* seq_lens;
+  const float* score;         // [B][Hkv][Tmax]
+  const uint8_t* protect;     // [B][Hkv][Tmax] or NULL
+  const int32_t* keep;        // [B]
+  int sink, recent;
+  const uint8_t* tier;        // the store
+  const int32_t* row_of;
+  const int32_t* indptr;
+  const uint32_t* ids;
+  long long page_cap;
+  const uint32_t* free_ids[3];
+  long long free_len[3];
+  const int32_t* cursor;      // [3]
+  uint8_t* pool[3];
+  long long slots[3];
+  long long stride[3];
+  uint8_t* tier_out;          // the store after the eviction
+  int32_t* row_of_out;
+  int32_t* indptr_out;
+  int32_t* tier_indptr_out;   // or NULL
+  uint32_t* ids_out;
+  long long out_cap;
+  int32_t* cursor_out;
+  int32_t* err;
+  int32_t* counts;            // workspace: [3U] kept tokens per (unit, tier)
+  int32_t* tbase;             // [3U] pages of the tier before the unit
+  int32_t* src;               // [U][src_stride] old local row of each new one
+  long long src_stride;
+  int clusters, chunk, cached;
+};
+constexpr long long kEvictTmax = 1ll << 20;
+size_t evict_workspace_bytes(int B, int Hkv, long long Tmax, int P);
+void evict_carve(EvictParams& p, void* ws);
+cudaError_t launch_evict(EvictParams& p, cudaStream_t stream);
+
 }  // namespace skv

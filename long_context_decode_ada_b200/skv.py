@@ -36,6 +36,7 @@ EXPORTS = [
     "skv_decode_attention", "skv_decode_attention_static", "skv_decode_attention_host",
     "skv_decode_attention_host_pipelined", "skv_decode_attention_host_drain",
     "skv_decode_utility", "skv_merge_partials",
+    "skv_tree_workspace_size", "skv_tree_attention", "skv_evict_workspace_size", "skv_evict",
     "skv_dense_pack_bf16",
     "skv_dense_decode_bf16",
     "skv_set_profile_event", "skv_set_wait_limit", "skv_check",
@@ -55,6 +56,18 @@ class SkvPools(C.Structure):
 
 class SkvFreeLists(C.Structure):
     _fields_ = [("ids", C.c_void_p * 3), ("len", C.c_int64 * 3)]
+
+
+class SkvTree(C.Structure):
+    _fields_ = [("N", C.c_int32), ("kv_dtype", C.c_int32), ("count", C.c_void_p),
+                ("K", C.c_void_p), ("V", C.c_void_p), ("mask", C.c_void_p),
+                ("q_stride", C.c_int64), ("kv_stride", C.c_int64)]
+
+
+class SkvScore(C.Structure):
+    _fields_ = [("softcap", C.c_float), ("reserved", C.c_int32), ("slopes", C.c_void_p),
+                ("q_pos", C.c_void_p), ("row_of", C.c_void_p), ("seq_lens", C.c_void_p),
+                ("Tmax", C.c_int64)]
 
 
 _p, _i, _i64, _sz = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
@@ -92,6 +105,14 @@ _SIGS = {
                                  _p, _p, _sz, _p]),
     "skv_dense_decode_bf16": (_i, [_p, _p, _i, _i, _i, _i, _p, _p, _p, _i64, _p, _p, _p, _p, _sz,
                                    _i, _p]),
+    "skv_tree_workspace_size": (_i, [_p, _i, _i, _i, _i, _i64, _i, _i, C.POINTER(_sz)]),
+    "skv_tree_attention": (_i, [_p, _p, _i, _i, _i, _i, C.POINTER(SkvTree), C.POINTER(SkvScore),
+                                _p, _p, _p, _i64, C.POINTER(SkvPools), _p, _p, _p, _p, _sz, _i,
+                                _p]),
+    "skv_evict_workspace_size": (_i, [_p, _i, _i, _i64, C.POINTER(_sz)]),
+    "skv_evict": (_i, [_p, _i, _i, _i64, _p, _p, _p, _p, _i, _i, _p, _p, _p, _p, _i64,
+                       C.POINTER(SkvFreeLists), _p, C.POINTER(SkvPools), _p, _p, _p, _p, _p, _i64,
+                       _p, _p, _p, _sz, _p]),
     "skv_set_profile_event": (_i, [_p, _p]),
     "skv_set_wait_limit": (_i, [_p, _i64]),
     "skv_check": (_i, [_p, _p, _p]),
@@ -189,6 +210,30 @@ def _check_ingest(B: int, Hkv: int, Tmax: int, d: int, K=None, V=None, seq_lens=
         _expect(budget, "budget", B, 8, torch.int64, cuda=cuda)
     if quota is not None:
         _expect(quota, "quota", 3 * B, 4, torch.int32, cuda=cuda)
+
+
+_Q_TYPES = {torch.float16: Q_FP16, torch.bfloat16: Q_BF16}
+
+
+def _token_stride(t: torch.Tensor, name: str, shape, device) -> int:
+    """The token stride of a drafted tensor [B][N][H][128]: dense heads, any
+    token stride that is a multiple of 8, the batch N tokens apart (a slice
+    of a fused projection is such a tensor)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _Q_TYPES:
+        raise SkvError(SKV_ERR_ARG, f"{name}: an fp16 or bf16 tensor is required")
+    if t.device != device:
+        raise SkvError(SKV_ERR_ARG, f"{name}: on {t.device}, the store is on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise SkvError(SKV_ERR_ARG, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    B, N, H, d = shape
+    sb, sn, sh, sd = t.stride()
+    if N == 1:  # the token stride of a single token is the batch's
+        sn = sb if B > 1 else H * d
+    if sd != 1 or (H > 1 and sh != d) or (B > 1 and sb != N * sn) or sn < H * d or sn % 8 \
+            or t.data_ptr() % 16:
+        raise SkvError(SKV_ERR_ARG, f"{name}: strides {t.stride()}: need dense heads, a token "
+                                    "stride that is a multiple of 8 and a batch stride of N tokens")
+    return sn
 
 
 def _stream(stream=None):
@@ -502,6 +547,168 @@ class PagedCache:
             num_splits, _stream(stream)))
         return out, lse
 
+    def _own(self, t: Optional[torch.Tensor], name: str, numel: int, dtype: torch.dtype):
+        """Check of a tensor on the store's device (None passes)."""
+        if t is None:
+            return
+        _expect(t, name, numel, dtype.itemsize, dtype)
+        if t.device != self.pools[0].device:
+            raise SkvError(SKV_ERR_ARG, f"{name}: on {t.device}, the store is on "
+                                        f"{self.pools[0].device}")
+
+    def _own_stream(self, stream=None):
+        s = stream if stream is not None else torch.cuda.current_stream(self.pools[0].device)
+        return C.c_void_p(s.cuda_stream)
+
+    def tree_workspace(self, N: int, Hq: int, positions: bool = False,
+                       num_splits: int = 0) -> torch.Tensor:
+        n = C.c_size_t()
+        _check(lib().skv_tree_workspace_size(self.ctx.handle, self.B, N, Hq, self.Hkv,
+                                             self.page_cap, 1 if positions else 0, num_splits,
+                                             C.byref(n)))
+        return torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.device)
+
+    def tree_attention(self, q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                       v: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                       count: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                       slopes: Optional[torch.Tensor] = None,
+                       q_pos: Optional[torch.Tensor] = None,
+                       seq_lens: Optional[torch.Tensor] = None, out=None, lse=None,
+                       workspace=None, num_splits: int = 0, stream=None):
+        """Attention of N <= 64 drafted tokens a sequence over the store
+        (skv_tree_attention); returns (out, lse), lse None unless given.
+          q      fp16 or bf16 [B][N][Hq][128]; out has its type and shape
+          k, v   the drafted tokens' keys and values [B][N][Hkv][128], both of
+                 one type, or None: the store alone.  q, k and v may be slices
+                 of a fused projection (k and v with the same strides)
+          mask   int64 [B][N], bit j of row i: token i sees drafted token j;
+                 None: a chain (tree_mask() makes one from parents)
+          count  int32 [B] drafted tokens of each sequence, None: N
+          softcap  0 or c: scores c tanh(x / c)
+          slopes fp32 [Hq]: scores less slopes[h] times the distance; needs
+                 q_pos int32 [B][N] and seq_lens int32 [B]
+        Rows i >= count[b] of out and lse are left as they were (an `out` made
+        here is zero there)."""
+        dev = self.pools[0].device
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise SkvError(SKV_ERR_ARG, "q: a tensor [B][N][Hq][128] is required")
+        N, Hq = q.shape[1], q.shape[2]
+        t = SkvTree(N=N, kv_dtype=Q_FP16)
+        t.q_stride = _token_stride(q, "q", (self.B, N, Hq, self.ctx.d), dev)
+        if (k is None) != (v is None):
+            raise SkvError(SKV_ERR_ARG, "k and v go together")
+        if k is not None:
+            shape = (self.B, N, self.Hkv, self.ctx.d)
+            t.kv_stride = _token_stride(k, "k", shape, dev)
+            if _token_stride(v, "v", shape, dev) != t.kv_stride or v.dtype != k.dtype:
+                raise SkvError(SKV_ERR_ARG, "k and v: one type and the same strides")
+            t.kv_dtype = _Q_TYPES[k.dtype]
+            t.K, t.V = k.data_ptr(), v.data_ptr()
+        elif mask is not None:
+            raise SkvError(SKV_ERR_ARG, "mask: without drafted keys there is nothing to mask")
+        self._own(mask, "mask", self.B * N, torch.int64)
+        self._own(count, "count", self.B, torch.int32)
+        t.mask = None if mask is None else mask.data_ptr()
+        t.count = None if count is None else count.data_ptr()
+        sc = SkvScore(softcap=float(softcap))
+        if slopes is not None:
+            if q_pos is None or seq_lens is None:
+                raise SkvError(SKV_ERR_ARG, "slopes need q_pos and seq_lens")
+            self._own(slopes, "slopes", Hq, torch.float32)
+            self._own(q_pos, "q_pos", self.B * N, torch.int32)
+            self._own(seq_lens, "seq_lens", self.B, torch.int32)
+            sc.slopes, sc.q_pos = slopes.data_ptr(), q_pos.data_ptr()
+            sc.row_of, sc.seq_lens = self.row_of.data_ptr(), seq_lens.data_ptr()
+            sc.Tmax = self.Tmax
+        if out is None:
+            out = torch.zeros((self.B, N, Hq, self.ctx.d), dtype=q.dtype, device=dev)
+        self._own(out, "out", self.B * N * Hq * self.ctx.d, q.dtype)
+        self._own(lse, "lse", self.B * N * Hq, torch.float32)
+        if workspace is None:
+            workspace = self.tree_workspace(N, Hq, slopes is not None, num_splits)
+        self._own(workspace, "workspace", workspace.numel(), torch.uint8)
+        _check(lib().skv_tree_attention(
+            self.ctx.handle, _ptr(q), _Q_TYPES[q.dtype], self.B, Hq, self.Hkv, C.byref(t),
+            C.byref(sc), _ptr(self.page_indptr),
+            _ptr(self.page_tier_indptr) if self.split_by_bytes else None, _ptr(self.page_ids),
+            self.page_cap, C.byref(self._pools_c), _ptr(out), _ptr(lse), _ptr(self.err),
+            _ptr(workspace), workspace.numel(), num_splits, self._own_stream(stream)))
+        return out, lse
+
+    def set_free_lists(self, free_lists, cursor=None):
+        """Give a store that was not filled by allocate() its free lists (int32
+        slot numbers per tier, on the device) and their cursors (int32 [3]:
+        the first unused entry of each; None: after the store's own pages)."""
+        dev = self.pools[0].device
+        for t in range(3):
+            _expect(free_lists[t], f"free_lists[{t}]", free_lists[t].numel(), 4, torch.int32)
+        self._free = [f.to(dev) for f in free_lists]
+        fl = SkvFreeLists()
+        for t in range(3):
+            fl.ids[t] = self._free[t].data_ptr() if self._free[t].numel() else None
+            fl.len[t] = self._free[t].numel()
+        self._free_c = fl
+        if cursor is not None:
+            self._own(cursor, "cursor", 3, torch.int32)
+            cursor = cursor.clone()
+        self._cursor = cursor
+
+    def spare(self) -> "PagedCache":
+        """An empty store over the same pools and free lists: the `into` of
+        evict()."""
+        s = PagedCache.__new__(PagedCache)
+        s.__dict__.update({k: x for k, x in self.__dict__.items()
+                           if k not in ("_ws_append", "_ws_retier", "_ws_evict", "released",
+                                        "n_released")})
+        for name in ("tier", "row_of", "page_indptr", "page_tier_indptr", "page_ids", "err"):
+            setattr(s, name, torch.zeros_like(getattr(self, name)))
+        s.tier.fill_(TIER_DROP)
+        s.row_of.fill_(-1)
+        s._cursor = torch.zeros(3, dtype=torch.int32, device=self.pools[0].device)
+        return s
+
+    def evict(self, score: torch.Tensor, seq_lens: torch.Tensor, keep: torch.Tensor,
+              sink: int = 0, recent: int = 0, protect: Optional[torch.Tensor] = None,
+              into: Optional["PagedCache"] = None, stream=None) -> "PagedCache":
+        """The store without the tokens of least score (skv_evict): per
+        (sequence, kv head) keep[b] tokens stay, among them the first `sink`
+        positions, the last `recent` and the protected ones.  score fp32
+        [B][Hkv][Tmax] (the utility that decode_utility accumulates), keep
+        int32 [B].  The result is `into` (made by spare(); a new one when
+        None), a store over the same pools whose pages take free slots; this
+        store stays as it is, and its pages may be reused once nothing reads
+        it.  Device errors are in the result's error word."""
+        n = self.B * self.Hkv * self.Tmax
+        self._own(score, "score", n, torch.float32)
+        self._own(seq_lens, "seq_lens", self.B, torch.int32)
+        self._own(keep, "keep", self.B, torch.int32)
+        self._own(protect, "protect", n, torch.uint8)
+        if into is None:
+            into = self.spare()
+        if into is self or into.tier is self.tier:
+            raise SkvError(SKV_ERR_ARG, "evict: into must be another store (see spare())")
+        if into.pools is not self.pools or into.tier.shape != self.tier.shape:
+            raise SkvError(SKV_ERR_ARG, "evict: into must be a spare() of this store")
+        if getattr(self, "_free_c", None) is None:
+            raise SkvError(SKV_ERR_ARG, "evict: the store has no free lists (set_free_lists)")
+        into._free, into._free_c = self._free, self._free_c
+        cursor = self.free_cursor()
+        if getattr(self, "_ws_evict", None) is None:
+            size = C.c_size_t()
+            _check(lib().skv_evict_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
+                                                  C.byref(size)))
+            self._ws_evict = torch.empty(max(size.value, 1), dtype=torch.uint8,
+                                         device=self.device)
+        _check(lib().skv_evict(
+            self.ctx.handle, self.B, self.Hkv, self.Tmax, _ptr(seq_lens), _ptr(score),
+            _ptr(protect), _ptr(keep), int(sink), int(recent), _ptr(self.tier),
+            _ptr(self.row_of), _ptr(self.page_indptr), _ptr(self.page_ids), self.page_cap,
+            C.byref(self._free_c), _ptr(cursor), C.byref(self._pools_c), _ptr(into.tier),
+            _ptr(into.row_of), _ptr(into.page_indptr), _ptr(into.page_tier_indptr),
+            _ptr(into.page_ids), into.page_cap, _ptr(into._cursor), _ptr(into.err),
+            _ptr(self._ws_evict), self._ws_evict.numel(), self._own_stream(stream)))
+        return into
+
     def check(self, stream=None):
         self.ctx.check(self.err, stream)
 
@@ -557,6 +764,24 @@ class DenseCache:
 
     def check(self, stream=None):
         self.ctx.check(self.err, stream)
+
+
+def tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """int64 [B][N] masks of trees given by parents int [B][N] (the index of
+    an earlier token, -1: a child of the store's last token): token i sees
+    itself and its ancestors."""
+    B, N = parents.shape
+    if N > 64:
+        raise SkvError(SKV_ERR_ARG, "tree_mask: at most 64 tokens")
+    if bool((parents >= torch.arange(N, device=parents.device)).any()) or \
+            bool((parents < -1).any()):
+        raise SkvError(SKV_ERR_ARG, "tree_mask: a parent comes before its child")
+    m = torch.zeros((B, N), dtype=torch.int64, device=parents.device)
+    for i in range(N):
+        par = parents[:, i:i + 1].long()
+        up = torch.where(par >= 0, m.gather(1, par.clamp(min=0)), torch.zeros_like(par))
+        m[:, i] = up[:, 0] | (-(1 << 63) if i == 63 else 1 << i)
+    return m
 
 
 def workload_to_device(w, device="cuda"):
