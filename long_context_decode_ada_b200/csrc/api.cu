@@ -1029,7 +1029,8 @@ int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, i
   if (!ctx || !bytes) return fail(SKV_ERR_ARG, "skv_tree_workspace_size: null argument");
   if (!tree_sizes_ok(B, N, Hq, Hkv, page_cap) || num_splits < 0)
     return fail(SKV_ERR_ARG, "skv_tree_workspace_size: bad sizes");
-  *bytes = positions ? (size_t)page_cap * ctx->P * 4 : 0;
+  *bytes = skv::tree_workspace_bytes(page_cap, ctx->P, positions, decode_splits(ctx, num_splits), N,
+                                     Hq / Hkv, nullptr, nullptr);
   return ok();
 }
 
@@ -1097,8 +1098,9 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
     p.row_of = score->row_of;
     p.seq_lens = score->seq_lens;
     p.Tmax = score->Tmax;
-    p.row_pos = static_cast<int32_t*>(workspace);
   }
+  p.S = decode_splits(ctx, num_splits);
+  skv::tree_workspace_bytes(page_cap, ctx->P, bias, p.S, p.N, Hq / Hkv, &p, workspace);
   p.indptr = page_indptr;
   p.tier_indptr = page_tier_indptr;
   p.ids = page_ids;

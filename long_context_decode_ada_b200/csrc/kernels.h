@@ -288,7 +288,14 @@ struct TreeParams {
   int t1_scheme;
   float rho[4];               // decoded 2-bit shares
   float cos6[64], sin6[64], cos4[16], sin4[16], cos5[32], sin5[32];
+  int S;                      // runs (CTAs)
+  int2* join;                 // workspace: per run the unit it starts and shares (-1: none), its last run
+  float* part;                // workspace: partial O [2S][N * G][128]
+  float2* part_ml;            // workspace: their (m, l), log2 domain
 };
+// Bytes of workspace; with p, its pointers into ws are set.
+size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int N, int G,
+                            TreeParams* p, void* ws);
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
 
 // Eviction by score (evict.cu).

@@ -1,9 +1,47 @@
 // tree.cu -- attention of the drafted tokens of a tree over the paged store:
-// every row (drafted token i, query head) sees the store's resident tokens
-// and the drafted tokens its mask names, with scores optionally capped by a
-// tanh or biased by distance (the same keys and values as the decode: logits
-// from the radius and angle codes, int8 or fp16 values).
+// every row r = (drafted token i, query head g of a kv head) sees the store's
+// resident tokens and the drafted tokens its mask names, with scores
+// optionally capped by a tanh or biased by distance.
+//
+//   S = Q K^T / sqrt d,  O = sum_t 2^(S - m) v_t,  l = sum_t 2^(S - m)
+//
+// Work split: the page list is cut into runs of about equal cost, one per
+// CTA; a run is a list of segments (a unit = (sequence, kv head), or a part
+// of one), a segment a list of tiles of 64 tokens (64 / P pages), the unit's
+// drafted tokens being one more tile behind its pages.  A unit that lies in
+// one run is finished there; the parts of a unit that several runs share go
+// to the workspace as (m, l, O) and a second grid joins them.
+//
+// Roles of a CTA (one per SM):
+//   planner (1 warp)   turns the page list into tile descriptors (a ring of 32
+//                      in shared memory), checks ids and headers, and asks for
+//                      the pages' bytes in L2 (bulk prefetch)
+//   decode (16 warps)  two teams of 8 take the tiles in turn, a warp 8 rows:
+//                      codes to fp16 keys by gathers from a replicated table
+//                      (one conflict-free wavefront a gather), int8 values to
+//                      fp16, both written as swizzled operand tiles (32 KB a
+//                      tile, three tiles in flight).  The loads of a warp's
+//                      next rows are issued as soon as the registers of the
+//                      present ones are free
+//   mma (1 thread)     S = Q K^T and O += P V by tcgen05.mma (fp16, fp32
+//                      accumulators); Q and P are read from tensor memory, so
+//                      that shared memory feeds K and V only
+//   softmax (8 warps)  two groups of 4, one per stream: scores from tensor
+//                      memory, running maximum and sum, weights back as fp16
+//
+// The two streams have accumulators of their own.  With at most 128 rows they
+// take alternate tiles, and with at most 64 (32) rows the rows are entered 2
+// (4) times, each copy handling its part of a tile's columns: every lane of
+// tensor memory then has work, and the copies' sums meet at the segment's
+// end.  With more than 128 rows stream b has the rows 128 b .. 128 b + 127 of
+// every tile.  The running maximum is raised (and O rescaled) only when a
+// score passes it by more than 2^8, so weights stay within fp16.
+//
+// Tensor memory (512 columns): Q 0-63 (and 64-127 for the second block), P of
+// the streams at 64 and 96 (over S with two blocks), S at 128 and 192, O at
+// 256 and 384.
 #include <algorithm>
+#include <cstddef>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -12,241 +50,1403 @@ namespace skv {
 
 namespace {
 
-constexpr int kTreeThreads = 128;
-constexpr int kTreeWarps = kTreeThreads / 32;
+constexpr int kTile = 64;            // tokens of a tile
+constexpr int kStages = 3;           // tiles of keys and values in flight
+constexpr int kRing = 32;            // tile descriptors
+constexpr int kBatch = 8;            // tiles the planner publishes at once
+constexpr int kTeamWarps = 8;        // decode warps of a team (8 rows each)
+constexpr int kSoftWarps = 8;
+constexpr int kDecodeWarps = 2 * kTeamWarps;
+constexpr int kPlanner = kSoftWarps + kDecodeWarps;
+constexpr int kMma = kPlanner + 1;
+constexpr int kThreads = (kSoftWarps + kDecodeWarps + 4) * 32;
+// registers a thread: softmax, decode, planner / mma; their sum over the
+// threads is what the block is launched with (896 x 72)
+constexpr int kRegsSoft = 104, kRegsDecode = 64, kRegsHelp = 40;
+static_assert(256 * kRegsSoft + 512 * kRegsDecode + 128 * kRegsHelp <= kThreads * 72, "registers");
+constexpr float kRaise = 8.0f;       // log2 units a score may pass the running maximum
+constexpr int kBufRow = 132;         // floats of a row of the output buffer
 
-// Positions of the store's rows: row_pos[page * P + row] = t, by the row map.
-__global__ void __launch_bounds__(256) tree_positions_kernel(const __grid_constant__ TreeParams p) {
-  const long long u = blockIdx.y;
-  const long long T = min((long long)p.seq_lens[u / p.Hkv], p.Tmax);
-  const long long a = p.indptr[u], rows = ((long long)p.indptr[u + 1] - a) * p.P;
-  for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < T;
-       t += (long long)gridDim.x * blockDim.x) {
-    const long long r = p.row_of[u * p.Tmax + t];
-    if (r < 0) continue;
-    if (a < 0 || r >= rows || a * p.P + r >= p.page_cap * p.P)
-      report(p.err, SKV_ERR_CORRUPT);
-    else
-      p.row_pos[a * p.P + r] = (int32_t)t;
-  }
-}
+enum : uint32_t { kFirst = 1, kLast = 2, kDraft = 4, kEnd = 8 };
 
-__device__ __forceinline__ float load16(const void* base, long long i, int bf16) {
-  const uint16_t x = static_cast<const uint16_t*>(base)[i];
-  return bf16 ? __bfloat162float(__ushort_as_bfloat16(x)) : __half2float(__ushort_as_half(x));
-}
+// columns of tensor memory
+constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 256;
 
-// The four key components 4 lane .. 4 lane + 3 of row `row` of a page.
-__device__ __forceinline__ void key4(const TreeParams& p, const uint8_t* page, int tier, int row,
-                                     int lane, float (&k)[4]) {
-  if (tier == SKV_TIER_T0) {
-    const uint2 w = *reinterpret_cast<const uint2*>(
-        page + kHdrBytes + row * 256 + (((lane >> 1) ^ (4 * (row & 1))) * 16) + (lane & 1) * 8);
-    const __half2 a = *reinterpret_cast<const __half2*>(&w.x);
-    const __half2 b = *reinterpret_cast<const __half2*>(&w.y);
-    k[0] = __low2float(a);
-    k[1] = __high2float(a);
-    k[2] = __low2float(b);
-    k[3] = __high2float(b);
-    return;
-  }
-  const uint8_t* rs = page + kHdrBytes;
-  const float r = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(rs + 2 * row)));
-  const int cb = tier == SKV_TIER_T1 ? 64 : 48;
-  const uint8_t* c = rs + 2 * p.P + cb * row;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int pr = 2 * lane + e;
-    const int g = (pr & 15) >> 2, j = 4 * (pr >> 4) + (pr & 3);
-    float cs, sn, w;
-    if (tier == SKV_TIER_T1) {
-      const uint32_t x = c[16 * g + j];
-      if (p.t1_scheme) {
-        cs = p.cos5[x >> 3];
-        sn = p.sin5[x >> 3];
-        w = (float)((x & 7) + 1) / 32.0f;
-      } else {
-        cs = p.cos6[x >> 2];
-        sn = p.sin6[x >> 2];
-        w = p.rho[x & 3];
-      }
-    } else {
-      const uint32_t a = (c[8 * g + (j >> 1)] >> (4 * (j & 1))) & 15u;
-      const uint32_t s = (c[32 + 4 * g + (j >> 2)] >> (2 * (j & 3))) & 3u;
-      cs = p.cos4[a];
-      sn = p.sin4[a];
-      w = p.rho[s];
-    }
-    k[2 * e] = r * w * cs;
-    k[2 * e + 1] = r * w * sn;
-  }
-}
-
-__device__ __forceinline__ void value4(const TreeParams& p, const uint8_t* page, int tier, int row,
-                                       int lane, float (&v)[4]) {
-  if (tier == SKV_TIER_T0) {
-    const uint8_t* vs = page + kHdrBytes + 256 * p.P;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = __half2float(__ushort_as_half(
-          *reinterpret_cast<const uint16_t*>(vs + v_frag_offset(row, 4 * lane + e, 2))));
-    return;
-  }
-  const int cb = tier == SKV_TIER_T1 ? 64 : 48;
-  const uint8_t* ss = page + kHdrBytes + (2 + cb) * p.P;
-  const float s = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(ss + 2 * row)));
-  const int8_t* vs = reinterpret_cast<const int8_t*>(ss + 2 * p.P);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = s * (float)vs[v_frag_offset(row, 4 * lane + e, 1)];
-}
-
-template <int G>
-struct TreeState {
-  float m[G], l[G], o[G][4];
+struct Tile {
+  unsigned long long page[4];   // address, 0: none
+  unsigned long long valid;     // bit c: column c holds a token
+  int unit, n;                  // (sequence, kv head) and its drafted tokens
+  uint32_t flags;
+  int first;                    // index of the first page in the page list
+  int slot;                     // partial slot, -1: the unit lies in this run
+  uint8_t tier[4];              // 3: no page
+  uint8_t rows[4];
 };
 
-// One key / value into the running softmax of the G heads (log2 domain).
-template <int G>
-__device__ __forceinline__ void tree_step(const TreeParams& p, TreeState<G>& st,
-                                          const float (&q)[G][4], const float (&slope)[G],
-                                          const float (&k)[4], const float (&v)[4], float dist) {
+struct __align__(16) Fixed {
+  unsigned long long full[kStages], empty[kStages];
+  unsigned long long sfull[2], pfull[2], odone[2];
+  unsigned long long qfull, sync, fin;
+  unsigned long long dfull[kRing / kBatch], rfree[kRing / kBatch];
+  unsigned long long scan[kThreads / 32];
+  unsigned long long ctot, cstart;
+  int ustart;
+  int abort;
+  uint32_t tmem;
+  int bad[kRing];               // a drafted value of the tile is outside fp16
+  __align__(16) Tile ring[kRing];
+  __align__(16) float pos[kStages][kTile];   // positions (from the unit's first q_pos)
+  __align__(16) float cs[kStages][kTile];    // drafted keys: what a score is scaled by
+  float m[2][128], l[2][128];
+};
+
+constexpr uint32_t kTbl1 = 256 * 128, kTbl2 = 64 * 128;   // entries of 32 copies of 4 bytes
+constexpr uint32_t kStageBytes = 2 * kTile * 256;         // keys, values
+constexpr uint32_t kBufBytes = 128 * kBufRow * 4;
+constexpr uint32_t kAtTbl2 = kStages * kStageBytes;       // 8 KB aligned
+constexpr uint32_t kAtTbl1 = kAtTbl2 + kTbl2;
+constexpr uint32_t kAtBuf = kAtTbl1 + kTbl1;
+constexpr uint32_t kAtFixed = kAtBuf + kBufBytes;
+// the base is rounded up to 8 KB (the T2 table's address bits are disjoint
+// from its index bits)
+constexpr uint32_t kSmemBytes = kAtFixed + sizeof(Fixed) + 8192;
+static_assert(kAtTbl2 % 8192 == 0 && kAtFixed % 16 == 0, "layout");
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+// ------------------------------------------------------------ tensor memory
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tc_ld16(uint32_t a, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// D (128 lanes x N fp32) (+)= A (tensor memory, 128 x 16 fp16) B (shared, 16 x N)
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, unsigned long long b, uint32_t idesc,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+
+// fp16 A and B, fp32 D, M = 128; B's values contiguous along k, or along n
+constexpr uint32_t kIdescS = (1u << 4) | ((kTile / 8) << 17) | (8u << 24);
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((kHeadDim / 8) << 17) | (8u << 24);
+
+// Operand tiles in shared memory: rows of 128 bytes, their 16-byte chunks
+// permuted by the row's low three bits (128-byte swizzle), groups of 8 rows
+// 1024 bytes apart; the second 64 dims follow 8 KB behind.
+constexpr unsigned long long kDescBase =
+    ((unsigned long long)(1024 / 16) << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ unsigned long long key_operand(uint32_t at) {
+  return kDescBase | (1ull << 16) | (unsigned long long)((at & 0x3FFFFu) >> 4);
+}
+__device__ __forceinline__ unsigned long long value_operand(uint32_t at) {
+  return kDescBase | ((unsigned long long)(8192 / 16) << 16) |
+         (unsigned long long)((at & 0x3FFFFu) >> 4);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 ldg128(const uint8_t* a) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 h =
+      __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+__device__ __forceinline__ float from16(uint16_t x, int bf16) {
+  return bf16 ? __bfloat162float(__ushort_as_bfloat16(x)) : __half2float(__ushort_as_half(x));
+}
+__device__ __forceinline__ float2 from16x2(uint32_t x, int bf16) {
+  return make_float2(from16((uint16_t)x, bf16), from16((uint16_t)(x >> 16), bf16));
+}
+// |x| of both halves as one comparable word: the larger bit pattern
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t x) {
+  return max(m, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
+}
+// e with 2^e |x| in [2^14, 2^15) for the largest |x| (bit pattern m)
+__device__ __forceinline__ int scale_exp(uint32_t m, int bf16) {
+  if (m == 0) return 0;
+  const uint32_t b = __float_as_uint(from16((uint16_t)m, bf16));
+  const int e = 141 - (int)(b >> 23);
+  return b >= 0x7F800000u ? 0 : min(100, e);
+}
+
+// A bounded wait of a whole warp: false for all lanes when one gave up.
+__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
+                                          int32_t* err) {
+  bool done = mbar_wait_bounded(smem_u32(&bar), parity, &f.abort);
+  done = __all_sync(0xFFFFFFFFu, done);
+  if (!done && (threadIdx.x & 31) == 0 && !*(volatile int*)&f.abort) {
+    *(volatile int*)&f.abort = 1;
+    report(err, SKV_ERR_TIMEOUT);
+  }
+  return done;
+}
+__device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+}
+
+// ------------------------------------------------------------------ the split
+// Pages of a unit by tier and their costs.  A dense page's bytes take 2.6
+// times a coded one's, but its conversion less: it counts twice.  More than
+// 128 rows cost half as much again (decoded once, multiplied twice).
+struct Unit {
+  long long first;     // index of the first page
+  int np, n;           // pages, drafted tokens
+  int nt[3];
+  int w[3];
+  unsigned long long pages, last, cost;  // cost of the pages, start of the last item, all
+};
+
+__device__ __forceinline__ Unit unit_of(const TreeParams& p, int u) {
+  Unit x;
+  const long long a = max(0, p.indptr[u]), z = min((long long)p.indptr[u + 1], p.page_cap);
+  const int b = u / p.Hkv;
+  x.n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
+  x.first = a;
+  x.np = (int)max(0ll, z - a);
+  int n0 = 0, n1 = x.np;
+  if (p.tier_indptr) {
+    const int t0 = p.tier_indptr[3 * u], t1 = p.tier_indptr[3 * u + 1],
+              t2 = p.tier_indptr[3 * u + 2];
+    n0 = min(max(t1 - t0, 0), x.np);
+    n1 = min(max(t2 - t1, 0), x.np - n0);
+  }
+  x.nt[0] = n0;
+  x.nt[1] = n1;
+  x.nt[2] = x.np - n0 - n1;
+  const int f = x.n * (p.Hq / p.Hkv) > 128 ? 3 : 2;
+  x.w[0] = 2 * f;
+  x.w[1] = x.w[2] = f;
+  x.pages = (unsigned long long)x.w[0] * x.nt[0] + (unsigned long long)f * (x.nt[1] + x.nt[2]);
+  const int ipp = kTile / p.P;
+  if (x.n == 0) {
+    x.pages = x.last = x.cost = 0;
+  } else if (p.K || x.np == 0) {
+    x.last = x.pages;
+    x.cost = x.pages + (unsigned long long)(f * ipp);
+  } else {
+    const int k = (x.np - 1) / ipp * ipp;  // the last tile's first page
+    const int a0 = min(k, n0);
+    x.last = (unsigned long long)x.w[0] * a0 + (unsigned long long)f * (k - a0);
+    x.cost = x.pages;
+  }
+  return x;
+}
+
+// The first tile of the unit that starts at cost y or above.
+__device__ __forceinline__ int tile_at(const Unit& x, long long y, int ipp) {
+  if (y <= 0) return 0;
+  long long g = 0;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    float s = q[g][0] * k[0] + q[g][1] * k[1] + q[g][2] * k[2] + q[g][3] * k[3];
+  for (int t = 0; t < 3; ++t) {
+    const long long c = (long long)x.nt[t] * x.w[t];
+    if (y > c) {
+      y -= c;
+      g += x.nt[t];
+    } else {
+      g += (y + x.w[t] - 1) / x.w[t];
+      y = 0;
+      break;
+    }
+  }
+  if (y > 0) g = x.np;
+  const int tiles = (x.np + ipp - 1) / ipp;
+  return min(tiles, (int)((g + ipp - 1) / ipp));
+}
+
+// Total cost and the unit that holds the start of run c (block-wide).
+__device__ __forceinline__ int find_start(const TreeParams& p, Fixed& f, int c) {
+  const int U = p.B * p.Hkv, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (U + kThreads - 1) / kThreads;
+  const int u0 = min(U, tid * per), u1 = min(U, u0 + per);
+  unsigned long long mine = 0;
+  for (int u = u0; u < u1; ++u) mine += unit_of(p, u).cost;
+  unsigned long long x = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    s *= p.qk_scale;
-    if (p.softcap > 0.0f) s = p.softcap * tanhf(s / p.softcap);
-    s = (s - slope[g] * dist) * 1.4426950408889634f;
-    const float mn = fmaxf(st.m[g], s);
-    const float a = st.m[g] == mn ? 1.0f : exp2f(st.m[g] - mn);
-    const float w = mn == -INFINITY ? 0.0f : exp2f(s - mn);
-    st.l[g] = st.l[g] * a + w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) f.scan[w] = x;
+  if (tid == 0) f.ustart = U;
+  __syncthreads();
+  unsigned long long before = x - mine, tot = 0;
+  for (int k = 0; k < kThreads / 32; ++k) {
+    if (k < w) before += f.scan[k];
+    tot += f.scan[k];
+  }
+  // at least kMinTiles tiles of coded rows a run
+  constexpr unsigned long long kMinTiles = 1;
+  const unsigned long long least = kMinTiles * 2 * (kTile / p.P);
+  const int S = (int)min((unsigned long long)p.S, max(1ull, (tot + least - 1) / least));
+  if (c < S && tot > 0) {
+    const unsigned long long from = ((unsigned long long)c * tot + S - 1) / S;
+    unsigned long long cc = before;
+    for (int u = u0; u < u1; ++u) {
+      const unsigned long long k = unit_of(p, u).cost;
+      if (cc <= from && from < cc + k) {
+        f.ustart = u;
+        f.cstart = cc;
+      }
+      cc += k;
+    }
+  }
+  if (tid == 0) f.ctot = tot;
+  __syncthreads();
+  return S;
+}
+
+// ---------------------------------------------------------------- the planner
+__device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int S, int lane) {
+  const int U = p.B * p.Hkv, ipp = kTile / p.P, sh = __ffs(ipp) - 1;
+  const unsigned long long tot = f.ctot;
+  int u = f.ustart, k = 0, kend = 0, slot = -1, ends = 0;
+  bool open = false, draft = false, fresh = false;
+  unsigned long long cc = f.cstart;
+  const unsigned long long from = ((unsigned long long)c * tot + S - 1) / S,
+                           to = ((unsigned long long)(c + 1) * tot + S - 1) / S;
+  int2 join = make_int2(-1, 0);
+  Unit x = {};
+  for (int batch = 0; ends < 2; ++batch) {
+    if (batch >= 2 &&
+        !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f, p.err))
+      break;
+    const int mine = lane >> sh, pg = lane & (ipp - 1);
+    int t_unit = 0, t_n = 0, t_np = 0, t_slot = -1;
+    long long t_first = 0;
+    uint32_t t_flags = kEnd;
+    for (int e = 0; e < kBatch; ++e) {
+      // the next unit with a part in this run
+      while (!open && u < U && cc < to) {
+        x = unit_of(p, u);
+        if (x.cost > 0 && cc + x.last >= from) {
+          k = tile_at(x, (long long)(from - cc), ipp);
+          kend = tile_at(x, (long long)(to - cc), ipp);
+          draft = p.K != nullptr && cc + x.last < to;
+          const int r0 = (int)(cc * S / tot), r1 = (int)((cc + x.last) * S / tot);
+          slot = r0 == r1 ? -1 : (c == r0 ? 2 * c + 1 : 2 * c);
+          if (c == r0 && r1 > r0) join = make_int2(u, r1);
+          open = fresh = true;
+        } else {
+          cc += x.cost;
+          ++u;
+        }
+      }
+      uint32_t fl = kEnd;
+      int np = 0;
+      long long first = 0;
+      if (open) {
+        fl = fresh ? (uint32_t)kFirst : 0u;
+        fresh = false;
+        if (k < kend) {
+          first = x.first + (long long)k * ipp;
+          np = min(ipp, x.np - k * ipp);
+          ++k;
+        } else if (draft) {
+          fl |= kDraft;
+          draft = false;
+        }
+        // (a part without tiles gets an empty one)
+        if (k >= kend && !draft) fl |= kLast;
+      } else {
+        ++ends;
+      }
+      if (mine == e) {
+        t_unit = u;
+        t_n = x.n;
+        t_np = np;
+        t_first = first;
+        t_flags = fl;
+        t_slot = slot;
+      }
+      if (fl & kLast) {
+        open = false;
+        cc += x.cost;
+        ++u;
+      }
+    }
+    // a lane per page
+    unsigned long long at = 0;
+    int tier = 3, rows = 0;
+    if (mine < kBatch && pg < t_np) {
+      const uint32_t id = p.ids[t_first + pg], sl = id & 0x3FFFFFFFu;
+      const int t = (int)(id >> 30);
+      if (t > 2 || (long long)sl >= p.slots[t]) {
+        report(p.err, SKV_ERR_CORRUPT);
+      } else {
+        const uint8_t* a = p.pool[t] + (long long)sl * p.stride[t];
+        const uint32_t bytes = (uint32_t)(kHdrBytes + p.P * tier_row_bytes(t));
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(bytes) : "memory");
+        const uint32_t h = *reinterpret_cast<const uint32_t*>(a);
+        rows = (int)(h & 0xFFFFu);
+        if ((h >> 16) != ((uint32_t)t | ((uint32_t)kPageMagic << 8)) || rows > p.P) {
+          report(p.err, SKV_ERR_CORRUPT);
+          rows = 0;
+        } else {
+          tier = t;
+          at = reinterpret_cast<unsigned long long>(a);
+        }
+      }
+    }
+    unsigned long long valid =
+        rows == 0 ? 0ull : (rows == 64 ? ~0ull : ((1ull << rows) - 1)) << (pg * p.P);
+    for (int o = 1; o < ipp; o <<= 1) valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, o);
+    if (mine < kBatch) {
+      const int e = (batch & 3) * kBatch + mine;
+      Tile& d = f.ring[e];
+      d.page[pg] = at;
+      d.tier[pg] = (uint8_t)tier;
+      d.rows[pg] = (uint8_t)rows;
+      if (pg == 0) {
+        d.valid = (t_flags & kDraft) ? (t_n >= 64 ? ~0ull : (1ull << t_n) - 1) : valid;
+        d.unit = t_unit;
+        d.n = t_n;
+        d.flags = t_flags;
+        d.first = (int)t_first;
+        d.slot = t_slot;
+        f.bad[e] = 0;
+      }
+    }
+    warp_arrive(f.dfull[batch & 3]);
+  }
+  if (lane == 0) p.join[c] = join;
+}
+
+// ----------------------------------------------------------------- the decode
+// Lane (t, g) = 4 t + g of a warp: row t of its 8, key dims 32 i + 8 g + 0..7.
+struct Rows {
+  uint4 k[4], v[4];
+  uint32_t r, s;     // radius; scales of value rows 2 t4, 2 t4 + 1
+  int tier, rows;    // rows in use of the warp's 8
+};
+
+struct Place {       // of a warp's 8 rows in its page
+  const uint8_t* page;
+  int tier, rows, at;
+};
+
+__device__ __forceinline__ Place place_of(const Tile& d, int P, int w) {
+  Place x;
+  const int k = 8 * w / P;
+  x.at = 8 * w - k * P;
+  x.page = reinterpret_cast<const uint8_t*>(d.page[k]);
+  x.tier = d.tier[k];
+  x.rows = min(max((int)d.rows[k] - x.at, 0), 8);
+  if (x.rows == 0) x.tier = 3;
+  return x;
+}
+
+__device__ __forceinline__ void load_keys(const Place& x, int P, int lane, Rows& o) {
+  const int t = lane >> 2, g = lane & 3;
+  if (x.tier == SKV_TIER_T0) {
+    const uint8_t* a = x.page + kHdrBytes + 256 * (x.at + t);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) st.o[g][e] = st.o[g][e] * a + w * v[e];
-    st.m[g] = mn;
+    for (int i = 0; i < 4; ++i) o.k[i] = ldg128(a + 16 * ((4 * i + g) ^ (4 * (t & 1))));
+  } else if (x.tier < 3) {
+    const uint8_t* a = x.page + kHdrBytes;
+    o.r = *reinterpret_cast<const uint16_t*>(a + 2 * (x.at + t));
+    a += 2 * P;
+    if (x.tier == SKV_TIER_T1) {
+      o.k[0] = ldg128(a + 64 * (x.at + t) + 16 * g);
+    } else {
+      a += 48 * (x.at + t);
+      const uint2 n = *reinterpret_cast<const uint2*>(a + 8 * g);
+      o.k[0].x = n.x;
+      o.k[0].y = n.y;
+      o.k[0].z = *reinterpret_cast<const uint32_t*>(a + 32 + 4 * g);
+    }
   }
 }
 
-// A block per (unit, drafted token): its warps share the rows of each page,
-// warp 0 takes the drafted tokens, and the four states meet at the end.
-template <int G>
-__global__ void __launch_bounds__(kTreeThreads)
-    tree_kernel(const __grid_constant__ TreeParams p) {
-  __shared__ float sm[kTreeWarps][G][2];
-  __shared__ float so[kTreeWarps][G][kHeadDim];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long u = blockIdx.x / p.N;
-  const int i = (int)(blockIdx.x - u * p.N);
-  const int b = (int)(u / p.Hkv), h = (int)(u - (long long)b * p.Hkv);
-  const int n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
-  if (i >= n) return;
-  const long long tok = (long long)b * p.N + i;
-  float q[G][4], slope[G];
-  TreeState<G> st;
+__device__ __forceinline__ void load_values(const Place& x, int P, int lane, Rows& o) {
+  if (x.tier == SKV_TIER_T0) {
+    const uint8_t* a = x.page + kHdrBytes + 256 * P + 256 * x.at + 16 * lane;
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
+    for (int i = 0; i < 4; ++i) o.v[i] = ldg128(a + 512 * i);
+  } else if (x.tier < 3) {
+    const int cb = x.tier == SKV_TIER_T1 ? 64 : 48;
+    const uint8_t* a = x.page + kHdrBytes + (2 + cb) * P;
+    o.s = *reinterpret_cast<const uint32_t*>(a + 2 * (x.at + 2 * (lane & 3)));
+    a += 2 * P + 128 * x.at + 16 * lane;
+    o.v[0] = ldg128(a);
+    o.v[1] = ldg128(a + 512);
+  }
+}
+
+// address of the entry of code byte k of w, in the lane's column of the table
+__device__ __forceinline__ uint32_t t1_at(uint32_t w, int k, uint32_t tb) {
+  return tb + (__byte_perm(w, 0u, 0x4440u | (uint32_t)k) << 7);
+}
+__device__ __forceinline__ uint32_t t2_at(uint32_t nw, uint32_t cw, int j, uint32_t tb) {
+  const int sn = 4 * (j & 7) - 7, sc = 2 * j - 11;
+  const uint32_t xn = sn >= 0 ? (nw >> sn) : (nw << -sn);
+  const uint32_t xc = sc >= 0 ? (cw >> sc) : (cw << -sc);
+  return (xn & 0x780u) | (xc & 0x1800u) | tb;
+}
+
+// keys of 8 rows -> fp16 rows T0 .. T0 + 7 of the tile at kb
+__device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, int lane,
+                                           uint32_t tb1, uint32_t tb2) {
+  const int t = lane >> 2, g = lane & 3, odd = t & 1;
+  // odd rows go through their chunks in the order 1 0 3 2, which spreads a
+  // quarter warp's stores over all banks
+  const uint32_t row = kb + (uint32_t)(T0 + t) * 128;
+  const uint32_t at[2] = {row + (((4 * odd + g) ^ t) << 4), row + (((4 * (odd ^ 1) + g) ^ t) << 4)};
+  if (o.tier == SKV_TIER_T0) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      q[g][e] = load16(p.q, tok * p.q_stride + (long long)(h * G + g) * kHeadDim + 4 * lane + e,
-                       p.q_bf16);
-      st.o[g][e] = 0.0f;
+      uint4 x;
+      x.x = odd ? o.k[e ^ 1].x : o.k[e].x;
+      x.y = odd ? o.k[e ^ 1].y : o.k[e].y;
+      x.z = odd ? o.k[e ^ 1].z : o.k[e].z;
+      x.w = odd ? o.k[e ^ 1].w : o.k[e].w;
+      sts128(at[e & 1] + (e >> 1) * 8192, x);
     }
-    slope[g] = p.slopes ? p.slopes[h * G + g] : 0.0f;
-    st.m[g] = -INFINITY;
-    st.l[g] = 0.0f;
+  } else if (o.tier == SKV_TIER_T1) {
+    const uint32_t r = o.r | (o.r << 16);
+    const uint32_t w[4] = {odd ? o.k[0].y : o.k[0].x, odd ? o.k[0].x : o.k[0].y,
+                           odd ? o.k[0].w : o.k[0].z, odd ? o.k[0].z : o.k[0].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint4 x;
+      x.x = hmul2(lds32(t1_at(w[e], 0, tb1)), r);
+      x.y = hmul2(lds32(t1_at(w[e], 1, tb1)), r);
+      x.z = hmul2(lds32(t1_at(w[e], 2, tb1)), r);
+      x.w = hmul2(lds32(t1_at(w[e], 3, tb1)), r);
+      sts128(at[e & 1] + (e >> 1) * 8192, x);
+    }
+  } else if (o.tier == SKV_TIER_T2) {
+    const uint32_t r = o.r | (o.r << 16);
+    // pairs 4 i .. 4 i + 3: nibbles and crumbs 4 i + b; odd rows swap halves
+    const int sw = 16 * odd;
+    const uint32_t n[2] = {__funnelshift_r(o.k[0].x, o.k[0].x, sw),
+                           __funnelshift_r(o.k[0].y, o.k[0].y, sw)};
+    const uint32_t cw = odd ? ((o.k[0].z >> 8) & 0x00FF00FFu) | ((o.k[0].z << 8) & 0xFF00FF00u)
+                            : o.k[0].z;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint4 x;
+      x.x = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e, tb2)), r);
+      x.y = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 1, tb2)), r);
+      x.z = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 2, tb2)), r);
+      x.w = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 3, tb2)), r);
+      sts128(at[e & 1] + (e >> 1) * 8192, x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sts128(at[e & 1] + (e >> 1) * 8192, make_uint4(0, 0, 0, 0));
   }
-  const int qpos = p.slopes ? p.q_pos[tok] : 0;
-  const long long g0 = max(0, p.indptr[u]), g1 = min((long long)p.indptr[u + 1], p.page_cap);
-  for (long long pg = g0; pg < g1; ++pg) {
-    const uint32_t id = p.ids[pg];
-    const int tier = (int)(id >> 30);
-    const long long slot = id & 0x3FFFFFFFu;
-    if (tier > 2 || slot >= p.slots[tier]) {
-      if (threadIdx.x == 0) report(p.err, SKV_ERR_CORRUPT);
-      continue;
+}
+
+// Values of 8 rows -> fp16.  The tile's columns are a permutation of the
+// dims that a lane of the pages' fragment order holds together: column
+// 64 h + 8 g + 2 m + hi is dim 64 h + 16 m + 8 hi + g.
+__device__ __forceinline__ int column_of(int d) {
+  return (d & 64) + 8 * (d & 7) + 2 * ((d >> 4) & 3) + ((d >> 3) & 1);
+}
+
+__device__ __forceinline__ void store_values(const Rows& o, uint32_t vb, int T0, int lane) {
+  const int g = lane >> 2, a = 2 * (lane & 3), b = a + 1;
+  const uint32_t ra = vb + (uint32_t)(T0 + a) * 128 + ((g ^ a) << 4);
+  const uint32_t rb = vb + (uint32_t)(T0 + b) * 128 + ((g ^ b) << 4);
+  if (o.tier == SKV_TIER_T0) {
+    const bool ua = a < o.rows, ub = b < o.rows;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = o.v[2 * h], y = o.v[2 * h + 1];
+      uint4 p = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                           __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+      uint4 q = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                           __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
+      if (!ua) p = make_uint4(0, 0, 0, 0);
+      if (!ub) q = make_uint4(0, 0, 0, 0);
+      sts128(ra + h * 8192, p);
+      sts128(rb + h * 8192, q);
     }
-    const uint8_t* page = p.pool[tier] + slot * p.stride[tier];
-    const uint32_t hdr = *reinterpret_cast<const uint32_t*>(page);
-    const int rows = (int)(hdr & 0xFFFFu);
-    if ((hdr >> 16) != ((uint32_t)tier | ((uint32_t)kPageMagic << 8)) || rows > p.P) {
-      if (threadIdx.x == 0) report(p.err, SKV_ERR_CORRUPT);
-      continue;
+  } else if (o.tier < 3) {
+    // v + 128 as the low byte of 1024 + x in fp16, less 1152 (exact), times
+    // the scale (rounded once); rows that are not there get the scale 0
+    const uint32_t sa = a < o.rows ? __byte_perm(o.s, 0u, 0x1010) : 0u;
+    const uint32_t sb = b < o.rows ? __byte_perm(o.s, 0u, 0x3232) : 0u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w[4] = {o.v[h].x, o.v[h].y, o.v[h].z, o.v[h].w};
+      uint32_t p[4], q[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t u = w[m] ^ 0x80808080u;
+        const uint32_t x = __byte_perm(u, 0x64646464u, 0x4240), y = __byte_perm(u, 0x64646464u, 0x4341);
+        const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+        const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+        p[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hx), sa);
+        q[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hy), sb);
+      }
+      sts128(ra + h * 8192, make_uint4(p[0], p[1], p[2], p[3]));
+      sts128(rb + h * 8192, make_uint4(q[0], q[1], q[2], q[3]));
     }
-    for (int r = w; r < rows; r += kTreeWarps) {
-      float k[4], v[4];
-      key4(p, page, tier, r, lane, k);
-      value4(p, page, tier, r, lane, v);
-      const float dist = p.slopes ? (float)(qpos - p.row_pos[pg * p.P + r]) : 0.0f;
-      tree_step<G>(p, st, q, slope, k, v, dist);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      sts128(ra + h * 8192, make_uint4(0, 0, 0, 0));
+      sts128(rb + h * 8192, make_uint4(0, 0, 0, 0));
     }
   }
-  if (p.K && w == 0) {
+}
+
+// Drafted keys and values of 8 tokens.  A key is scaled by a power of two to
+// fp16's range (taken off its scores again), so that bf16 keys enter exactly;
+// a value outside fp16's range enters as 0 and is added at the segment's end.
+__device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, uint32_t kb,
+                                         uint32_t vb, float* cs, int* bad, int T0, int lane) {
+  const int t = lane >> 2, g = lane & 3, j = T0 + t;
+  const int b = d.unit / p.Hkv, h = d.unit - b * p.Hkv;
+  const bool live = j < d.n;
+  const long long at = ((long long)b * p.N + j) * p.kv_stride + (long long)h * kHeadDim;
+  uint4 x[4];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (live)
+      x[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.K) + at + 32 * i + 8 * g);
+    mx = max_bits(max_bits(max_bits(max_bits(mx, x[i].x), x[i].y), x[i].z), x[i].w);
+  }
+  mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+  mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+  const int e = scale_exp(mx, p.kv_bf16);
+  const float up = pow2i(e);
+  const uint32_t row = kb + (uint32_t)j * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 y = from16x2(w[k], p.kv_bf16);
+      w[k] = pack_f16x2(y.x * up, y.y * up);
+    }
+    sts128(row + (i >> 1) * 8192 + (((4 * (i & 1) + g) ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  if (g == 0) cs[j] = pow2i(-e);
+  bool out = false;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int hf = c >> 1, gg = g + 4 * (c & 1);
+    uint32_t w[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      float y[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        if (live)
+          y[hi] = from16(static_cast<const uint16_t*>(p.V)[at + 64 * hf + 16 * m + 8 * hi + gg],
+                         p.kv_bf16);
+        if (!(fabsf(y[hi]) <= 65504.0f)) {
+          y[hi] = 0.0f;
+          out = true;
+        }
+      }
+      w[m] = pack_f16x2(y[0], y[1]);
+    }
+    sts128(vb + (uint32_t)j * 128 + hf * 8192 + ((gg ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  if (out) *(volatile int*)bad = 1;
+}
+
+template <bool BIAS>
+__device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t base, int wd,
+                                            int lane) {
+  const int w = wd & (kTeamWarps - 1), P = p.P;
+  const uint32_t tb1 = base + kAtTbl1 + 4 * lane, tb2 = base + kAtTbl2 + 4 * lane;
+  Rows o;
+  int t = wd / kTeamWarps;
+  if (!warp_wait(f.dfull[0], 0, f, p.err)) return;
+  uint32_t flags = f.ring[t].flags;
+  o.tier = 3;
+  o.rows = 0;
+  o.r = o.s = 0;
+  if (!(flags & (kEnd | kDraft))) {
+    const Place x = place_of(f.ring[t], P, w);
+    o.tier = x.tier;
+    o.rows = x.rows;
+    load_keys(x, P, lane, o);
+    load_values(x, P, lane, o);
+  }
+  while (!(flags & kEnd)) {
+    const int stage = t % kStages, turn = t / kStages;
+    const uint32_t kb = base + stage * kStageBytes, vb = kb + kTile * 256;
+    const Tile& d = f.ring[t & (kRing - 1)];
+    if (turn > 0 && !warp_wait(f.empty[stage], (turn - 1) & 1, f, p.err)) return;
+    if (BIAS && lane < 8) {
+      const int b = d.unit / p.Hkv;
+      const int q0 = p.q_pos[(long long)b * p.N];
+      int q = q0;
+      if (flags & kDraft) {
+        if (8 * w + lane < d.n) q = p.q_pos[(long long)b * p.N + 8 * w + lane];
+      } else if (lane < o.rows) {
+        const int k = 8 * w / P;
+        q = p.row_pos[((long long)d.first + k) * P + (8 * w - k * P) + lane];
+      }
+      f.pos[stage][8 * w + lane] = (float)(q - q0);
+    }
+    const int t2 = t + 2;
+    const bool turned = (t2 >> 3) != (t >> 3);
+    uint32_t next;
+    if (flags & kDraft) {
+      store_draft(p, d, kb, vb, f.cs[stage], &f.bad[t & (kRing - 1)], 8 * w, lane);
+      if (turned && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
+      const Tile& dn = f.ring[t2 & (kRing - 1)];
+      next = dn.flags;
+      o.tier = 3;
+      if (!(next & (kEnd | kDraft))) {
+        const Place x = place_of(dn, P, w);
+        o.tier = x.tier;
+        o.rows = x.rows;
+        load_keys(x, P, lane, o);
+        load_values(x, P, lane, o);
+      }
+    } else {
+      store_keys(o, kb, 8 * w, lane, tb1, tb2);
+      if (turned && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
+      const Tile& dn = f.ring[t2 & (kRing - 1)];
+      next = dn.flags;
+      Place x;
+      x.page = nullptr;
+      x.tier = 3;
+      x.rows = 0;
+      x.at = 0;
+      if (!(next & (kEnd | kDraft))) x = place_of(dn, P, w);
+      load_keys(x, P, lane, o);
+      store_values(o, vb, 8 * w, lane);
+      o.tier = x.tier;
+      o.rows = x.rows;
+      load_values(x, P, lane, o);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    warp_arrive(f.full[stage]);
+    flags = next;
+    t = t2;
+  }
+}
+
+// ------------------------------------------------------------------- the MMAs
+struct Pending {
+  int s, stage, tile;
+  bool first, release;
+};
+
+__device__ __forceinline__ bool one_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
+                                         int32_t* err) {
+  if (mbar_wait_bounded(smem_u32(&bar), parity, &f.abort)) return true;
+  if (!*(volatile int*)&f.abort) {
+    *(volatile int*)&f.abort = 1;
+    report(err, SKV_ERR_TIMEOUT);
+  }
+  return false;
+}
+
+__device__ __forceinline__ void mma_role(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
+  const int G = p.Hq / p.Hkv;
+  uint32_t jobs[2] = {0, 0};  // jobs of the streams so far
+  uint32_t segs = 0;
+  int nb = 1, j = 0;
+  bool first[2] = {true, true}, pending = false;
+  Pending q = {};
+  const auto pv = [&]() {
+    if (!one_wait(f.pfull[q.s], (jobs[q.s] - 1) & 1, f, p.err)) return false;
+    tc_fence_after();
+    const uint32_t vb = base + q.stage * kStageBytes + kTile * 256;
+    const uint32_t a = tm + (nb == 2 ? kColS + 64 * q.s : kColP + 32 * q.s);
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k)
+      tc_mma(tm + kColO + 128 * q.s, a + 8 * k, value_operand(vb + 2048 * k), kIdescO,
+             !(q.first && k == 0));
+    tc_commit(smem_u32(&f.odone[q.s]));
+    if (q.release) {
+      tc_commit(smem_u32(&f.empty[q.stage]));
+      if ((q.tile & (kBatch - 1)) == kBatch - 1)
+        tc_commit(smem_u32(&f.rfree[(q.tile / kBatch) & 3]));
+    }
+    pending = false;
+    return true;
+  };
+  for (int t = 0;; ++t) {
+    if ((t & (kBatch - 1)) == 0 && !one_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
+    const Tile& d = f.ring[t & (kRing - 1)];
+    const uint32_t flags = d.flags;
+    if (flags & kEnd) break;
+    if (flags & kFirst) {
+      if (!one_wait(f.qfull, segs & 1, f, p.err)) return;
+      ++segs;
+      nb = d.n * G > 128 ? 2 : 1;
+      j = 0;
+      first[0] = first[1] = true;
+    }
+    const int stage = t % kStages;
+    if (!one_wait(f.full[stage], (t / kStages) & 1, f, p.err)) return;
+    tc_fence_after();
+    const uint32_t kb = base + stage * kStageBytes;
+    for (int b = 0; b < nb; ++b, ++j) {
+      const int s = j & 1;
+#pragma unroll
+      for (int k = 0; k < kHeadDim / 16; ++k)
+        tc_mma(tm + kColS + 64 * s, tm + kColQ + (nb == 2 ? 64 * s : 0) + 8 * k,
+               key_operand(kb + (k >> 2) * 8192 + (k & 3) * 32), kIdescS, k > 0);
+      tc_commit(smem_u32(&f.sfull[s]));
+      if (pending && !pv()) return;
+      ++jobs[s];
+      q.s = s;
+      q.stage = stage;
+      q.tile = t;
+      q.first = first[s];
+      q.release = b == nb - 1;
+      first[s] = false;
+      pending = true;
+    }
+    if ((flags & kLast) && !pv()) return;
+  }
+}
+
+// ---------------------------------------------------------------- the softmax
+struct Row {           // a lane's row in its stream
+  float c;             // what a product is scaled by (log2 domain, before the cap)
+  float cap, slope, rel;
+  float m, l;
+  uint32_t jobs;       // of this stream so far
+  int mine;            // of this stream in the segment
+};
+
+// Columns c0 .. c0 + NC - 1 of a tile: scores to weights.  S at `sa`, the
+// weights' tensor memory at `pa`; bits: the columns this row sees.
+template <int NC, bool CAP, bool BIAS>
+__device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& r, uint32_t sa,
+                                            uint32_t pa, uint32_t oa, int wg,
+                                            unsigned long long bits, const float* cs,
+                                            const float* pos) {
+  float s[NC];
+#pragma unroll
+  for (int k = 0; k < NC; k += 16) tc_ld16(sa + k, s + k);
+  tc_wait_ld();
+  constexpr unsigned long long kAll = NC == 64 ? ~0ull : (1ull << (NC & 63)) - 1;
+  if (cs) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) s[k] *= cs[k];
+  }
+  if (CAP || BIAS) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      if (CAP) {
+        const float e = ex2f(s[k] * r.c);
+        s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
+      } else {
+        s[k] *= r.c;
+      }
+      if (BIAS) s[k] = fmaf(r.slope, pos[k] - r.rel, s[k]);
+    }
+  }
+  if (bits != kAll) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k)
+      if (!((bits >> k) & 1)) s[k] = -INFINITY;
+  }
+  float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int k = 4; k < NC; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+  float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  if (!(CAP || BIAS)) top *= r.c;
+  if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise)) {
+    // raise the maximum of the rows that need it; their sums follow
+    const float m = top > r.m + kRaise ? top : r.m;
+    const float a = m == r.m ? 1.0f : ex2f(r.m - m);
+    r.l *= a;
+    r.m = m;
+    if (r.mine > 0) {
+      if (!warp_wait(f.odone[wg], (r.jobs - 1) & 1, f, p.err)) return false;
+      tc_fence_after();
+#pragma unroll 1
+      for (int k = 0; k < kHeadDim; k += 16) {
+        float o[16];
+        tc_ld16(oa + k, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= a;
+        tc_st8(oa + k, reinterpret_cast<const uint32_t*>(o));
+        tc_st8(oa + k + 8, reinterpret_cast<const uint32_t*>(o) + 8);
+      }
+    }
+  }
+  const float m = r.m == -INFINITY ? 0.0f : r.m;
+  float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NC; k += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = s[k + 2 * e], y = s[k + 2 * e + 1];
+      const float a = ex2f((CAP || BIAS) ? x - m : fmaf(x, r.c, -m));
+      const float b = ex2f((CAP || BIAS) ? y - m : fmaf(y, r.c, -m));
+      l0 += a;
+      l1 += b;
+      w[e] = pack_f16x2(a, b);
+    }
+    tc_st8(pa + k / 2, w);
+  }
+  r.l += l0 + l1;
+  tc_wait_st();
+  return true;
+}
+
+// One row of the result: v = the lane's four dims (4 lane ..) of O, relative
+// to M, and its sum L.  Drafted values outside fp16's range are added here.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void write_row(const TreeParams& p, const Tile& d, bool bad, int r,
+                                          float M, float L, float (&v)[4], int lane) {
+  const int G = p.Hq / p.Hkv, i = r / G, g = r - i * G;
+  const int b = d.unit / p.Hkv, h = d.unit - b * p.Hkv, hq = h * G + g;
+  const long long tok = (long long)b * p.N + i;
+  if (bad) {
     unsigned long long bits = p.mask ? p.mask[tok] : (i == 63 ? ~0ull : (2ull << i) - 1);
-    if (n < 64) bits &= (1ull << n) - 1;
+    if (d.n < 64) bits &= (1ull << d.n) - 1;
     while (bits) {
       const int j = __ffsll((long long)bits) - 1;
       bits &= bits - 1;
-      const long long at = ((long long)b * p.N + j) * p.kv_stride + (long long)h * kHeadDim;
-      float k[4], v[4];
+      const long long at = ((long long)b * p.N + j) * p.kv_stride + (long long)h * kHeadDim + 4 * lane;
+      float y[4], s = 0.0f;
+      bool out = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        k[e] = load16(p.K, at + 4 * lane + e, p.kv_bf16);
-        v[e] = load16(p.V, at + 4 * lane + e, p.kv_bf16);
+        y[e] = from16(static_cast<const uint16_t*>(p.V)[at + e], p.kv_bf16);
+        if (fabsf(y[e]) <= 65504.0f)
+          y[e] = 0.0f;
+        else
+          out = true;
+        s += from16(static_cast<const uint16_t*>(p.q)[tok * p.q_stride + (long long)hq * kHeadDim +
+                                                      4 * lane + e],
+                    p.q_bf16) *
+             from16(static_cast<const uint16_t*>(p.K)[at + e], p.kv_bf16);
       }
-      const float dist = p.slopes ? (float)(qpos - p.q_pos[(long long)b * p.N + j]) : 0.0f;
-      tree_step<G>(p, st, q, slope, k, v, dist);
+      if (!__any_sync(0xFFFFFFFFu, out)) continue;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      s *= p.qk_scale;
+      if (CAP) s = p.softcap * tanhf(s / p.softcap);
+      if (BIAS)
+        s -= p.slopes[hq] * (float)(p.q_pos[tok] - p.q_pos[(long long)b * p.N + j]);
+      const float w = exp2f(s * 1.4426950408889634f - M);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (y[e] != 0.0f) v[e] += w * y[e];
     }
   }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    if (lane == 0) {
-      sm[w][g][0] = st.m[g];
-      sm[w][g][1] = st.l[g];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) so[w][g][4 * lane + e] = st.o[g][e];
+  if (d.slot >= 0) {
+    const long long at = (long long)d.slot * (p.N * G) + r;
+    *reinterpret_cast<float4*>(p.part + at * kHeadDim + 4 * lane) =
+        make_float4(v[0], v[1], v[2], v[3]);
+    if (lane == 0) p.part_ml[at] = make_float2(M, L);
+    return;
   }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const long long at = (tok * p.Hq + hq) * kHeadDim + 4 * lane;
+  uint2 w;
+  if (p.q_bf16)
+    w = make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+  else
+    w = make_uint2(pack_f16x2(v[0] * inv, v[1] * inv), pack_f16x2(v[2] * inv, v[3] * inv));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+  if (lane == 0 && p.lse)
+    p.lse[tok * p.Hq + hq] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, float* buf, uint32_t tm0,
+                                             int warp, int lane) {
+  const int G = p.Hq / p.Hkv;
+  const int wg = warp >> 2, part = warp & 3, tl = 32 * part + lane;
+  const uint32_t tm = tm0 + ((uint32_t)(32 * part) << 16);
+  const uint32_t oa = tm + kColO + 128 * wg;
+  Row r = {};
+  uint32_t syncs = 0;
+  int nb = 1, rc = 128, j = 0, row = 0, copy = 0, R = 0;
+  bool busy = true;  // the warp has rows
+  unsigned long long see = 0;
+  const auto meet = [&]() {
+    warp_arrive(f.sync);
+    return warp_wait(f.sync, syncs++ & 1, f, p.err);
+  };
+  for (int t = 0;; ++t) {
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
+    const Tile& d = f.ring[t & (kRing - 1)];
+    const uint32_t flags = d.flags;
+    if (flags & kEnd) return;
+    if (flags & kFirst) {
+      R = d.n * G;
+      nb = R > 128 ? 2 : 1;
+      rc = R <= 32 ? 32 : (R <= 64 ? 64 : 128);
+      row = nb == 2 ? 128 * wg + tl : (tl & (rc - 1));
+      copy = nb == 2 ? 0 : tl / rc;
+      const int b = d.unit / p.Hkv, h = d.unit - b * p.Hkv;
+      const int i = row / G, hq = h * G + (row - i * G);
+      const bool live = row < R;
+      busy = __any_sync(0xFFFFFFFFu, live);
+      const long long tok = (long long)b * p.N + i;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                      tok * p.q_stride + (long long)hq * kHeadDim);
+      // the row as fp16 scaled by a power of two (bf16 converts exactly)
+      uint32_t mx = 0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (live) x = q[k];
+        mx = max_bits(max_bits(max_bits(max_bits(mx, x.x), x.y), x.z), x.w);
+      }
+      const int e = scale_exp(mx, p.q_bf16);
+      const float up = pow2i(e);
+      // one block: both streams use it, each group writes half its dims
+      for (int k = 0; k < 16; k += 2) {
+        if (nb == 1 && (k >> 3) != wg) continue;
+        uint32_t w[8];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) x = q[k + y];
+          const uint32_t z[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float2 a = from16x2(z[v], p.q_bf16);
+            w[4 * y + v] = pack_f16x2(a.x * up, a.y * up);
+          }
+        }
+        tc_st8(tm + kColQ + (nb == 2 ? 64 * wg : 0) + 4 * k, w);
+      }
+      if (nb == 1) {
+        // the weights of the other copies' columns stay zero
+        const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) tc_st8(tm + kColP + 32 * wg + k, z);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(f.qfull);
+      const float log2e = 1.4426950408889634f;
+      const float c = p.qk_scale * pow2i(-e);
+      if (CAP) {
+        r.c = c * (2.0f * log2e / p.softcap);   // exp2 of it is e^(2 x / cap)
+        r.cap = p.softcap * log2e;
+      } else {
+        r.c = c * log2e;
+      }
+      if (BIAS) {
+        r.slope = live ? p.slopes[hq] * log2e : 0.0f;
+        const int q0 = p.q_pos[(long long)b * p.N];
+        r.rel = live ? (float)(p.q_pos[tok] - q0) : 0.0f;
+      }
+      r.m = -INFINITY;
+      r.l = 0.0f;
+      r.mine = 0;
+      j = 0;
+      see = 0;
+      if (live && p.K)
+        see = p.mask ? p.mask[tok] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+    }
+    for (int b = 0; b < nb; ++b, ++j) {
+      if ((j & 1) != wg) continue;
+      if (!warp_wait(f.sfull[wg], r.jobs & 1, f, p.err)) return;
+      tc_fence_after();
+      if (busy) {
+        const int stage = t % kStages;
+        unsigned long long bits = d.valid;
+        const float* cs = nullptr;
+        if (flags & kDraft) {
+          bits &= see;
+          cs = f.cs[stage];
+        }
+        const float* pos = f.pos[stage];
+        const uint32_t sa = tm + kColS + 64 * wg;
+        bool ok;
+        if (nb == 2) {
+          ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, sa, oa, wg, bits, cs, pos);
+        } else {
+          const uint32_t pa = tm + kColP + 32 * wg;
+          const int c0 = copy * (kTile * rc / 128);
+          if (cs) cs += c0;
+          pos += c0;
+          if (rc == 128) {
+            ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, pa, oa, wg, bits, cs, pos);
+          } else if (rc == 64) {
+            ok = softmax_job<32, CAP, BIAS>(p, f, r, sa + c0, pa + c0 / 2, oa, wg,
+                                            (bits >> c0) & 0xFFFFFFFFull, cs, pos);
+          } else {
+            ok = softmax_job<16, CAP, BIAS>(p, f, r, sa + c0, pa + c0 / 2, oa, wg,
+                                            (bits >> c0) & 0xFFFFull, cs, pos);
+          }
+        }
+        if (!ok) return;
+      }
+      tc_fence_before();
+      warp_arrive(f.pfull[wg]);
+      ++r.jobs;
+      ++r.mine;
+    }
+    if (!(flags & kLast)) continue;
+    // the segment's end: the streams' and copies' sums meet
+    if (r.mine > 0) {
+      if (!warp_wait(f.odone[wg], (r.jobs - 1) & 1, f, p.err)) return;
+      tc_fence_after();
+    }
+    const bool bad = *(volatile int*)&f.bad[t & (kRing - 1)] != 0;
+    f.m[wg][tl] = r.m;
+    f.l[wg][tl] = r.l;
+    if (!meet()) return;
+    float* const mine = buf + tl * kBufRow;
+    const int c0 = column_of(4 * lane);
+    if (nb == 1) {
+      const int copies = 128 / rc, sub = tl & (rc - 1);
+      float M = -INFINITY;
+      for (int k = 0; k < copies; ++k)
+        M = fmaxf(M, fmaxf(f.m[0][sub + rc * k], f.m[1][sub + rc * k]));
+      const float a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
+      for (int s = 1; s >= 0; --s) {
+        if (wg == s && busy) {
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim; k += 16) {
+            float o[16];
+            if (r.mine > 0) {
+              tc_ld16(oa + k, o);
+              tc_wait_ld();
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (a != 0.0f) x = make_float4(o[e] * a, o[e + 1] * a, o[e + 2] * a, o[e + 3] * a);
+              float4* to = reinterpret_cast<float4*>(mine + k + e);
+              if (s == 0) {
+                const float4 y = *to;
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+              }
+              *to = x;
+            }
+          }
+        }
+        if (s == 1) tc_fence_before();
+        if (!meet()) return;
+      }
+      for (int x = warp; x < R; x += kSoftWarps) {
+        float Mx = -INFINITY, Lx = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < copies; ++k)
+          Mx = fmaxf(Mx, fmaxf(f.m[0][x + rc * k], f.m[1][x + rc * k]));
+        for (int k = 0; k < copies; ++k) {
+          const float* from = buf + (x + rc * k) * kBufRow + c0;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            // (a sum without a maximum: 0, or NaN where every score is NaN)
+            const float m = f.m[s][x + rc * k], l = f.l[s][x + rc * k];
+            if (l != 0.0f) Lx += m == -INFINITY ? l : l * ex2f(m - Mx);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += from[8 * e];
+        }
+        write_row<CAP, BIAS>(p, d, bad, x, Mx, Lx, v, lane);
+      }
+    } else {
+      for (int b = 0; b < 2; ++b) {
+        if (wg == b && busy) {
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim; k += 16) {
+            float o[16];
+            tc_ld16(oa + k, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(mine + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (!meet()) return;
+        for (int x = warp; x < 128 && 128 * b + x < R; x += kSoftWarps) {
+          const float* from = buf + x * kBufRow + c0;
+          float v[4] = {from[0], from[8], from[16], from[24]};
+          const float Mx = f.m[b][x];
+          if (Mx == -INFINITY) v[0] = v[1] = v[2] = v[3] = 0.0f;
+          write_row<CAP, BIAS>(p, d, bad, 128 * b + x, Mx, f.l[b][x], v, lane);
+        }
+        if (!meet()) return;
+      }
+    }
+  }
+}
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  const uint32_t at = smem_u32(raw);
+  const uint32_t base = (at + 8191u) & ~8191u;
+  uint8_t* const mem = raw + (base - at);
+  Fixed& f = *reinterpret_cast<Fixed*>(mem + kAtFixed);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    f.abort = 0;
+    for (int k = 0; k < kStages; ++k) {
+      mbar_init(smem_u32(&f.full[k]), kTeamWarps);
+      mbar_init(smem_u32(&f.empty[k]), 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&f.sfull[k]), 1);
+      mbar_init(smem_u32(&f.pfull[k]), 4);
+      mbar_init(smem_u32(&f.odone[k]), 1);
+    }
+    mbar_init(smem_u32(&f.qfull), kSoftWarps);
+    mbar_init(smem_u32(&f.sync), kSoftWarps);
+    mbar_init(smem_u32(&f.fin), 1);
+    for (int k = 0; k < kRing / kBatch; ++k) {
+      mbar_init(smem_u32(&f.dfull[k]), 1);
+      mbar_init(smem_u32(&f.rfree[k]), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&f.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // the keys of the code words at radius 1 (share times cosine and sine), in
+  // fp16, 32 copies: copy L is read by lane L
+  for (int i = tid; i < 8 * (256 + 64); i += kThreads) {
+    const int e = i >> 3;
+    float cs, sn, w;
+    if (e < 256 && p.t1_scheme) {
+      cs = p.cos5[e >> 3];
+      sn = p.sin5[e >> 3];
+      w = (float)((e & 7) + 1) / 32.0f;
+    } else if (e < 256) {
+      cs = p.cos6[e >> 2];
+      sn = p.sin6[e >> 2];
+      w = p.rho[e & 3];
+    } else {
+      cs = p.cos4[(e - 256) & 15];
+      sn = p.sin4[(e - 256) & 15];
+      w = p.rho[(e - 256) >> 4];
+    }
+    const uint32_t h = pack_f16x2(w * cs, w * sn);
+    uint8_t* const to = mem + (e < 256 ? kAtTbl1 + 16 * i : kAtTbl2 + 16 * (i - 8 * 256));
+    *reinterpret_cast<uint4*>(to) = make_uint4(h, h, h, h);
+  }
+  tc_fence_before();
+  const int S = find_start(p, f, blockIdx.x);   // (block-wide barriers)
+  tc_fence_after();
+  const uint32_t tm = *(volatile uint32_t*)&f.tmem;
+
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(mem + kAtBuf), tm, warp, lane);
+  } else if (warp < kPlanner) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
+    decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
+    if (warp == kPlanner) {
+      planner(p, f, blockIdx.x, S, lane);
+    } else if (warp == kMma) {
+      if (lane == 0) {
+        mma_role(p, f, base, tm);
+        // nothing in flight when tensor memory is given back
+        tc_commit(smem_u32(&f.fin));
+        int none = 0;
+        if (!mbar_wait_bounded(smem_u32(&f.fin), 0, &none)) report(p.err, SKV_ERR_TIMEOUT);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
   __syncthreads();
-  for (int x = threadIdx.x; x < G * kHeadDim; x += kTreeThreads) {
-    const int g = x / kHeadDim, d = x % kHeadDim;
-    float M = -INFINITY, L = 0.0f, o = 0.0f;
-    for (int k = 0; k < kTreeWarps; ++k) M = fmaxf(M, sm[k][g][0]);
-    for (int k = 0; k < kTreeWarps; ++k) {
-      const float a = sm[k][g][0] == M ? 1.0f : exp2f(sm[k][g][0] - M);
-      L += a * sm[k][g][1];
-      o += a * so[k][g][d];
-    }
-    o = L > 0.0f ? o / L : (L == 0.0f ? 0.0f : o);
-    const long long at = (tok * p.Hq + h * G + g) * kHeadDim + d;
-    if (p.q_bf16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o);
-    else
-      static_cast<__half*>(p.out)[at] = __float2half_rn(o);
-    if (d == 0 && p.lse)
-      p.lse[tok * p.Hq + h * G + g] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (warp == kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
   }
+}
+
+// The parts of the units that several runs share: a warp per row.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int2 join = p.join[c];
+  if (join.x < 0) return;
+  const int G = p.Hq / p.Hkv, b = join.x / p.Hkv, h = join.x - b * p.Hkv;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
+  if (r >= n * G) return;
+  const int rows = p.N * G, parts = join.y - c + 1;
+  // part k: slot 2 c + 1 of the first run, 2 (c + k) of the others
+  const auto at = [&](int k) {
+    return (long long)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rows + r;
+  };
+  float M = -INFINITY;
+  for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float L = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float2 ml = p.part_ml[at(k)];
+    const float4 x = *reinterpret_cast<const float4*>(p.part + at(k) * kHeadDim + 4 * lane);
+    const float a = ml.x == -INFINITY ? 0.0f : ex2f(ml.x - M);
+    L += a * ml.y;
+    v.x += a * x.x;
+    v.y += a * x.y;
+    v.z += a * x.z;
+    v.w += a * x.w;
+  }
+  const int i = r / G, hq = h * G + (r - i * G);
+  const long long tok = (long long)b * p.N + i;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  uint2 w;
+  if (p.q_bf16)
+    w = make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  else
+    w = make_uint2(pack_f16x2(v.x * inv, v.y * inv), pack_f16x2(v.z * inv, v.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (tok * p.Hq + hq) * kHeadDim + 4 * lane) = w;
+  if (lane == 0 && p.lse)
+    p.lse[tok * p.Hq + hq] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// Positions of the store's rows: row_pos[page * P + row] = t, by the row map.
+__global__ void __launch_bounds__(256) tree_positions_kernel(const __grid_constant__ TreeParams p) {
+  const long long U = (long long)p.B * p.Hkv;
+  for (long long u = blockIdx.y; u < U; u += gridDim.y) {
+    const long long T = min((long long)p.seq_lens[u / p.Hkv], p.Tmax);
+    const long long a = p.indptr[u], rows = ((long long)p.indptr[u + 1] - a) * p.P;
+    for (long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x; t < T;
+         t += (long long)gridDim.x * blockDim.x) {
+      const long long r = p.row_of[u * p.Tmax + t];
+      if (r < 0) continue;
+      if (a < 0 || r >= rows || a * p.P + r >= p.page_cap * p.P)
+        report(p.err, SKV_ERR_CORRUPT);
+      else
+        p.row_pos[a * p.P + r] = (int32_t)t;
+    }
+  }
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      tree_kernel<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  tree_kernel<CAP, BIAS><<<(unsigned)p.S, kThreads, kSmemBytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+// Workspace: the positions, then the joins, then the parts of two slots a run.
+size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int N, int G,
+                            TreeParams* p, void* ws) {
+  const size_t pos = positions ? ((size_t)page_cap * P * 4 + 127) / 128 * 128 : 0;
+  const size_t join = ((size_t)S * 8 + 127) / 128 * 128;
+  const size_t rows = 2ull * S * N * G;
+  if (p) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p->row_pos = reinterpret_cast<int32_t*>(w);
+    p->join = reinterpret_cast<int2*>(w + pos);
+    p->part = reinterpret_cast<float*>(w + pos + join);
+    p->part_ml = reinterpret_cast<float2*>(w + pos + join + rows * kHeadDim * 4);
+  }
+  return pos + join + rows * (kHeadDim * 4 + 8);
+}
+
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   const long long U = (long long)p.B * p.Hkv;
   if (U == 0) return cudaSuccess;
-  if (U * p.N > 0x7FFFFFFFLL || U > 65535) return cudaErrorInvalidValue;
+  cudaError_t e;
   if (p.slopes && p.Tmax > 0) {
     const long long bx = std::min<long long>((p.Tmax + 255) / 256, std::max<long long>(1, 1184 / U));
-    tree_positions_kernel<<<dim3((unsigned)bx, (unsigned)U), 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    tree_positions_kernel<<<dim3((unsigned)bx, (unsigned)std::min<long long>(U, 65535)), 256, 0,
+                            stream>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const unsigned grid = (unsigned)(U * p.N);
-  switch (p.Hq / p.Hkv) {
-    case 1: tree_kernel<1><<<grid, kTreeThreads, 0, stream>>>(p); break;
-    case 2: tree_kernel<2><<<grid, kTreeThreads, 0, stream>>>(p); break;
-    default: tree_kernel<4><<<grid, kTreeThreads, 0, stream>>>(p); break;
-  }
-  return cudaGetLastError();
+  if (p.softcap > 0.0f)
+    e = p.slopes ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
+  else
+    e = p.slopes ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
+  if (e != cudaSuccess) return e;
+  // the join: its launch overlaps the grid before it, its work waits for it
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.S, (unsigned)((p.N * (p.Hq / p.Hkv) + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel, p);
 }
 
 }  // namespace skv
