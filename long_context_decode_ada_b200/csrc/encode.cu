@@ -119,6 +119,15 @@ __device__ __forceinline__ uint32_t rho_code(long long mx, long long my, u128 R2
   return c;
 }
 
+// byte offset, within a page's V section, of element (row, dim)
+__device__ __forceinline__ int v_frag_offset(int row, int dd, int elem_bytes) {
+  const int k = row >> 3, tr = row & 7, t4 = tr >> 1, lo = tr & 1;
+  const int mt = dd >> 4, rem = dd & 15, g = rem & 7, hi = rem >> 3;
+  const int L = 4 * g + t4, e = 2 * hi + lo;
+  if (elem_bytes == 1) return k * 1024 + 512 * (mt >> 2) + 16 * L + 4 * (mt & 3) + e;
+  return k * 2048 + 512 * (mt >> 1) + 16 * L + 8 * (mt & 1) + 2 * e;
+}
+
 // The boundary vectors of the three angle codes (fp32 values), in shared
 // memory as doubles, (x, y) of a boundary in one 16-byte load.
 struct Boundaries {

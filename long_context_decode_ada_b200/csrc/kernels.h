@@ -297,6 +297,9 @@ struct TreeParams {
 size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int N, int G,
                             TreeParams* p, void* ws);
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
+// The form for few rows (tree_rows.cu): N * Hq / Hkv up to kTreeRows.
+constexpr int kTreeRows = 32;
+cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t stream);
 
 // Eviction by score (evict.cu).
 struct EvictParams {

@@ -16,14 +16,14 @@
 //   planner (1 warp)   turns the page list into tile descriptors (a ring of 32
 //                      in shared memory), checks ids and headers, and asks for
 //                      the pages' bytes in L2 (bulk prefetch)
-//   decode (16 warps)  two teams of 8 take the tiles in turn, a warp 8 rows:
-//                      codes to fp16 keys by gathers from a replicated table
-//                      (one conflict-free wavefront a gather), int8 values to
-//                      fp16, both written as swizzled operand tiles (32 KB a
-//                      tile, three tiles in flight).  The loads of a warp's
-//                      next rows are issued as soon as the registers of the
-//                      present ones are free
-//   mma (1 thread)     S = Q K^T and O += P V by tcgen05.mma (fp16, fp32
+//   decode (12 warps)  three teams of 4 take the tiles in turn, a warp 16 rows
+//                      in two steps of 8: codes to fp16 keys by gathers from a
+//                      replicated table (one conflict-free wavefront a
+//                      gather), int8 values to fp16, both written as swizzled
+//                      operand tiles (32 KB a tile, three in flight).  The
+//                      loads of the next 8 rows are issued as soon as the
+//                      registers of the present ones are free
+//   mma (1 warp)       S = Q K^T and O += P V by tcgen05.mma (fp16, fp32
 //                      accumulators); Q and P are read from tensor memory, so
 //                      that shared memory feeds K and V only
 //   softmax (8 warps)  two groups of 4, one per stream: scores from tensor
@@ -43,75 +43,77 @@
 #include <algorithm>
 #include <cstddef>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "tree.cuh"
 
 namespace skv {
 
 namespace {
 
-constexpr int kTile = 64;            // tokens of a tile
-constexpr int kStages = 3;           // tiles of keys and values in flight
+using namespace tree;
+
+constexpr int kStages = 3;           // tiles of keys and values in flight, one a team
 constexpr int kRing = 32;            // tile descriptors
 constexpr int kBatch = 8;            // tiles the planner publishes at once
-constexpr int kTeamWarps = 8;        // decode warps of a team (8 rows each)
+constexpr int kTeamWarps = 4;        // decode warps of a team (16 rows each)
 constexpr int kSoftWarps = 8;
-constexpr int kDecodeWarps = 2 * kTeamWarps;
+constexpr int kDecodeWarps = kStages * kTeamWarps;
 constexpr int kPlanner = kSoftWarps + kDecodeWarps;
 constexpr int kMma = kPlanner + 1;
 constexpr int kThreads = (kSoftWarps + kDecodeWarps + 4) * 32;
 // registers a thread: softmax, decode, planner / mma; their sum over the
-// threads is what the block is launched with (896 x 72)
-constexpr int kRegsSoft = 104, kRegsDecode = 64, kRegsHelp = 40;
-static_assert(256 * kRegsSoft + 512 * kRegsDecode + 128 * kRegsHelp <= kThreads * 72, "registers");
-constexpr float kRaise = 8.0f;       // log2 units a score may pass the running maximum
-constexpr int kBufRow = 132;         // floats of a row of the output buffer
+// threads is what the block is launched with (768 x 80)
+constexpr int kRegsSoft = 112, kRegsDecode = 64, kRegsHelp = 64;
+static_assert(32 * (kSoftWarps * kRegsSoft + kDecodeWarps * kRegsDecode + 4 * kRegsHelp) <=
+                  kThreads * 80, "registers");
+constexpr int kBufRow = 68;          // floats of a row of the output buffer (64 dims)
 
 enum : uint32_t { kFirst = 1, kLast = 2, kDraft = 4, kEnd = 8 };
 
 // columns of tensor memory
 constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 256;
 
-struct Tile {
-  unsigned long long page[4];   // address, 0: none
+struct __align__(16) Part {     // 16 rows of a tile
+  unsigned long long page;      // address (tier < 3)
+  uint16_t at, rows;            // first row within the page, rows in use
+  uint32_t tier;                // 3: no row
+};
+
+struct __align__(16) Tile {
+  Part part[4];
   unsigned long long valid;     // bit c: column c holds a token
   int unit, n;                  // (sequence, kv head) and its drafted tokens
   uint32_t flags;
   int first;                    // index of the first page in the page list
   int slot;                     // partial slot, -1: the unit lies in this run
-  uint8_t tier[4];              // 3: no page
-  uint8_t rows[4];
+  int bad;                      // a drafted value lies outside fp16
 };
 
 struct __align__(16) Fixed {
-  unsigned long long full[kStages], empty[kStages];
+  unsigned long long kfull[kStages], vfull[kStages], kempty[kStages], vempty[kStages];
   unsigned long long sfull[2], pfull[2], odone[2];
   unsigned long long qfull, sync, fin;
   unsigned long long dfull[kRing / kBatch], rfree[kRing / kBatch];
   unsigned long long scan[kThreads / 32];
-  unsigned long long ctot, cstart;
-  int ustart;
+  Run run;
   int abort;
   uint32_t tmem;
-  int bad[kRing];               // a drafted value of the tile is outside fp16
   __align__(16) Tile ring[kRing];
   __align__(16) float pos[kStages][kTile];   // positions (from the unit's first q_pos)
   __align__(16) float cs[kStages][kTile];    // drafted keys: what a score is scaled by
   float m[2][128], l[2][128];
 };
 
-constexpr uint32_t kTbl1 = 256 * 128, kTbl2 = 64 * 128;   // entries of 32 copies of 4 bytes
+// Shared memory: [fixed block, output buffer][tables][stages].  The tables
+// start on a 64 KB boundary: entry e of T1's (the code byte) is at 256 e, in
+// 32 copies of 4 bytes, so that one byte permutation forms a gather's
+// address; T2's entries (angle | share << 4) fill the other halves.
+constexpr uint32_t kTblBytes = 65536;
 constexpr uint32_t kStageBytes = 2 * kTile * 256;         // keys, values
 constexpr uint32_t kBufBytes = 128 * kBufRow * 4;
-constexpr uint32_t kAtTbl2 = kStages * kStageBytes;       // 8 KB aligned
-constexpr uint32_t kAtTbl1 = kAtTbl2 + kTbl2;
-constexpr uint32_t kAtBuf = kAtTbl1 + kTbl1;
-constexpr uint32_t kAtFixed = kAtBuf + kBufBytes;
-// the base is rounded up to 8 KB (the T2 table's address bits are disjoint
-// from its index bits)
-constexpr uint32_t kSmemBytes = kAtFixed + sizeof(Fixed) + 8192;
-static_assert(kAtTbl2 % 8192 == 0 && kAtFixed % 16 == 0, "layout");
-static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr uint32_t kAtBuf = (sizeof(Fixed) + 127) / 128 * 128;
+constexpr uint32_t kLowBytes = kAtBuf + kBufBytes;
+constexpr uint32_t kSmemBytes = 232448;
+static_assert(kLowBytes + 1024 <= 65536, "the tables start at 64 KB");
 
 // ------------------------------------------------------------ tensor memory
 __device__ __forceinline__ void tc_fence_before() {
@@ -168,66 +170,10 @@ constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((kHeadDim / 8) << 17) | (
 // Operand tiles in shared memory: rows of 128 bytes, their 16-byte chunks
 // permuted by the row's low three bits (128-byte swizzle), groups of 8 rows
 // 1024 bytes apart; the second 64 dims follow 8 KB behind.
-constexpr unsigned long long kDescBase =
-    ((unsigned long long)(1024 / 16) << 32) | (1ull << 46) | (2ull << 61);
-__device__ __forceinline__ unsigned long long key_operand(uint32_t at) {
-  return kDescBase | (1ull << 16) | (unsigned long long)((at & 0x3FFFFu) >> 4);
-}
-__device__ __forceinline__ unsigned long long value_operand(uint32_t at) {
-  return kDescBase | ((unsigned long long)(8192 / 16) << 16) |
-         (unsigned long long)((at & 0x3FFFFu) >> 4);
-}
-
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
-               "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 ldg128(const uint8_t* a) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 h =
-      __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcpf(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-__device__ __forceinline__ float from16(uint16_t x, int bf16) {
-  return bf16 ? __bfloat162float(__ushort_as_bfloat16(x)) : __half2float(__ushort_as_half(x));
-}
-__device__ __forceinline__ float2 from16x2(uint32_t x, int bf16) {
-  return make_float2(from16((uint16_t)x, bf16), from16((uint16_t)(x >> 16), bf16));
-}
-// |x| of both halves as one comparable word: the larger bit pattern
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t x) {
-  return max(m, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
-}
-// e with 2^e |x| in [2^14, 2^15) for the largest |x| (bit pattern m)
-__device__ __forceinline__ int scale_exp(uint32_t m, int bf16) {
-  if (m == 0) return 0;
-  const uint32_t b = __float_as_uint(from16((uint16_t)m, bf16));
-  const int e = 141 - (int)(b >> 23);
-  return b >= 0x7F800000u ? 0 : min(100, e);
+constexpr uint32_t kDescHigh = (1024 / 16) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescKeys = 1u << 16, kDescValues = (8192u / 16) << 16;
+__device__ __forceinline__ unsigned long long operand(uint32_t low) {
+  return ((unsigned long long)kDescHigh << 32) | low;
 }
 
 // A bounded wait of a whole warp: false for all lanes when one gave up.
@@ -241,152 +187,54 @@ __device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t pari
   }
   return done;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
 }
 
-// ------------------------------------------------------------------ the split
-// Pages of a unit by tier and their costs.  A dense page's bytes take 2.6
-// times a coded one's, but its conversion less: it counts twice.  More than
-// 128 rows cost half as much again (decoded once, multiplied twice).
-struct Unit {
-  long long first;     // index of the first page
-  int np, n;           // pages, drafted tokens
-  int nt[3];
-  int w[3];
-  unsigned long long pages, last, cost;  // cost of the pages, start of the last item, all
+// More than 128 rows cost half as much again (decoded once, multiplied twice).
+struct RowsCost {
+  __device__ __forceinline__ int operator()(int rows) const { return rows > 128 ? 3 : 2; }
 };
 
-__device__ __forceinline__ Unit unit_of(const TreeParams& p, int u) {
-  Unit x;
-  const long long a = max(0, p.indptr[u]), z = min((long long)p.indptr[u + 1], p.page_cap);
-  const int b = u / p.Hkv;
-  x.n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
-  x.first = a;
-  x.np = (int)max(0ll, z - a);
-  int n0 = 0, n1 = x.np;
-  if (p.tier_indptr) {
-    const int t0 = p.tier_indptr[3 * u], t1 = p.tier_indptr[3 * u + 1],
-              t2 = p.tier_indptr[3 * u + 2];
-    n0 = min(max(t1 - t0, 0), x.np);
-    n1 = min(max(t2 - t1, 0), x.np - n0);
-  }
-  x.nt[0] = n0;
-  x.nt[1] = n1;
-  x.nt[2] = x.np - n0 - n1;
-  const int f = x.n * (p.Hq / p.Hkv) > 128 ? 3 : 2;
-  x.w[0] = 2 * f;
-  x.w[1] = x.w[2] = f;
-  x.pages = (unsigned long long)x.w[0] * x.nt[0] + (unsigned long long)f * (x.nt[1] + x.nt[2]);
-  const int ipp = kTile / p.P;
-  if (x.n == 0) {
-    x.pages = x.last = x.cost = 0;
-  } else if (p.K || x.np == 0) {
-    x.last = x.pages;
-    x.cost = x.pages + (unsigned long long)(f * ipp);
-  } else {
-    const int k = (x.np - 1) / ipp * ipp;  // the last tile's first page
-    const int a0 = min(k, n0);
-    x.last = (unsigned long long)x.w[0] * a0 + (unsigned long long)f * (k - a0);
-    x.cost = x.pages;
-  }
-  return x;
-}
-
-// The first tile of the unit that starts at cost y or above.
-__device__ __forceinline__ int tile_at(const Unit& x, long long y, int ipp) {
-  if (y <= 0) return 0;
-  long long g = 0;
-#pragma unroll
-  for (int t = 0; t < 3; ++t) {
-    const long long c = (long long)x.nt[t] * x.w[t];
-    if (y > c) {
-      y -= c;
-      g += x.nt[t];
-    } else {
-      g += (y + x.w[t] - 1) / x.w[t];
-      y = 0;
-      break;
-    }
-  }
-  if (y > 0) g = x.np;
-  const int tiles = (x.np + ipp - 1) / ipp;
-  return min(tiles, (int)((g + ipp - 1) / ipp));
-}
-
-// Total cost and the unit that holds the start of run c (block-wide).
-__device__ __forceinline__ int find_start(const TreeParams& p, Fixed& f, int c) {
-  const int U = p.B * p.Hkv, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int per = (U + kThreads - 1) / kThreads;
-  const int u0 = min(U, tid * per), u1 = min(U, u0 + per);
-  unsigned long long mine = 0;
-  for (int u = u0; u < u1; ++u) mine += unit_of(p, u).cost;
-  unsigned long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) f.scan[w] = x;
-  if (tid == 0) f.ustart = U;
-  __syncthreads();
-  unsigned long long before = x - mine, tot = 0;
-  for (int k = 0; k < kThreads / 32; ++k) {
-    if (k < w) before += f.scan[k];
-    tot += f.scan[k];
-  }
-  // at least kMinTiles tiles of coded rows a run
-  constexpr unsigned long long kMinTiles = 1;
-  const unsigned long long least = kMinTiles * 2 * (kTile / p.P);
-  const int S = (int)min((unsigned long long)p.S, max(1ull, (tot + least - 1) / least));
-  if (c < S && tot > 0) {
-    const unsigned long long from = ((unsigned long long)c * tot + S - 1) / S;
-    unsigned long long cc = before;
-    for (int u = u0; u < u1; ++u) {
-      const unsigned long long k = unit_of(p, u).cost;
-      if (cc <= from && from < cc + k) {
-        f.ustart = u;
-        f.cstart = cc;
-      }
-      cc += k;
-    }
-  }
-  if (tid == 0) f.ctot = tot;
-  __syncthreads();
-  return S;
-}
-
 // ---------------------------------------------------------------- the planner
-__device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int S, int lane) {
-  const int U = p.B * p.Hkv, ipp = kTile / p.P, sh = __ffs(ipp) - 1;
-  const unsigned long long tot = f.ctot;
-  int u = f.ustart, k = 0, kend = 0, slot = -1, ends = 0;
+__device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int lane) {
+  const int U = p.B * p.Hkv, ipp = kTile / p.P, lgP = __ffs(p.P) - 1;
+  const int mine = lane >> 2, part = lane & 3;      // the lane's tile of a batch, its 16 rows
+  const int pg = 16 * part >> lgP, at = 16 * part & (p.P - 1);
+  const Run run = f.run;
+  int u = run.unit, k = 0, kend = 0, slot = -1, ends = 0;
   bool open = false, draft = false, fresh = false;
-  unsigned long long cc = f.cstart;
-  const unsigned long long from = ((unsigned long long)c * tot + S - 1) / S,
-                           to = ((unsigned long long)(c + 1) * tot + S - 1) / S;
+  unsigned long long cc = run.before;
   int2 join = make_int2(-1, 0);
   Unit x = {};
-  for (int batch = 0; ends < 2; ++batch) {
+  // (an end for each team)
+  for (int batch = 0; ends < kStages; ++batch) {
     if (batch >= 2 &&
         !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f, p.err))
       break;
-    const int mine = lane >> sh, pg = lane & (ipp - 1);
     int t_unit = 0, t_n = 0, t_np = 0, t_slot = -1;
     long long t_first = 0;
     uint32_t t_flags = kEnd;
+#pragma unroll 1
     for (int e = 0; e < kBatch; ++e) {
       // the next unit with a part in this run
-      while (!open && u < U && cc < to) {
-        x = unit_of(p, u);
-        if (x.cost > 0 && cc + x.last >= from) {
-          k = tile_at(x, (long long)(from - cc), ipp);
-          kend = tile_at(x, (long long)(to - cc), ipp);
-          draft = p.K != nullptr && cc + x.last < to;
-          const int r0 = (int)(cc * S / tot), r1 = (int)((cc + x.last) * S / tot);
-          slot = r0 == r1 ? -1 : (c == r0 ? 2 * c + 1 : 2 * c);
-          if (c == r0 && r1 > r0) join = make_int2(u, r1);
+      while (!open && u < U && cc < run.to) {
+        x = unit_of(p, u, RowsCost());
+        Share y;
+        if (part_of(p, x, run, c, cc, y)) {
+          k = y.k;
+          kend = y.kend;
+          draft = y.draft;
+          slot = y.slot;
+          if (y.starts) join = make_int2(u, y.last);
           open = fresh = true;
         } else {
           cc += x.cost;
@@ -426,47 +274,44 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
         ++u;
       }
     }
-    // a lane per page
-    unsigned long long at = 0;
-    int tier = 3, rows = 0;
-    if (mine < kBatch && pg < t_np) {
+    // a lane per 16 rows
+    Part o;
+    o.page = 0;
+    o.at = (uint16_t)at;
+    o.rows = 0;
+    o.tier = 3;
+    if (pg < t_np) {
       const uint32_t id = p.ids[t_first + pg], sl = id & 0x3FFFFFFFu;
       const int t = (int)(id >> 30);
       if (t > 2 || (long long)sl >= p.slots[t]) {
         report(p.err, SKV_ERR_CORRUPT);
       } else {
         const uint8_t* a = p.pool[t] + (long long)sl * p.stride[t];
-        const uint32_t bytes = (uint32_t)(kHdrBytes + p.P * tier_row_bytes(t));
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(bytes) : "memory");
+        if (at == 0) prefetch_page(a, p.P, t);
         const uint32_t h = *reinterpret_cast<const uint32_t*>(a);
-        rows = (int)(h & 0xFFFFu);
+        const int rows = (int)(h & 0xFFFFu);
         if ((h >> 16) != ((uint32_t)t | ((uint32_t)kPageMagic << 8)) || rows > p.P) {
           report(p.err, SKV_ERR_CORRUPT);
-          rows = 0;
-        } else {
-          tier = t;
-          at = reinterpret_cast<unsigned long long>(a);
+        } else if (rows > at) {
+          o.page = reinterpret_cast<unsigned long long>(a);
+          o.rows = (uint16_t)min(rows - at, 16);
+          o.tier = (uint32_t)t;
         }
       }
     }
-    unsigned long long valid =
-        rows == 0 ? 0ull : (rows == 64 ? ~0ull : ((1ull << rows) - 1)) << (pg * p.P);
-    for (int o = 1; o < ipp; o <<= 1) valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, o);
-    if (mine < kBatch) {
-      const int e = (batch & 3) * kBatch + mine;
-      Tile& d = f.ring[e];
-      d.page[pg] = at;
-      d.tier[pg] = (uint8_t)tier;
-      d.rows[pg] = (uint8_t)rows;
-      if (pg == 0) {
-        d.valid = (t_flags & kDraft) ? (t_n >= 64 ? ~0ull : (1ull << t_n) - 1) : valid;
-        d.unit = t_unit;
-        d.n = t_n;
-        d.flags = t_flags;
-        d.first = (int)t_first;
-        d.slot = t_slot;
-        f.bad[e] = 0;
-      }
+    unsigned long long valid = (unsigned long long)((1u << o.rows) - 1) << (16 * part);
+    valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 1);
+    valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 2);
+    Tile& d = f.ring[(batch & 3) * kBatch + mine];
+    d.part[part] = o;
+    if (part == 0) {
+      d.valid = (t_flags & kDraft) ? (t_n >= 64 ? ~0ull : (1ull << t_n) - 1) : valid;
+      d.unit = t_unit;
+      d.n = t_n;
+      d.flags = t_flags;
+      d.first = (int)t_first;
+      d.slot = t_slot;
+      d.bad = 0;
     }
     warp_arrive(f.dfull[batch & 3]);
   }
@@ -478,39 +323,23 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
 struct Rows {
   uint4 k[4], v[4];
   uint32_t r, s;     // radius; scales of value rows 2 t4, 2 t4 + 1
-  int tier, rows;    // rows in use of the warp's 8
 };
 
-struct Place {       // of a warp's 8 rows in its page
-  const uint8_t* page;
-  int tier, rows, at;
-};
-
-__device__ __forceinline__ Place place_of(const Tile& d, int P, int w) {
-  Place x;
-  const int k = 8 * w / P;
-  x.at = 8 * w - k * P;
-  x.page = reinterpret_cast<const uint8_t*>(d.page[k]);
-  x.tier = d.tier[k];
-  x.rows = min(max((int)d.rows[k] - x.at, 0), 8);
-  if (x.rows == 0) x.tier = 3;
-  return x;
-}
-
-__device__ __forceinline__ void load_keys(const Place& x, int P, int lane, Rows& o) {
+__device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t tier, int at, int P,
+                                          int lane, Rows& o) {
   const int t = lane >> 2, g = lane & 3;
-  if (x.tier == SKV_TIER_T0) {
-    const uint8_t* a = x.page + kHdrBytes + 256 * (x.at + t);
+  const uint8_t* a = page + kHdrBytes;
+  if (tier == SKV_TIER_T0) {
+    a += 256 * (at + t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.k[i] = ldg128(a + 16 * ((4 * i + g) ^ (4 * (t & 1))));
-  } else if (x.tier < 3) {
-    const uint8_t* a = x.page + kHdrBytes;
-    o.r = *reinterpret_cast<const uint16_t*>(a + 2 * (x.at + t));
+  } else if (tier < 3) {
+    o.r = *reinterpret_cast<const uint16_t*>(a + 2 * (at + t));
     a += 2 * P;
-    if (x.tier == SKV_TIER_T1) {
-      o.k[0] = ldg128(a + 64 * (x.at + t) + 16 * g);
+    if (tier == SKV_TIER_T1) {
+      o.k[0] = ldg128(a + 64 * (at + t) + 16 * g);
     } else {
-      a += 48 * (x.at + t);
+      a += 48 * (at + t);
       const uint2 n = *reinterpret_cast<const uint2*>(a + 8 * g);
       o.k[0].x = n.x;
       o.k[0].y = n.y;
@@ -519,41 +348,44 @@ __device__ __forceinline__ void load_keys(const Place& x, int P, int lane, Rows&
   }
 }
 
-__device__ __forceinline__ void load_values(const Place& x, int P, int lane, Rows& o) {
-  if (x.tier == SKV_TIER_T0) {
-    const uint8_t* a = x.page + kHdrBytes + 256 * P + 256 * x.at + 16 * lane;
+__device__ __forceinline__ void load_values(const uint8_t* page, uint32_t tier, int at, int P,
+                                            int lane, Rows& o) {
+  const uint8_t* a = page + kHdrBytes;
+  if (tier == SKV_TIER_T0) {
+    a += 256 * (P + at) + 16 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.v[i] = ldg128(a + 512 * i);
-  } else if (x.tier < 3) {
-    const int cb = x.tier == SKV_TIER_T1 ? 64 : 48;
-    const uint8_t* a = x.page + kHdrBytes + (2 + cb) * P;
-    o.s = *reinterpret_cast<const uint32_t*>(a + 2 * (x.at + 2 * (lane & 3)));
-    a += 2 * P + 128 * x.at + 16 * lane;
+  } else if (tier < 3) {
+    const int cb = tier == SKV_TIER_T1 ? 64 : 48;
+    a += (2 + cb) * P;
+    o.s = *reinterpret_cast<const uint32_t*>(a + 2 * (at + 2 * (lane & 3)));
+    a += 2 * P + 128 * at + 16 * lane;
     o.v[0] = ldg128(a);
     o.v[1] = ldg128(a + 512);
   }
 }
 
-// address of the entry of code byte k of w, in the lane's column of the table
+// Address of a code's entry in the lane's copy: byte k of w as the second
+// byte of the table's address (T1); T2 pair j of nibbles nw, crumbs cw.
 __device__ __forceinline__ uint32_t t1_at(uint32_t w, int k, uint32_t tb) {
-  return tb + (__byte_perm(w, 0u, 0x4440u | (uint32_t)k) << 7);
+  return __byte_perm(w, tb, 0x7604u | (uint32_t)(k << 4));
 }
 __device__ __forceinline__ uint32_t t2_at(uint32_t nw, uint32_t cw, int j, uint32_t tb) {
-  const int sn = 4 * (j & 7) - 7, sc = 2 * j - 11;
+  const int sn = 4 * (j & 7) - 8, sc = 2 * j - 12;
   const uint32_t xn = sn >= 0 ? (nw >> sn) : (nw << -sn);
   const uint32_t xc = sc >= 0 ? (cw >> sc) : (cw << -sc);
-  return (xn & 0x780u) | (xc & 0x1800u) | tb;
+  return (xn & 0xF00u) | (xc & 0x3000u) | tb;
 }
 
 // keys of 8 rows -> fp16 rows T0 .. T0 + 7 of the tile at kb
-__device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, int lane,
-                                           uint32_t tb1, uint32_t tb2) {
+__device__ __forceinline__ void store_keys(const Rows& o, uint32_t tier, uint32_t kb, int T0,
+                                           int lane, uint32_t tb) {
   const int t = lane >> 2, g = lane & 3, odd = t & 1;
   // odd rows go through their chunks in the order 1 0 3 2, which spreads a
   // quarter warp's stores over all banks
   const uint32_t row = kb + (uint32_t)(T0 + t) * 128;
   const uint32_t at[2] = {row + (((4 * odd + g) ^ t) << 4), row + (((4 * (odd ^ 1) + g) ^ t) << 4)};
-  if (o.tier == SKV_TIER_T0) {
+  if (tier == SKV_TIER_T0) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint4 x;
@@ -563,20 +395,21 @@ __device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, i
       x.w = odd ? o.k[e ^ 1].w : o.k[e].w;
       sts128(at[e & 1] + (e >> 1) * 8192, x);
     }
-  } else if (o.tier == SKV_TIER_T1) {
+  } else if (tier == SKV_TIER_T1) {
     const uint32_t r = o.r | (o.r << 16);
     const uint32_t w[4] = {odd ? o.k[0].y : o.k[0].x, odd ? o.k[0].x : o.k[0].y,
                            odd ? o.k[0].w : o.k[0].z, odd ? o.k[0].z : o.k[0].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint4 x;
-      x.x = hmul2(lds32(t1_at(w[e], 0, tb1)), r);
-      x.y = hmul2(lds32(t1_at(w[e], 1, tb1)), r);
-      x.z = hmul2(lds32(t1_at(w[e], 2, tb1)), r);
-      x.w = hmul2(lds32(t1_at(w[e], 3, tb1)), r);
+      x.x = hmul2(lds32(t1_at(w[e], 0, tb)), r);
+      x.y = hmul2(lds32(t1_at(w[e], 1, tb)), r);
+      x.z = hmul2(lds32(t1_at(w[e], 2, tb)), r);
+      x.w = hmul2(lds32(t1_at(w[e], 3, tb)), r);
       sts128(at[e & 1] + (e >> 1) * 8192, x);
     }
-  } else if (o.tier == SKV_TIER_T2) {
+  } else if (tier == SKV_TIER_T2) {
+    const uint32_t tb2 = tb + 128;
     const uint32_t r = o.r | (o.r << 16);
     // pairs 4 i .. 4 i + 3: nibbles and crumbs 4 i + b; odd rows swap halves
     const int sw = 16 * odd;
@@ -602,16 +435,13 @@ __device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, i
 // Values of 8 rows -> fp16.  The tile's columns are a permutation of the
 // dims that a lane of the pages' fragment order holds together: column
 // 64 h + 8 g + 2 m + hi is dim 64 h + 16 m + 8 hi + g.
-__device__ __forceinline__ int column_of(int d) {
-  return (d & 64) + 8 * (d & 7) + 2 * ((d >> 4) & 3) + ((d >> 3) & 1);
-}
-
-__device__ __forceinline__ void store_values(const Rows& o, uint32_t vb, int T0, int lane) {
+__device__ __forceinline__ void store_values(const Rows& o, uint32_t tier, int rows, uint32_t vb,
+                                             int T0, int lane) {
   const int g = lane >> 2, a = 2 * (lane & 3), b = a + 1;
   const uint32_t ra = vb + (uint32_t)(T0 + a) * 128 + ((g ^ a) << 4);
   const uint32_t rb = vb + (uint32_t)(T0 + b) * 128 + ((g ^ b) << 4);
-  if (o.tier == SKV_TIER_T0) {
-    const bool ua = a < o.rows, ub = b < o.rows;
+  if (tier == SKV_TIER_T0) {
+    const bool ua = a < rows, ub = b < rows;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 x = o.v[2 * h], y = o.v[2 * h + 1];
@@ -624,11 +454,11 @@ __device__ __forceinline__ void store_values(const Rows& o, uint32_t vb, int T0,
       sts128(ra + h * 8192, p);
       sts128(rb + h * 8192, q);
     }
-  } else if (o.tier < 3) {
+  } else if (tier < 3) {
     // v + 128 as the low byte of 1024 + x in fp16, less 1152 (exact), times
     // the scale (rounded once); rows that are not there get the scale 0
-    const uint32_t sa = a < o.rows ? __byte_perm(o.s, 0u, 0x1010) : 0u;
-    const uint32_t sb = b < o.rows ? __byte_perm(o.s, 0u, 0x3232) : 0u;
+    const uint32_t sa = a < rows ? __byte_perm(o.s, 0u, 0x1010) : 0u;
+    const uint32_t sb = b < rows ? __byte_perm(o.s, 0u, 0x3232) : 0u;
     const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -715,156 +545,140 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
 }
 
 template <bool BIAS>
-__device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t base, int wd,
+__device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t tbl, int wd,
                                             int lane) {
-  const int w = wd & (kTeamWarps - 1), P = p.P;
-  const uint32_t tb1 = base + kAtTbl1 + 4 * lane, tb2 = base + kAtTbl2 + 4 * lane;
+  const int w = wd & (kTeamWarps - 1), stage = wd / kTeamWarps, P = p.P, T0 = 16 * w;
+  const uint32_t tb = tbl + 4 * lane;
+  const uint32_t kb = tbl + kTblBytes + stage * kStageBytes, vb = kb + kTile * 256;
   Rows o;
-  int t = wd / kTeamWarps;
+  int t = stage;
+  uint32_t turn = 0;
   if (!warp_wait(f.dfull[0], 0, f, p.err)) return;
   uint32_t flags = f.ring[t].flags;
-  o.tier = 3;
-  o.rows = 0;
+  Part x = f.ring[t].part[w];
+  const uint8_t* page = reinterpret_cast<const uint8_t*>(x.page);
   o.r = o.s = 0;
-  if (!(flags & (kEnd | kDraft))) {
-    const Place x = place_of(f.ring[t], P, w);
-    o.tier = x.tier;
-    o.rows = x.rows;
-    load_keys(x, P, lane, o);
-    load_values(x, P, lane, o);
-  }
+  load_keys(page, x.tier, x.at, P, lane, o);
+  load_values(page, x.tier, x.at, P, lane, o);
   while (!(flags & kEnd)) {
-    const int stage = t % kStages, turn = t / kStages;
-    const uint32_t kb = base + stage * kStageBytes, vb = kb + kTile * 256;
     const Tile& d = f.ring[t & (kRing - 1)];
-    if (turn > 0 && !warp_wait(f.empty[stage], (turn - 1) & 1, f, p.err)) return;
-    if (BIAS && lane < 8) {
+    const int rows = x.rows;
+    const uint32_t tier = x.tier;
+    const bool draft = (flags & kDraft) != 0;
+    if (turn > 0 && !warp_wait(f.kempty[stage], (turn - 1) & 1, f, p.err)) return;
+    if (!draft) {
+      store_keys(o, tier, kb, T0, lane, tb);
+      load_keys(page, tier, x.at + 8, P, lane, o);
+    }
+    if (turn > 0 && !warp_wait(f.vempty[stage], (turn - 1) & 1, f, p.err)) return;
+    if (BIAS && lane < 16) {
       const int b = d.unit / p.Hkv;
       const int q0 = p.q_pos[(long long)b * p.N];
       int q = q0;
-      if (flags & kDraft) {
-        if (8 * w + lane < d.n) q = p.q_pos[(long long)b * p.N + 8 * w + lane];
-      } else if (lane < o.rows) {
-        const int k = 8 * w / P;
-        q = p.row_pos[((long long)d.first + k) * P + (8 * w - k * P) + lane];
+      if (draft) {
+        if (T0 + lane < d.n) q = p.q_pos[(long long)b * p.N + T0 + lane];
+      } else if (lane < rows) {
+        q = p.row_pos[(long long)d.first * P + T0 + lane];  // (a tile's pages follow each other)
       }
-      f.pos[stage][8 * w + lane] = (float)(q - q0);
+      f.pos[stage][T0 + lane] = (float)(q - q0);
     }
-    const int t2 = t + 2;
-    const bool turned = (t2 >> 3) != (t >> 3);
-    uint32_t next;
-    if (flags & kDraft) {
-      store_draft(p, d, kb, vb, f.cs[stage], &f.bad[t & (kRing - 1)], 8 * w, lane);
-      if (turned && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
-      const Tile& dn = f.ring[t2 & (kRing - 1)];
-      next = dn.flags;
-      o.tier = 3;
-      if (!(next & (kEnd | kDraft))) {
-        const Place x = place_of(dn, P, w);
-        o.tier = x.tier;
-        o.rows = x.rows;
-        load_keys(x, P, lane, o);
-        load_values(x, P, lane, o);
-      }
+    if (!draft) {
+      store_values(o, tier, rows, vb, T0, lane);
+      load_values(page, tier, x.at + 8, P, lane, o);
+      store_keys(o, tier, kb, T0 + 8, lane, tb);
     } else {
-      store_keys(o, kb, 8 * w, lane, tb1, tb2);
-      if (turned && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
-      const Tile& dn = f.ring[t2 & (kRing - 1)];
-      next = dn.flags;
-      Place x;
-      x.page = nullptr;
-      x.tier = 3;
-      x.rows = 0;
-      x.at = 0;
-      if (!(next & (kEnd | kDraft))) x = place_of(dn, P, w);
-      load_keys(x, P, lane, o);
-      store_values(o, vb, 8 * w, lane);
-      o.tier = x.tier;
-      o.rows = x.rows;
-      load_values(x, P, lane, o);
+#pragma unroll 1
+      for (int e = 0; e < 16; e += 8)
+        store_draft(p, d, kb, vb, f.cs[stage], &f.ring[t & (kRing - 1)].bad, T0 + e, lane);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    warp_arrive(f.full[stage]);
-    flags = next;
+    warp_arrive(f.kfull[stage]);
+    const int t2 = t + kStages;
+    if ((t2 >> 3) != (t >> 3) && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
+    flags = f.ring[t2 & (kRing - 1)].flags;
+    x = f.ring[t2 & (kRing - 1)].part[w];
+    page = reinterpret_cast<const uint8_t*>(x.page);
+    load_keys(page, x.tier, x.at, P, lane, o);
+    if (!draft) store_values(o, tier, rows - 8, vb, T0 + 8, lane);
+    load_values(page, x.tier, x.at, P, lane, o);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    warp_arrive(f.vfull[stage]);
     t = t2;
+    ++turn;
   }
 }
 
 // ------------------------------------------------------------------- the MMAs
-struct Pending {
-  int s, stage, tile;
-  bool first, release;
-};
-
-__device__ __forceinline__ bool one_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
-                                         int32_t* err) {
-  if (mbar_wait_bounded(smem_u32(&bar), parity, &f.abort)) return true;
-  if (!*(volatile int*)&f.abort) {
-    *(volatile int*)&f.abort = 1;
-    report(err, SKV_ERR_TIMEOUT);
-  }
-  return false;
-}
-
-__device__ __forceinline__ void mma_role(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
+__device__ __forceinline__ void mma_role(const TreeParams& p, Fixed& f, uint32_t stages,
+                                         uint32_t tm) {
   const int G = p.Hq / p.Hkv;
-  uint32_t jobs[2] = {0, 0};  // jobs of the streams so far
+  const bool lead = elect_one();
+  uint32_t stage = 0, turn = 0;       // of the present tile: its stage, the stage's parity
+  uint32_t pturn = 0;                 // bit s: parity of stream s's weights
   uint32_t segs = 0;
   int nb = 1, j = 0;
-  bool first[2] = {true, true}, pending = false;
-  Pending q = {};
+  // the job whose weights are still to come
+  bool pending = false, free_tile = false, free_ring = false;
+  uint32_t ps = 0, pstage = 0, padd = 0, pvt = 0, pbatch = 0;
   const auto pv = [&]() {
-    if (!one_wait(f.pfull[q.s], (jobs[q.s] - 1) & 1, f, p.err)) return false;
+    if (!warp_wait(f.pfull[ps], (pturn >> ps) & 1, f, p.err)) return false;
+    pturn ^= 1u << ps;
+    if (!warp_wait(f.vfull[pstage], pvt, f, p.err)) return false;
     tc_fence_after();
-    const uint32_t vb = base + q.stage * kStageBytes + kTile * 256;
-    const uint32_t a = tm + (nb == 2 ? kColS + 64 * q.s : kColP + 32 * q.s);
+    if (lead) {
+      const uint32_t low = kDescValues | ((stages + pstage * kStageBytes + kTile * 256) >> 4);
+      const uint32_t a = tm + (nb == 2 ? kColS + 64 * ps : kColP + 32 * ps);
+      const uint32_t o = tm + kColO + 128 * ps;
 #pragma unroll
-    for (int k = 0; k < kTile / 16; ++k)
-      tc_mma(tm + kColO + 128 * q.s, a + 8 * k, value_operand(vb + 2048 * k), kIdescO,
-             !(q.first && k == 0));
-    tc_commit(smem_u32(&f.odone[q.s]));
-    if (q.release) {
-      tc_commit(smem_u32(&f.empty[q.stage]));
-      if ((q.tile & (kBatch - 1)) == kBatch - 1)
-        tc_commit(smem_u32(&f.rfree[(q.tile / kBatch) & 3]));
+      for (int k = 0; k < kTile / 16; ++k)
+        tc_mma(o, a + 8 * k, operand(low + 128 * k), kIdescO, k > 0 ? 1u : padd);
+      tc_commit(smem_u32(&f.odone[ps]));
+      if (free_tile) tc_commit(smem_u32(&f.vempty[pstage]));
+      if (free_ring) tc_commit(smem_u32(&f.rfree[pbatch]));
     }
+    __syncwarp();
     pending = false;
     return true;
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !one_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
-    const Tile& d = f.ring[t & (kRing - 1)];
-    const uint32_t flags = d.flags;
-    if (flags & kEnd) break;
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
+    const uint32_t flags = f.ring[t & (kRing - 1)].flags;
+    if (flags & kEnd) return;
     if (flags & kFirst) {
-      if (!one_wait(f.qfull, segs & 1, f, p.err)) return;
+      if (!warp_wait(f.qfull, segs & 1, f, p.err)) return;
       ++segs;
-      nb = d.n * G > 128 ? 2 : 1;
+      nb = f.ring[t & (kRing - 1)].n * G > 128 ? 2 : 1;
       j = 0;
-      first[0] = first[1] = true;
     }
-    const int stage = t % kStages;
-    if (!one_wait(f.full[stage], (t / kStages) & 1, f, p.err)) return;
+    if (!warp_wait(f.kfull[stage], turn, f, p.err)) return;
     tc_fence_after();
-    const uint32_t kb = base + stage * kStageBytes;
     for (int b = 0; b < nb; ++b, ++j) {
-      const int s = j & 1;
+      const uint32_t s = j & 1;
+      if (lead) {
+        const uint32_t low = kDescKeys | ((stages + stage * kStageBytes) >> 4);
+        const uint32_t a = tm + kColQ + (nb == 2 ? 64 * s : 0), o = tm + kColS + 64 * s;
 #pragma unroll
-      for (int k = 0; k < kHeadDim / 16; ++k)
-        tc_mma(tm + kColS + 64 * s, tm + kColQ + (nb == 2 ? 64 * s : 0) + 8 * k,
-               key_operand(kb + (k >> 2) * 8192 + (k & 3) * 32), kIdescS, k > 0);
-      tc_commit(smem_u32(&f.sfull[s]));
+        for (int k = 0; k < kHeadDim / 16; ++k)
+          tc_mma(o, a + 8 * k, operand(low + (k >> 2) * 512 + (k & 3) * 2), kIdescS, k > 0);
+        tc_commit(smem_u32(&f.sfull[s]));
+        if (b == nb - 1) tc_commit(smem_u32(&f.kempty[stage]));
+      }
+      __syncwarp();
       if (pending && !pv()) return;
-      ++jobs[s];
-      q.s = s;
-      q.stage = stage;
-      q.tile = t;
-      q.first = first[s];
-      q.release = b == nb - 1;
-      first[s] = false;
+      ps = s;
+      pstage = stage;
+      pvt = turn;
+      padd = j > 1 ? 1u : 0u;
+      free_tile = b == nb - 1;
+      free_ring = free_tile && (t & (kBatch - 1)) == kBatch - 1;
+      pbatch = (t / kBatch) & 3;
       pending = true;
     }
     if ((flags & kLast) && !pv()) return;
+    if (++stage == kStages) {
+      stage = 0;
+      turn ^= 1;
+    }
   }
 }
 
@@ -873,8 +687,8 @@ struct Row {           // a lane's row in its stream
   float c;             // what a product is scaled by (log2 domain, before the cap)
   float cap, slope, rel;
   float m, l;
-  uint32_t jobs;       // of this stream so far
-  int mine;            // of this stream in the segment
+  uint32_t turn;       // parity of the stream's next job
+  int mine;            // its jobs in the segment
 };
 
 // Columns c0 .. c0 + NC - 1 of a tile: scores to weights.  S at `sa`, the
@@ -922,7 +736,7 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
     r.l *= a;
     r.m = m;
     if (r.mine > 0) {
-      if (!warp_wait(f.odone[wg], (r.jobs - 1) & 1, f, p.err)) return false;
+      if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int k = 0; k < kHeadDim; k += 16) {
@@ -937,85 +751,25 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
     }
   }
   const float m = r.m == -INFINITY ? 0.0f : r.m;
-  float l0 = 0.0f, l1 = 0.0f;
+  const float2 c2 = make_float2(r.c, r.c), m2 = make_float2(-m, -m);
+  float2 l2 = make_float2(r.l, 0.0f);
 #pragma unroll
   for (int k = 0; k < NC; k += 16) {
     uint32_t w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float x = s[k + 2 * e], y = s[k + 2 * e + 1];
-      const float a = ex2f((CAP || BIAS) ? x - m : fmaf(x, r.c, -m));
-      const float b = ex2f((CAP || BIAS) ? y - m : fmaf(y, r.c, -m));
-      l0 += a;
-      l1 += b;
-      w[e] = pack_f16x2(a, b);
+      float2 x = make_float2(s[k + 2 * e], s[k + 2 * e + 1]);
+      x = (CAP || BIAS) ? add2(x, m2) : fma2(x, c2, m2);
+      x.x = ex2f(x.x);
+      x.y = ex2f(x.y);
+      l2 = add2(l2, x);
+      w[e] = pack_f16x2(x.x, x.y);
     }
     tc_st8(pa + k / 2, w);
   }
-  r.l += l0 + l1;
+  r.l = l2.x + l2.y;
   tc_wait_st();
   return true;
-}
-
-// One row of the result: v = the lane's four dims (4 lane ..) of O, relative
-// to M, and its sum L.  Drafted values outside fp16's range are added here.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ void write_row(const TreeParams& p, const Tile& d, bool bad, int r,
-                                          float M, float L, float (&v)[4], int lane) {
-  const int G = p.Hq / p.Hkv, i = r / G, g = r - i * G;
-  const int b = d.unit / p.Hkv, h = d.unit - b * p.Hkv, hq = h * G + g;
-  const long long tok = (long long)b * p.N + i;
-  if (bad) {
-    unsigned long long bits = p.mask ? p.mask[tok] : (i == 63 ? ~0ull : (2ull << i) - 1);
-    if (d.n < 64) bits &= (1ull << d.n) - 1;
-    while (bits) {
-      const int j = __ffsll((long long)bits) - 1;
-      bits &= bits - 1;
-      const long long at = ((long long)b * p.N + j) * p.kv_stride + (long long)h * kHeadDim + 4 * lane;
-      float y[4], s = 0.0f;
-      bool out = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = from16(static_cast<const uint16_t*>(p.V)[at + e], p.kv_bf16);
-        if (fabsf(y[e]) <= 65504.0f)
-          y[e] = 0.0f;
-        else
-          out = true;
-        s += from16(static_cast<const uint16_t*>(p.q)[tok * p.q_stride + (long long)hq * kHeadDim +
-                                                      4 * lane + e],
-                    p.q_bf16) *
-             from16(static_cast<const uint16_t*>(p.K)[at + e], p.kv_bf16);
-      }
-      if (!__any_sync(0xFFFFFFFFu, out)) continue;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      s *= p.qk_scale;
-      if (CAP) s = p.softcap * tanhf(s / p.softcap);
-      if (BIAS)
-        s -= p.slopes[hq] * (float)(p.q_pos[tok] - p.q_pos[(long long)b * p.N + j]);
-      const float w = exp2f(s * 1.4426950408889634f - M);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (y[e] != 0.0f) v[e] += w * y[e];
-    }
-  }
-  if (d.slot >= 0) {
-    const long long at = (long long)d.slot * (p.N * G) + r;
-    *reinterpret_cast<float4*>(p.part + at * kHeadDim + 4 * lane) =
-        make_float4(v[0], v[1], v[2], v[3]);
-    if (lane == 0) p.part_ml[at] = make_float2(M, L);
-    return;
-  }
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  const long long at = (tok * p.Hq + hq) * kHeadDim + 4 * lane;
-  uint2 w;
-  if (p.q_bf16)
-    w = make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
-  else
-    w = make_uint2(pack_f16x2(v[0] * inv, v[1] * inv), pack_f16x2(v[2] * inv, v[3] * inv));
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
-  if (lane == 0 && p.lse)
-    p.lse[tok * p.Hq + hq] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 template <bool CAP, bool BIAS>
@@ -1111,147 +865,136 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     }
     for (int b = 0; b < nb; ++b, ++j) {
       if ((j & 1) != wg) continue;
-      if (!warp_wait(f.sfull[wg], r.jobs & 1, f, p.err)) return;
+      if (!warp_wait(f.sfull[wg], r.turn, f, p.err)) return;
       tc_fence_after();
       if (busy) {
         const int stage = t % kStages;
         unsigned long long bits = d.valid;
+        const int c0 = nb == 2 ? 0 : copy * (kTile * rc / 128);
         const float* cs = nullptr;
         if (flags & kDraft) {
           bits &= see;
-          cs = f.cs[stage];
+          cs = f.cs[stage] + c0;
         }
-        const float* pos = f.pos[stage];
-        const uint32_t sa = tm + kColS + 64 * wg;
+        const float* pos = f.pos[stage] + c0;
+        const uint32_t sa = tm + kColS + 64 * wg + c0;
+        const uint32_t pa = nb == 2 ? sa : tm + kColP + 32 * wg + c0 / 2;
         bool ok;
-        if (nb == 2) {
-          ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, sa, oa, wg, bits, cs, pos);
-        } else {
-          const uint32_t pa = tm + kColP + 32 * wg;
-          const int c0 = copy * (kTile * rc / 128);
-          if (cs) cs += c0;
-          pos += c0;
-          if (rc == 128) {
-            ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, pa, oa, wg, bits, cs, pos);
-          } else if (rc == 64) {
-            ok = softmax_job<32, CAP, BIAS>(p, f, r, sa + c0, pa + c0 / 2, oa, wg,
-                                            (bits >> c0) & 0xFFFFFFFFull, cs, pos);
-          } else {
-            ok = softmax_job<16, CAP, BIAS>(p, f, r, sa + c0, pa + c0 / 2, oa, wg,
-                                            (bits >> c0) & 0xFFFFull, cs, pos);
-          }
-        }
+        if (rc == 128)
+          ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, pa, oa, wg, bits, cs, pos);
+        else if (rc == 64)
+          ok = softmax_job<32, CAP, BIAS>(p, f, r, sa, pa, oa, wg, (bits >> c0) & 0xFFFFFFFFull, cs,
+                                          pos);
+        else
+          ok = softmax_job<16, CAP, BIAS>(p, f, r, sa, pa, oa, wg, (bits >> c0) & 0xFFFFull, cs, pos);
         if (!ok) return;
       }
       tc_fence_before();
       warp_arrive(f.pfull[wg]);
-      ++r.jobs;
+      r.turn ^= 1;
       ++r.mine;
     }
     if (!(flags & kLast)) continue;
-    // the segment's end: the streams' and copies' sums meet
+    // the segment's end: the streams' and copies' sums meet, 64 dims at a time
     if (r.mine > 0) {
-      if (!warp_wait(f.odone[wg], (r.jobs - 1) & 1, f, p.err)) return;
+      if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return;
       tc_fence_after();
     }
-    const bool bad = *(volatile int*)&f.bad[t & (kRing - 1)] != 0;
+    const bool bad = *(const volatile int*)&d.bad != 0;
     f.m[wg][tl] = r.m;
     f.l[wg][tl] = r.l;
     if (!meet()) return;
     float* const mine = buf + tl * kBufRow;
-    const int c0 = column_of(4 * lane);
+    const int copies = 128 / rc, sub = tl & (rc - 1);
+    float a = 1.0f;
     if (nb == 1) {
-      const int copies = 128 / rc, sub = tl & (rc - 1);
       float M = -INFINITY;
       for (int k = 0; k < copies; ++k)
         M = fmaxf(M, fmaxf(f.m[0][sub + rc * k], f.m[1][sub + rc * k]));
-      const float a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
-      for (int s = 1; s >= 0; --s) {
-        if (wg == s && busy) {
+      a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
+    }
 #pragma unroll 1
-          for (int k = 0; k < kHeadDim; k += 16) {
-            float o[16];
-            if (r.mine > 0) {
-              tc_ld16(oa + k, o);
-              tc_wait_ld();
-            }
+    for (int step = 0; step < 4; ++step) {
+      // one block: both streams' halves in turn, the second adds to the
+      // first's; two blocks: a block's halves in turn
+      const int hf = nb == 1 ? step >> 1 : step & 1, s = nb == 1 ? 1 - (step & 1) : step >> 1;
+      if (wg == s && busy) {
+#pragma unroll 1
+        for (int k = 0; k < 64; k += 16) {
+          float o[16];
+          if (r.mine > 0) {
+            tc_ld16(oa + 64 * hf + k, o);
+            tc_wait_ld();
+          }
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (a != 0.0f) x = make_float4(o[e] * a, o[e + 1] * a, o[e + 2] * a, o[e + 3] * a);
-              float4* to = reinterpret_cast<float4*>(mine + k + e);
-              if (s == 0) {
-                const float4 y = *to;
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
-              }
-              *to = x;
+          for (int e = 0; e < 16; e += 4) {
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (a != 0.0f) x = make_float4(o[e] * a, o[e + 1] * a, o[e + 2] * a, o[e + 3] * a);
+            float4* to = reinterpret_cast<float4*>(mine + k + e);
+            if (nb == 1 && s == 0) {
+              const float4 y = *to;
+              x.x += y.x;
+              x.y += y.y;
+              x.z += y.z;
+              x.w += y.w;
             }
+            *to = x;
           }
         }
-        if (s == 1) tc_fence_before();
-        if (!meet()) return;
+        tc_fence_before();
       }
-      for (int x = warp; x < R; x += kSoftWarps) {
+      if (!meet()) return;
+      if (nb == 1 && s == 1) continue;
+      const int l = lane & 15, top = nb == 1 ? R : min(128, R - 128 * s);
+      for (int x = 2 * warp + (lane >> 4); x < top; x += 2 * kSoftWarps) {
         float Mx = -INFINITY, Lx = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < copies; ++k)
-          Mx = fmaxf(Mx, fmaxf(f.m[0][x + rc * k], f.m[1][x + rc * k]));
         for (int k = 0; k < copies; ++k) {
-          const float* from = buf + (x + rc * k) * kBufRow + c0;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            // (a sum without a maximum: 0, or NaN where every score is NaN)
-            const float m = f.m[s][x + rc * k], l = f.l[s][x + rc * k];
-            if (l != 0.0f) Lx += m == -INFINITY ? l : l * ex2f(m - Mx);
-          }
+          const int z = x + rc * k;
+          const float* from = buf + z * kBufRow + 32 * (l & 1) + 2 * ((l >> 2) & 3) + ((l >> 1) & 1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += from[8 * e];
+          Mx = nb == 2 ? f.m[s][z] : fmaxf(Mx, fmaxf(f.m[0][z], f.m[1][z]));
         }
-        write_row<CAP, BIAS>(p, d, bad, x, Mx, Lx, v, lane);
-      }
-    } else {
-      for (int b = 0; b < 2; ++b) {
-        if (wg == b && busy) {
-#pragma unroll 1
-          for (int k = 0; k < kHeadDim; k += 16) {
-            float o[16];
-            tc_ld16(oa + k, o);
-            tc_wait_ld();
+        if (nb == 2) {
+          Lx = f.l[s][x];
+          if (Mx == -INFINITY) v[0] = v[1] = v[2] = v[3] = 0.0f;
+        } else {
+          for (int k = 0; k < copies; ++k) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(mine + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int y = 0; y < 2; ++y) {
+              // (a sum without a maximum: 0, or NaN where every score is NaN)
+              const float mz = f.m[y][x + rc * k], lz = f.l[y][x + rc * k];
+              if (lz != 0.0f) Lx += mz == -INFINITY ? lz : lz * ex2f(mz - Mx);
+            }
           }
         }
-        if (!meet()) return;
-        for (int x = warp; x < 128 && 128 * b + x < R; x += kSoftWarps) {
-          const float* from = buf + x * kBufRow + c0;
-          float v[4] = {from[0], from[8], from[16], from[24]};
-          const float Mx = f.m[b][x];
-          if (Mx == -INFINITY) v[0] = v[1] = v[2] = v[3] = 0.0f;
-          write_row<CAP, BIAS>(p, d, bad, 128 * b + x, Mx, f.l[b][x], v, lane);
-        }
-        if (!meet()) return;
+        write_row<CAP, BIAS>(p, d.unit, d.n, d.slot, bad, nb == 1 ? x : 128 * s + x, Mx, Lx, v,
+                             64 * hf + 4 * l, lane);
       }
+      if (step < 3 && !meet()) return;
     }
   }
 }
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  const uint32_t at = smem_u32(raw);
-  const uint32_t base = (at + 8191u) & ~8191u;
-  uint8_t* const mem = raw + (base - at);
-  Fixed& f = *reinterpret_cast<Fixed*>(mem + kAtFixed);
+  extern __shared__ __align__(128) uint8_t raw[];
+  Fixed& f = *reinterpret_cast<Fixed*>(raw);
+  const uint32_t at = smem_u32(raw), tbl = (at + kLowBytes + kTblBytes - 1) & ~(kTblBytes - 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tbl + kTblBytes + kStages * kStageBytes > at + kSmemBytes) {
+    // (the window starts at 1 KB: it fits)
+    if (tid == 0) report(p.err, SKV_ERR_CUDA);
+    return;
+  }
 
   if (tid == 0) {
     f.abort = 0;
     for (int k = 0; k < kStages; ++k) {
-      mbar_init(smem_u32(&f.full[k]), kTeamWarps);
-      mbar_init(smem_u32(&f.empty[k]), 1);
+      mbar_init(smem_u32(&f.kfull[k]), kTeamWarps);
+      mbar_init(smem_u32(&f.vfull[k]), kTeamWarps);
+      mbar_init(smem_u32(&f.kempty[k]), 1);
+      mbar_init(smem_u32(&f.vempty[k]), 1);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&f.sfull[k]), 1);
@@ -1273,51 +1016,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // the keys of the code words at radius 1 (share times cosine and sine), in
-  // fp16, 32 copies: copy L is read by lane L
-  for (int i = tid; i < 8 * (256 + 64); i += kThreads) {
-    const int e = i >> 3;
-    float cs, sn, w;
-    if (e < 256 && p.t1_scheme) {
-      cs = p.cos5[e >> 3];
-      sn = p.sin5[e >> 3];
-      w = (float)((e & 7) + 1) / 32.0f;
-    } else if (e < 256) {
-      cs = p.cos6[e >> 2];
-      sn = p.sin6[e >> 2];
-      w = p.rho[e & 3];
-    } else {
-      cs = p.cos4[(e - 256) & 15];
-      sn = p.sin4[(e - 256) & 15];
-      w = p.rho[(e - 256) >> 4];
-    }
-    const uint32_t h = pack_f16x2(w * cs, w * sn);
-    uint8_t* const to = mem + (e < 256 ? kAtTbl1 + 16 * i : kAtTbl2 + 16 * (i - 8 * 256));
-    *reinterpret_cast<uint4*>(to) = make_uint4(h, h, h, h);
-  }
+  key_tables(p, tbl, tid, kThreads);
   tc_fence_before();
-  const int S = find_start(p, f, blockIdx.x);   // (block-wide barriers)
+  find_run<kThreads>(p, blockIdx.x, f.scan, &f.run, RowsCost());  // (block-wide barriers)
   tc_fence_after();
   const uint32_t tm = *(volatile uint32_t*)&f.tmem;
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(mem + kAtBuf), tm, warp, lane);
+    softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(raw + kAtBuf), tm, warp, lane);
   } else if (warp < kPlanner) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
-    decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane);
+    decode_role<BIAS>(p, f, tbl, warp - kSoftWarps, lane);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
     if (warp == kPlanner) {
-      planner(p, f, blockIdx.x, S, lane);
+      planner(p, f, blockIdx.x, lane);
     } else if (warp == kMma) {
-      if (lane == 0) {
-        mma_role(p, f, base, tm);
-        // nothing in flight when tensor memory is given back
-        tc_commit(smem_u32(&f.fin));
-        int none = 0;
-        if (!mbar_wait_bounded(smem_u32(&f.fin), 0, &none)) report(p.err, SKV_ERR_TIMEOUT);
-      }
+      mma_role(p, f, tbl + kTblBytes, tm);
+      // nothing in flight when tensor memory is given back
+      if (elect_one()) tc_commit(smem_u32(&f.fin));
+      __syncwarp();
+      int none = 0;
+      if (!mbar_wait_bounded(smem_u32(&f.fin), 0, &none) && lane == 0) report(p.err, SKV_ERR_TIMEOUT);
       __syncwarp();
     }
   }
@@ -1431,7 +1152,9 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (p.softcap > 0.0f)
+  if (p.N * (p.Hq / p.Hkv) <= kTreeRows)
+    e = launch_tree_rows(p, stream);
+  else if (p.softcap > 0.0f)
     e = p.slopes ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   else
     e = p.slopes ? launch<false, true>(p, stream) : launch<false, false>(p, stream);

@@ -1,0 +1,661 @@
+// tree_rows.cu -- the tree attention for few rows: at most 32 (drafted
+// tokens times query heads) a kv head, single tokens among them.
+//
+// Every warp takes 16 tokens at a time and keeps everything in registers: the
+// keys are rebuilt from their codes by gathers from a replicated table and
+// enter mma.sync (m16n8k16, A = 16 keys, B = 8 rows of Q) as they come, the
+// weights are transposed between the products by movmatrix, and the values
+// (A = V^T, in the pages' fragment order) go from global memory through the
+// int8 -> fp16 conversion straight into the second product.  No barrier lies
+// between a warp's loads and its sums; the warps' sums meet once per segment
+// in shared memory.  Up to 8 rows a warp has one column block, up to 16 two;
+// with 17 to 32 rows two warps share the tokens, 16 rows each (the second
+// gather costs less than the products).
+//
+// The loads of a warp's next 16 tokens are issued as soon as the registers
+// of the present ones are free; pages are asked for in L2 some tiles ahead.
+#include <algorithm>
+
+#include "tree.cuh"
+
+namespace skv {
+
+namespace {
+
+using namespace tree;
+
+constexpr int kWindow = 2048;                  // pages whose entries are held at once
+constexpr int kAhead = 16 * kTile;             // tokens asked for in L2 ahead
+constexpr int kObufRow = kHeadDim + 4;         // floats
+constexpr uint32_t kRowsTbl = 65536;
+constexpr uint32_t kRowsSmem = 232448;
+
+template <int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 16 : 12;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRows = 8 * NT;         // rows of a warp
+  // cost of a tile by the rows: one or two warps take its tokens
+  struct Cost {
+    __device__ __forceinline__ int operator()(int rows) const {
+      return NT == 1 || rows <= kRows ? 2 : 4;
+    }
+  };
+};
+
+struct __align__(16) Entry {      // a page
+  unsigned long long page;
+  uint32_t tier, rows;            // 3: unusable
+};
+
+template <int NT>
+struct __align__(16) RowsFixed {
+  Entry page[kWindow];
+  unsigned long long scan[Shape<NT>::kWarps];
+  Run run;
+  Share share;
+  Unit unit;
+  int u;                          // the segment's unit, -1: no more
+  int bad[2];                     // a drafted value lies outside fp16 (segments in turn)
+  unsigned long long before;      // cost before unit u
+  float m[Shape<NT>::kWarps][Shape<NT>::kRows], l[Shape<NT>::kWarps][Shape<NT>::kRows];
+};
+
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Lane 4 g + t: rows g, g + 8 of the 16 tokens for keys; rows 2 t, 2 t + 1 of
+// both halves for values.
+struct Raw {
+  uint4 k[2], v[4];
+  uint32_t r[2], s[2];
+};
+
+__device__ __forceinline__ void raw_keys(const uint8_t* page, uint32_t tier, int at, int P, int g,
+                                         int t, Raw& o) {
+  const uint8_t* a = page + kHdrBytes;
+  if (tier == SKV_TIER_T1 || tier == SKV_TIER_T2) {
+    o.r[0] = *reinterpret_cast<const uint16_t*>(a + 2 * (at + g));
+    o.r[1] = *reinterpret_cast<const uint16_t*>(a + 2 * (at + g) + 16);
+    a += 2 * P;
+    if (tier == SKV_TIER_T1) {
+      a += 64 * (at + g) + 16 * t;
+      o.k[0] = ldg128(a);
+      o.k[1] = ldg128(a + 512);
+    } else {
+      a += 48 * (at + g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint2 n = *reinterpret_cast<const uint2*>(a + 384 * h + 8 * t);
+        o.k[h].x = n.x;
+        o.k[h].y = n.y;
+        o.k[h].z = *reinterpret_cast<const uint32_t*>(a + 384 * h + 32 + 4 * t);
+      }
+    }
+  }
+}
+__device__ __forceinline__ void raw_values(const uint8_t* page, uint32_t tier, int at, int P,
+                                           int t, int lane, Raw& o) {
+  if (tier == SKV_TIER_T1 || tier == SKV_TIER_T2) {
+    const uint8_t* a = page + kHdrBytes + (tier == SKV_TIER_T1 ? 66 : 50) * P;
+    o.s[0] = *reinterpret_cast<const uint32_t*>(a + 2 * at + 4 * t);
+    o.s[1] = *reinterpret_cast<const uint32_t*>(a + 2 * at + 4 * t + 16);
+    a += 2 * P + 128 * at + 16 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = ldg128(a + 512 * i);
+  }
+}
+
+template <int NT>
+struct Frag {
+  uint32_t q[NT][16];     // B fragments of the rows
+  float acc[NT][8][4];    // O^T: dims 16 mt + g (+ 8), rows 2 t, 2 t + 1
+  float m[NT][2], l[NT][2];
+};
+
+// S^T += keys (A: two registers a row) x rows for k-step s
+template <int NT>
+__device__ __forceinline__ void qk(float (&c)[NT][4], const Frag<NT>& f, int s, uint32_t a0,
+                                   uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    mma_16816k16_f16(c[n], a0, a1, a2, a3, f.q[n][2 * s], f.q[n][2 * s + 1]);
+}
+
+__device__ __forceinline__ uint32_t tbl1(uint32_t w, int k, uint32_t tb) {
+  return lds32(__byte_perm(w, tb, 0x7604u | (uint32_t)(k << 4)));
+}
+__device__ __forceinline__ uint32_t tbl2(const uint4& w, int j, uint32_t tb) {
+  const int sn = 4 * (j & 7) - 8, sc = 2 * j - 12;
+  const uint32_t nw = j < 8 ? w.x : w.y;
+  const uint32_t xn = sn >= 0 ? (nw >> sn) : (nw << -sn);
+  const uint32_t xc = sc >= 0 ? (w.z >> sc) : (w.z << -sc);
+  return lds32((xn & 0xF00u) | (xc & 0x3000u) | tb);
+}
+
+// What a warp knows of its rows' scores (columns 2 t, 2 t + 1 of block n).
+template <int NT>
+struct Score {
+  float c[NT][2];         // what a product is scaled by (log2 domain, before the cap)
+  float cap;
+  float slope[NT][2], rel[NT][2];
+};
+
+// Scores to weights: c holds the products of tokens g, g + 8, rA / rB what
+// the keys are scaled by; bit 4 n + e of `see`: the score counts.  The
+// weights leave as B fragments (fp16; sums are taken before the rounding).
+template <int NT, bool CAP, bool BIAS>
+__device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float (&c)[NT][4],
+                                        float rA, float rB, float posA, float posB, uint32_t see,
+                                        uint32_t (&b)[NT][2]) {
+  constexpr uint32_t kAll = (1u << (4 * NT)) - 1;
+  bool raise = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = e & 1;
+      float x = c[n][e] * (e < 2 ? rA : rB) * sc.c[n][j];
+      if (CAP) x = fmaf(-2.0f * sc.cap, rcpf(1.0f + ex2f(x)), sc.cap);
+      if (BIAS) x = fmaf(sc.slope[n][j], (e < 2 ? posA : posB) - sc.rel[n][j], x);
+      c[n][e] = x;
+    }
+  }
+  if (see != kAll) {
+#pragma unroll
+    for (int k = 0; k < 4 * NT; ++k)
+      if (!((see >> k) & 1)) c[k >> 2][k & 3] = -INFINITY;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) raise |= fmaxf(c[n][j], c[n][j + 2]) > f.m[n][j] + kRaise;
+  if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float a[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = fmaxf(c[n][j], c[n][j + 2]);
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+        x = x > f.m[n][j] + kRaise ? x : f.m[n][j];
+        a[j] = x == f.m[n][j] ? 1.0f : ex2f(f.m[n][j] - x);
+        f.m[n][j] = x;
+        f.l[n][j] *= a[j];
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        f.acc[n][mt][0] *= a[0];
+        f.acc[n][mt][1] *= a[1];
+        f.acc[n][mt][2] *= a[0];
+        f.acc[n][mt][3] *= a[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float m0 = f.m[n][0] == -INFINITY ? 0.0f : f.m[n][0];
+    const float m1 = f.m[n][1] == -INFINITY ? 0.0f : f.m[n][1];
+    const float w0 = ex2f(c[n][0] - m0), w1 = ex2f(c[n][1] - m1);
+    const float w2 = ex2f(c[n][2] - m0), w3 = ex2f(c[n][3] - m1);
+    f.l[n][0] += w0 + w2;
+    f.l[n][1] += w1 + w3;
+    b[n][0] = transposed(pack_f16x2(w0, w1));
+    b[n][1] = transposed(pack_f16x2(w2, w3));
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ void pv(Frag<NT>& f, int mt, uint32_t a0, uint32_t a1, uint32_t a2,
+                                   uint32_t a3, const uint32_t (&b)[NT][2]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_16816k16_f16(f.acc[n][mt], a0, a1, a2, a3, b[n][0], b[n][1]);
+}
+
+// both halves of a mask of rows 2 t, 2 t + 1 that lie below `rows`
+__device__ __forceinline__ uint32_t pair_mask(int row, int rows) {
+  return (row < rows ? 0xFFFFu : 0u) | (row + 1 < rows ? 0xFFFF0000u : 0u);
+}
+
+// int8 values (two words of a tile row) to fp16, times the rows' scales: v + 128
+// as the low byte of 1024 + x, less 1152 (exact), then one rounding
+__device__ __forceinline__ uint32_t scaled(uint32_t u, uint32_t sel, uint32_t s) {
+  const uint32_t x = __byte_perm(u, 0x64646464u, sel);
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+  return hmul2(*reinterpret_cast<const uint32_t*>(&h), s);
+}
+
+// A value of a drafted token: 0 when fp16 does not hold it (added by
+// write_row) or the token is not there.
+__device__ __forceinline__ float draft_value(const TreeParams& p, long long at, bool live, bool& out) {
+  float y = 0.0f;
+  if (live) y = from16(static_cast<const uint16_t*>(p.V)[at], p.kv_bf16);
+  if (!(fabsf(y) <= 65504.0f)) {
+    y = 0.0f;
+    out = true;
+  }
+  return y;
+}
+
+// 16 drafted tokens from j0 on.
+template <int NT, bool CAP, bool BIAS>
+__device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, const Score<NT>& sc,
+                                             int b, int h, int n, int j0, int row0, int R, int G,
+                                             int q0, int lane, int* bad) {
+  const int g = lane >> 2, t = lane & 3;
+  const long long tok0 = (long long)b * p.N, off = (long long)h * kHeadDim;
+  const uint16_t* K = static_cast<const uint16_t*>(p.K);
+  float c[NT][4] = {}, up[2], down[2], pos[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int j = j0 + g + 8 * y;
+    uint32_t mx = 0;
+    if (j < n) {
+      const uint16_t* k = K + (tok0 + j) * p.kv_stride + off + 8 * t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(k + 32 * i);
+        mx = max_bits(max_bits(max_bits(max_bits(mx, x.x), x.y), x.z), x.w);
+      }
+      if (BIAS) pos[y] = (float)(p.q_pos[tok0 + j] - q0);
+    }
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+    const int e = scale_exp(mx, p.kv_bf16);
+    up[y] = pow2i(e);
+    down[y] = pow2i(-e);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a[2][4];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int j = j0 + g + 8 * y;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (j < n)
+        x = *reinterpret_cast<const uint4*>(K + (tok0 + j) * p.kv_stride + off + 8 * t + 32 * i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 z = from16x2(w[k], p.kv_bf16);
+        a[y][k] = pack_f16x2(z.x * up[y], z.y * up[y]);
+      }
+    }
+    qk<NT>(c, f, 2 * i, a[0][0], a[1][0], a[0][1], a[1][1]);
+    qk<NT>(c, f, 2 * i + 1, a[0][2], a[1][2], a[0][3], a[1][3]);
+  }
+  uint32_t see = 0, w[NT][2];
+#pragma unroll
+  for (int e = 0; e < 4 * NT; ++e) {
+    const int r = row0 + 8 * (e >> 2) + 2 * t + (e & 1), j = j0 + g + 8 * ((e >> 1) & 1);
+    if (r < R && j < n) {
+      const int i = r / G;
+      if (p.mask ? (p.mask[tok0 + i] >> j) & 1 : j <= i) see |= 1u << e;
+    }
+  }
+  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], pos[0], pos[1], see, w);
+  bool out = false;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    uint32_t a[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + 2 * t + 8 * (k >> 1);
+      const long long at = (tok0 + j) * p.kv_stride + off + 16 * mt + 8 * (k & 1) + g;
+      const float x = draft_value(p, at, j < n, out);
+      const float y = draft_value(p, at + p.kv_stride, j + 1 < n, out);
+      a[k] = pack_f16x2(x, y);
+    }
+    pv<NT>(f, mt, a[0], a[1], a[2], a[3], w);
+  }
+  if (out) *(volatile int*)bad = 1;
+}
+
+template <int NT, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
+    tree_rows_kernel(const __grid_constant__ TreeParams p) {
+  using S = Shape<NT>;
+  using Fixed = RowsFixed<NT>;
+  static_assert(sizeof(Fixed) + 1024 <= kRowsTbl, "the tables start at 64 KB");
+  extern __shared__ __align__(128) uint8_t raw[];
+  Fixed& f = *reinterpret_cast<Fixed*>(raw);
+  const uint32_t base = smem_u32(raw);
+  const uint32_t tbl = (base + (uint32_t)sizeof(Fixed) + kRowsTbl - 1) & ~(kRowsTbl - 1);
+  constexpr uint32_t kObuf = S::kWarps * S::kRows * kObufRow * 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  if (tbl + kRowsTbl + kObuf > base + kRowsSmem) {
+    // (the window starts at 1 KB: it fits)
+    if (tid == 0) report(p.err, SKV_ERR_CUDA);
+    return;
+  }
+  float* const obuf = reinterpret_cast<float*>(raw + (tbl + kRowsTbl - base));
+  key_tables(p, tbl, tid, S::kThreads);
+  const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kTile / P;
+  const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
+  const uint32_t tb = tbl + 4 * lane;
+  find_run<S::kThreads>(p, c, f.scan, &f.run, typename S::Cost());
+  // the next unit with a part in this run, by one thread
+  const auto open = [&](int u, unsigned long long cc) {
+    const int U = p.B * p.Hkv;
+    f.u = -1;
+    while (u < U && cc < f.run.to) {
+      f.unit = unit_of(p, u, typename S::Cost());
+      if (part_of(p, f.unit, f.run, c, cc, f.share)) {
+        f.u = u;
+        f.before = cc;
+        if (f.share.starts) p.join[c] = make_int2(u, f.share.last);
+        return;
+      }
+      cc += f.unit.cost;
+      ++u;
+    }
+  };
+  if (tid == 0) {
+    p.join[c] = make_int2(-1, 0);
+    f.bad[0] = f.bad[1] = 0;
+    open(f.run.unit, f.run.before);
+  }
+  __syncthreads();
+
+  for (int seg = 0;; seg ^= 1) {
+    const int u = f.u;
+    if (u < 0) break;
+    const int n = f.unit.n, slot = f.share.slot, R = n * G;
+    const int b = u / p.Hkv, h = u - b * p.Hkv;
+    const int blocks = R > S::kRows ? 2 : 1;      // (at most 2 S::kRows rows)
+    const int streams = S::kWarps / blocks;
+    const int stream = blocks == 2 ? warp >> 1 : warp;
+    const int row0 = blocks == 2 ? S::kRows * (warp & 1) : 0;
+    const long long first = f.unit.first + (long long)f.share.k * ipp;
+    const int pages = max(0, min(f.share.kend * ipp, f.unit.np) - f.share.k * ipp);
+    const int dparts = f.share.draft ? (n + 15) >> 4 : 0;
+    const long long tok0 = (long long)b * p.N;
+    const int q0 = BIAS ? p.q_pos[tok0] : 0;
+
+    // the rows as B fragments: fp16 scaled by a power of two a row
+    Frag<NT> fr;
+    Score<NT> sc;
+    sc.cap = p.softcap * 1.4426950408889634f;
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+      const int r = row0 + 8 * k + g, i = r / G;
+      uint4 x[4];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        x[y] = make_uint4(0, 0, 0, 0);
+        if (r < R)
+          x[y] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                 (tok0 + i) * p.q_stride +
+                                                 (long long)(h * G + r - i * G) * kHeadDim +
+                                                 32 * y + 8 * t);
+        mx = max_bits(max_bits(max_bits(max_bits(mx, x[y].x), x[y].y), x[y].z), x[y].w);
+      }
+      mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      const int e = scale_exp(mx, p.q_bf16);
+      const float up = pow2i(e);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float2 a = from16x2(w[v], p.q_bf16);
+          fr.q[k][4 * y + v] = pack_f16x2(a.x * up, a.y * up);
+        }
+      }
+      // of the lane's two score columns
+      const float scale = p.qk_scale * pow2i(-e) * 1.4426950408889634f *
+                          (CAP ? 2.0f / sc.cap * 1.4426950408889634f : 1.0f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sc.c[k][j] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4 * j);
+        fr.m[k][j] = -INFINITY;
+        fr.l[k][j] = 0.0f;
+        sc.slope[k][j] = sc.rel[k][j] = 0.0f;
+        const int rr = row0 + 8 * k + 2 * t + j;
+        if (BIAS && rr < R) {
+          const int ii = rr / G;
+          sc.slope[k][j] = p.slopes[h * G + rr - ii * G] * 1.4426950408889634f;
+          sc.rel[k][j] = (float)(p.q_pos[tok0 + ii] - q0);
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+        fr.acc[k][mt][0] = fr.acc[k][mt][1] = fr.acc[k][mt][2] = fr.acc[k][mt][3] = 0.0f;
+    }
+
+    for (int w0 = 0; w0 < pages || w0 == 0; w0 += kWindow) {
+      const int held = min(kWindow, pages - w0);
+      const int ahead = kAhead / P;
+      if (w0 > 0) __syncthreads();
+      for (int k = tid; k < held; k += S::kThreads) {
+        const uint32_t id = p.ids[first + w0 + k], sl = id & 0x3FFFFFFFu;
+        const int ti = (int)(id >> 30);
+        Entry e = {0, 3, 0};
+        if (ti > 2 || (long long)sl >= p.slots[ti]) {
+          report(p.err, SKV_ERR_CORRUPT);
+        } else {
+          const uint8_t* a = p.pool[ti] + (long long)sl * p.stride[ti];
+          if (k < ahead) prefetch_page(a, P, ti);
+          const uint32_t hd = *reinterpret_cast<const uint32_t*>(a);
+          const uint32_t rows = hd & 0xFFFFu;
+          if ((hd >> 16) != ((uint32_t)ti | ((uint32_t)kPageMagic << 8)) || rows > (uint32_t)P) {
+            report(p.err, SKV_ERR_CORRUPT);
+          } else {
+            e.page = reinterpret_cast<unsigned long long>(a);
+            e.tier = (uint32_t)ti;
+            e.rows = rows;
+          }
+        }
+        f.page[k] = e;
+      }
+      __syncthreads();
+      const int store = held << lgp;
+      const int total = store + (w0 + kWindow >= pages ? dparts : 0);
+      Raw o;
+      o.r[0] = o.r[1] = o.s[0] = o.s[1] = 0;
+      const uint8_t* page = nullptr;
+      uint32_t tier = 3;
+      int rows = 0, at = 0;
+      const auto look = [&](int q) {
+        tier = 3;
+        rows = 0;
+        if (q < store) {
+          const Entry e = f.page[q >> lgp];
+          at = 16 * (q & (ppp - 1));
+          page = reinterpret_cast<const uint8_t*>(e.page);
+          rows = min((int)e.rows - at, 16);
+          tier = rows > 0 ? e.tier : 3u;
+        }
+      };
+      look(stream);
+      raw_keys(page, tier, at, P, g, t, o);
+      raw_values(page, tier, at, P, t, lane, o);
+      for (int q = stream; q < total; q += streams) {
+        if (q >= store) {
+          draft_tokens<NT, CAP, BIAS>(p, fr, sc, b, h, n, 16 * (q - store), row0, R, G, q0, lane,
+                                      &f.bad[seg]);
+          continue;
+        }
+        const uint8_t* const pg = page;
+        const uint32_t ti = tier;
+        const int nr = rows, a0 = at;
+        if (row0 == 0 && lane == 0 && a0 == 0) {
+          const int k = (q >> lgp) + ahead;
+          if (k < held && f.page[k].tier < 3)
+            prefetch_page(reinterpret_cast<const uint8_t*>(f.page[k].page), P, (int)f.page[k].tier);
+        }
+        if (ti == 3) {
+          look(q + streams);
+          raw_keys(page, tier, at, P, g, t, o);
+          raw_values(page, tier, at, P, t, lane, o);
+          continue;
+        }
+        float cc[NT][4] = {}, cd[NT][4] = {};
+        float rA = 1.0f, rB = 1.0f, posA = 0.0f, posB = 0.0f;
+        if (BIAS) {
+          const int32_t* at_pos = p.row_pos + (first + w0 + (q >> lgp)) * P + a0;
+          if (g < nr) posA = (float)(at_pos[g] - q0);
+          if (g + 8 < nr) posB = (float)(at_pos[g + 8] - q0);
+        }
+        if (ti == SKV_TIER_T1) {
+          const uint32_t wa[4] = {o.k[0].x, o.k[0].y, o.k[0].z, o.k[0].w};
+          const uint32_t wb[4] = {o.k[1].x, o.k[1].y, o.k[1].z, o.k[1].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qk<NT>(cc, fr, 2 * i, tbl1(wa[i], 0, tb), tbl1(wb[i], 0, tb), tbl1(wa[i], 1, tb),
+                   tbl1(wb[i], 1, tb));
+            qk<NT>(cd, fr, 2 * i + 1, tbl1(wa[i], 2, tb), tbl1(wb[i], 2, tb), tbl1(wa[i], 3, tb),
+                   tbl1(wb[i], 3, tb));
+          }
+        } else if (ti == SKV_TIER_T2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qk<NT>(cc, fr, 2 * i, tbl2(o.k[0], 4 * i, tb + 128), tbl2(o.k[1], 4 * i, tb + 128),
+                   tbl2(o.k[0], 4 * i + 1, tb + 128), tbl2(o.k[1], 4 * i + 1, tb + 128));
+            qk<NT>(cd, fr, 2 * i + 1, tbl2(o.k[0], 4 * i + 2, tb + 128),
+                   tbl2(o.k[1], 4 * i + 2, tb + 128), tbl2(o.k[0], 4 * i + 3, tb + 128),
+                   tbl2(o.k[1], 4 * i + 3, tb + 128));
+          }
+        } else {
+          const uint8_t* a = pg + kHdrBytes + 256 * (a0 + g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int ch = 16 * ((4 * i + t) ^ (4 * (g & 1)));
+            const uint4 x = ldg128(a + ch), y = ldg128(a + 2048 + ch);
+            qk<NT>(cc, fr, 2 * i, x.x, y.x, x.y, y.y);
+            qk<NT>(cd, fr, 2 * i + 1, x.z, y.z, x.w, y.w);
+          }
+        }
+        if (ti != SKV_TIER_T0) {
+          rA = __half2float(__ushort_as_half((uint16_t)o.r[0]));
+          rB = __half2float(__ushort_as_half((uint16_t)o.r[1]));
+        }
+        look(q + streams);
+        raw_keys(page, tier, at, P, g, t, o);
+        uint32_t see = ~0u, w[NT][2];
+        if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
+        see &= (1u << (4 * NT)) - 1;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) cc[k][e] += cd[k][e];
+        weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, posA, posB, see, w);
+        const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
+        if (ti != SKV_TIER_T0) {
+          const uint32_t s0 = o.s[0] & m0, s1 = o.s[1] & m1;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t va[4] = {o.v[y].x, o.v[y].y, o.v[y].z, o.v[y].w};
+            const uint32_t vb[4] = {o.v[y + 2].x, o.v[y + 2].y, o.v[y + 2].z, o.v[y + 2].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ua = va[k] ^ 0x80808080u, ub = vb[k] ^ 0x80808080u;
+              pv<NT>(fr, 4 * y + k, scaled(ua, 0x4140, s0), scaled(ua, 0x4342, s0),
+                     scaled(ub, 0x4140, s1), scaled(ub, 0x4342, s1), w);
+            }
+          }
+        } else {
+          const uint8_t* a = pg + kHdrBytes + 256 * (P + a0) + 16 * lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 x = ldg128(a + 512 * k), y = ldg128(a + 2048 + 512 * k);
+            pv<NT>(fr, 2 * k, x.x & m0, x.y & m0, y.x & m1, y.y & m1, w);
+            pv<NT>(fr, 2 * k + 1, x.z & m0, x.w & m0, y.z & m1, y.w & m1, w);
+          }
+        }
+        raw_values(page, tier, at, P, t, lane, o);
+      }
+    }
+
+    // the warps' sums meet
+#pragma unroll
+    for (int k = 0; k < NT; ++k) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float l = fr.l[k][j];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        if (g == 0) {
+          f.m[warp][8 * k + 2 * t + j] = fr.m[k][j];
+          f.l[warp][8 * k + 2 * t + j] = l;
+        }
+        float* to = obuf + (warp * S::kRows + 8 * k + 2 * t + j) * kObufRow + g;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          to[16 * mt] = fr.acc[k][mt][j];
+          to[16 * mt + 8] = fr.acc[k][mt][j + 2];
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == S::kThreads - 1) {
+      f.bad[seg ^ 1] = 0;
+      open(u + 1, f.before + f.unit.cost);
+    }
+    const bool bad = *(volatile int*)&f.bad[seg] != 0;
+    for (int r = warp; r < R; r += S::kWarps) {
+      const int blk = r >= S::kRows ? 1 : 0, lr = r - S::kRows * blk;
+      float m = -INFINITY, l = 0.0f;
+      if (lane < streams) {
+        const int w = blocks * lane + blk;
+        m = f.m[w][lr];
+        l = f.l[w][lr];
+      }
+      float M = m;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+      const float a = m == -INFINITY ? 0.0f : ex2f(m - M);
+      // (a sum without a maximum: 0, or NaN where every score is NaN)
+      float L = m == -INFINITY ? l : l * a;
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int k = 0; k < streams; ++k) {
+        const float ak = __shfl_sync(0xFFFFFFFFu, a, k);
+        const float4 x = *reinterpret_cast<const float4*>(
+            obuf + ((blocks * k + blk) * S::kRows + lr) * kObufRow + 4 * lane);
+        v[0] += ak * x.x;
+        v[1] += ak * x.y;
+        v[2] += ak * x.z;
+        v[3] += ak * x.w;
+      }
+      write_row<CAP, BIAS>(p, u, n, slot, bad, r, M, L, v, 4 * lane, lane);
+    }
+    __syncthreads();
+  }
+}
+
+template <int NT, bool CAP, bool BIAS>
+cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(tree_rows_kernel<NT, CAP, BIAS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kRowsSmem);
+  if (e != cudaSuccess) return e;
+  tree_rows_kernel<NT, CAP, BIAS>
+      <<<(unsigned)p.S, Shape<NT>::kThreads, kRowsSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t launch_score(const TreeParams& p, cudaStream_t stream) {
+  if (p.softcap > 0.0f)
+    return p.slopes ? launch<NT, true, true>(p, stream) : launch<NT, true, false>(p, stream);
+  return p.slopes ? launch<NT, false, true>(p, stream) : launch<NT, false, false>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t stream) {
+  return p.N * (p.Hq / p.Hkv) <= 8 ? launch_score<1>(p, stream) : launch_score<2>(p, stream);
+}
+
+}  // namespace skv
