@@ -7,35 +7,40 @@
 //
 // Work split: the page list is cut into runs of about equal cost, one per
 // CTA; a run is a list of segments (a unit = (sequence, kv head), or a part
-// of one), a segment a list of tiles of 64 tokens (64 / P pages), the unit's
-// drafted tokens being one more tile behind its pages.  A unit that lies in
-// one run is finished there; the parts of a unit that several runs share go
-// to the workspace as (m, l, O) and a second grid joins them.
+// of one), a segment a list of tiles of 128 tokens (128 / P pages), the
+// unit's drafted tokens being one more tile behind its pages.  A unit that
+// lies in one run is finished there; the parts of a unit that several runs
+// share go to the workspace as (m, l, O) and a second grid joins them.
 //
 // Roles of a CTA (one per SM):
-//   planner (1 warp)   turns the page list into tile descriptors (a ring of 32
+//   planner (1 warp)   turns the page list into tile descriptors (a ring of 16
 //                      in shared memory), checks ids and headers, and asks for
 //                      the pages' bytes in L2 (bulk prefetch)
-//   decode (12 warps)  three teams of 4 take the tiles in turn, a warp 16 rows
-//                      in two steps of 8: codes to fp16 keys by gathers from a
+//   decode (8 warps)   two teams of 4 take the tiles in turn, a warp 32 rows
+//                      in steps of 8: codes to fp16 keys by gathers from a
 //                      replicated table (one conflict-free wavefront a
 //                      gather), int8 values to fp16, both written as swizzled
-//                      operand tiles (32 KB a tile, three in flight).  The
-//                      loads of the next 8 rows are issued as soon as the
+//                      operand tiles (64 KB a tile, two in flight).  The loads
+//                      of the rows 16 further on are issued as soon as the
 //                      registers of the present ones are free
-//   mma (1 warp)       S = Q K^T and O += P V by tcgen05.mma (fp16, fp32
-//                      accumulators); Q and P are read from tensor memory, so
-//                      that shared memory feeds K and V only
+//   mma (2 warps)      S = Q K^T, and O += P V, by tcgen05.mma (fp16, fp32
+//                      accumulators), 64 tokens a job; Q and P are read from
+//                      tensor memory, so that shared memory feeds K and V only
 //   softmax (8 warps)  two groups of 4, one per stream: scores from tensor
 //                      memory, running maximum and sum, weights back as fp16
 //
-// The two streams have accumulators of their own.  With at most 128 rows they
-// take alternate tiles, and with at most 64 (32) rows the rows are entered 2
-// (4) times, each copy handling its part of a tile's columns: every lane of
+// The two streams have accumulators of their own.  With at most 128 rows each
+// takes one half of every tile, and with at most 64 rows the rows are
+// entered twice, each copy handling half of a job's columns: every lane of
 // tensor memory then has work, and the copies' sums meet at the segment's
-// end.  With more than 128 rows stream b has the rows 128 b .. 128 b + 127 of
-// every tile.  The running maximum is raised (and O rescaled) only when a
-// score passes it by more than 2^8, so weights stay within fp16.
+// end.  With more than 128 rows stream b has the rows
+// 128 b .. 128 b + 127 of both halves.  The running maximum is raised (and O
+// rescaled) only when a score passes it by more than 2^8, so weights stay
+// within fp16.
+//
+// What costs here is not the products but the instructions around them: the
+// roles' loops are kept short (32 columns of softmax at a time), since straight-line code for four roles starves the
+// schedulers of instructions.
 //
 // Tensor memory (512 columns): Q 0-63 (and 64-127 for the second block), P of
 // the streams at 64 and 96 (over S with two blocks), S at 128 and 192, O at
@@ -51,21 +56,18 @@ namespace {
 
 using namespace tree;
 
-constexpr int kStages = 3;           // tiles of keys and values in flight, one a team
-constexpr int kRing = 32;            // tile descriptors
-constexpr int kBatch = 8;            // tiles the planner publishes at once
-constexpr int kTeamWarps = 4;        // decode warps of a team (16 rows each)
+constexpr int kTile = 128;           // tokens of a tile
+constexpr int kJob = 64;             // tokens of a job (a tile's half)
+constexpr int kStages = 2;           // tiles of keys and values in flight, one a team
+constexpr int kRing = 16;            // tile descriptors
+constexpr int kBatch = 4;            // tiles the planner publishes at once
+constexpr int kTeamWarps = 4;        // decode warps of a team (32 rows each)
 constexpr int kSoftWarps = 8;
 constexpr int kDecodeWarps = kStages * kTeamWarps;
 constexpr int kPlanner = kSoftWarps + kDecodeWarps;
-constexpr int kMma = kPlanner + 1;
+constexpr int kMmaS = kPlanner + 1, kMmaO = kPlanner + 2;
 constexpr int kThreads = (kSoftWarps + kDecodeWarps + 4) * 32;
-// registers a thread: softmax, decode, planner / mma; their sum over the
-// threads is what the block is launched with (768 x 80)
-constexpr int kRegsSoft = 112, kRegsDecode = 64, kRegsHelp = 64;
-static_assert(32 * (kSoftWarps * kRegsSoft + kDecodeWarps * kRegsDecode + 4 * kRegsHelp) <=
-                  kThreads * 80, "registers");
-constexpr int kBufRow = 68;          // floats of a row of the output buffer (64 dims)
+constexpr int kBufRow = 36;          // floats of a row of the output buffer (32 dims)
 
 enum : uint32_t { kFirst = 1, kLast = 2, kDraft = 4, kEnd = 8 };
 
@@ -79,8 +81,8 @@ struct __align__(16) Part {     // 16 rows of a tile
 };
 
 struct __align__(16) Tile {
-  Part part[4];
-  unsigned long long valid;     // bit c: column c holds a token
+  Part part[8];
+  unsigned long long valid[2];  // of the halves: bit c: column c holds a token
   int unit, n;                  // (sequence, kv head) and its drafted tokens
   uint32_t flags;
   int first;                    // index of the first page in the page list
@@ -90,8 +92,8 @@ struct __align__(16) Tile {
 
 struct __align__(16) Fixed {
   unsigned long long kfull[kStages], vfull[kStages], kempty[kStages], vempty[kStages];
-  unsigned long long sfull[2], pfull[2], odone[2];
-  unsigned long long qfull, sync, fin;
+  unsigned long long sfull[2], sfree[2], pfull[2], odone[2];
+  unsigned long long qfull, sync, fin[2];
   unsigned long long dfull[kRing / kBatch], rfree[kRing / kBatch];
   unsigned long long scan[kThreads / 32];
   Run run;
@@ -103,17 +105,21 @@ struct __align__(16) Fixed {
   float m[2][128], l[2][128];
 };
 
-// Shared memory: [fixed block, output buffer][tables][stages].  The tables
-// start on a 64 KB boundary: entry e of T1's (the code byte) is at 256 e, in
-// 32 copies of 4 bytes, so that one byte permutation forms a gather's
-// address; T2's entries (angle | share << 4) fill the other halves.
+// Shared memory: [fixed block, output buffer][keys 0][tables][values 0, keys 1,
+// values 1]; the tables start on a 64 KB boundary.
 constexpr uint32_t kTblBytes = 65536;
-constexpr uint32_t kStageBytes = 2 * kTile * 256;         // keys, values
+constexpr uint32_t kOperand = kTile * 256;                // a tile's keys or values
 constexpr uint32_t kBufBytes = 128 * kBufRow * 4;
 constexpr uint32_t kAtBuf = (sizeof(Fixed) + 127) / 128 * 128;
-constexpr uint32_t kLowBytes = kAtBuf + kBufBytes;
+constexpr uint32_t kLowBytes = kAtBuf + kBufBytes + kOperand;
 constexpr uint32_t kSmemBytes = 232448;
 static_assert(kLowBytes + 1024 <= 65536, "the tables start at 64 KB");
+__device__ __forceinline__ uint32_t keys_at(uint32_t tbl, uint32_t stage) {
+  return stage == 0 ? tbl - kOperand : tbl + kTblBytes + kOperand;
+}
+__device__ __forceinline__ uint32_t values_at(uint32_t tbl, uint32_t stage) {
+  return tbl + kTblBytes + (stage == 0 ? 0 : 2 * kOperand);
+}
 
 // ------------------------------------------------------------ tensor memory
 __device__ __forceinline__ void tc_fence_before() {
@@ -146,6 +152,13 @@ __device__ __forceinline__ void tc_ld16(uint32_t a, float* x) {
       : "r"(a)
       : "memory");
 }
+__device__ __forceinline__ void tc_ld8(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(a)
+               : "memory");
+}
 __device__ __forceinline__ void tc_st8(uint32_t a, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a),
@@ -164,28 +177,37 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, unsigned long lon
 }
 
 // fp16 A and B, fp32 D, M = 128; B's values contiguous along k, or along n
-constexpr uint32_t kIdescS = (1u << 4) | ((kTile / 8) << 17) | (8u << 24);
+constexpr uint32_t kIdescS = (1u << 4) | ((kJob / 8) << 17) | (8u << 24);
 constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((kHeadDim / 8) << 17) | (8u << 24);
 
 // Operand tiles in shared memory: rows of 128 bytes, their 16-byte chunks
 // permuted by the row's low three bits (128-byte swizzle), groups of 8 rows
-// 1024 bytes apart; the second 64 dims follow 8 KB behind.
+// 1024 bytes apart; the second 64 dims follow 16 KB behind.
+constexpr uint32_t kHalfDims = kTile * 128;   // from dims 0-63 of a tile to dims 64-127
 constexpr uint32_t kDescHigh = (1024 / 16) | (1u << 14) | (2u << 29);
-constexpr uint32_t kDescKeys = 1u << 16, kDescValues = (8192u / 16) << 16;
+constexpr uint32_t kDescKeys = 1u << 16, kDescValues = (kHalfDims / 16) << 16;
 __device__ __forceinline__ unsigned long long operand(uint32_t low) {
   return ((unsigned long long)kDescHigh << 32) | low;
 }
 
-// A bounded wait of a whole warp: false for all lanes when one gave up.
+// A bounded wait of a whole warp (about 1 s): false for all lanes when one
+// gave up.
 __device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
                                           int32_t* err) {
-  bool done = mbar_wait_bounded(smem_u32(&bar), parity, &f.abort);
-  done = __all_sync(0xFFFFFFFFu, done);
-  if (!done && (threadIdx.x & 31) == 0 && !*(volatile int*)&f.abort) {
-    *(volatile int*)&f.abort = 1;
-    report(err, SKV_ERR_TIMEOUT);
+  const uint32_t a = smem_u32(&bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_test_wait(a, parity))) return true;
+  const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+  while (!__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(a, parity, 200000u))) {
+    const bool late = (uint32_t)clock() - t0 > 2000000000u;
+    if (!__any_sync(0xFFFFFFFFu, late || *(volatile int*)&f.abort)) continue;
+    if ((threadIdx.x & 31) == 0 && !*(volatile int*)&f.abort) {
+      *(volatile int*)&f.abort = 1;
+      report(err, SKV_ERR_TIMEOUT);
+    }
+    return false;
   }
-  return done;
+  return true;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -201,13 +223,15 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
 
 // More than 128 rows cost half as much again (decoded once, multiplied twice).
 struct RowsCost {
+  static constexpr int kTile = 128;
   __device__ __forceinline__ int operator()(int rows) const { return rows > 128 ? 3 : 2; }
 };
+static_assert(RowsCost::kTile == kTile, "tiles");
 
 // ---------------------------------------------------------------- the planner
 __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int lane) {
   const int U = p.B * p.Hkv, ipp = kTile / p.P, lgP = __ffs(p.P) - 1;
-  const int mine = lane >> 2, part = lane & 3;      // the lane's tile of a batch, its 16 rows
+  const int mine = lane >> 3, part = lane & 7;      // the lane's tile of a batch, its 16 rows
   const int pg = 16 * part >> lgP, at = 16 * part & (p.P - 1);
   const Run run = f.run;
   int u = run.unit, k = 0, kend = 0, slot = -1, ends = 0;
@@ -229,7 +253,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
       while (!open && u < U && cc < run.to) {
         x = unit_of(p, u, RowsCost());
         Share y;
-        if (part_of(p, x, run, c, cc, y)) {
+        if (share_of(p, x, run, c, cc, ipp, y)) {
           k = y.k;
           kend = y.kend;
           draft = y.draft;
@@ -299,13 +323,16 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
         }
       }
     }
-    unsigned long long valid = (unsigned long long)((1u << o.rows) - 1) << (16 * part);
+    unsigned long long valid = (unsigned long long)((1u << o.rows) - 1) << (16 * (part & 3));
     valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 1);
     valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 2);
     Tile& d = f.ring[(batch & 3) * kBatch + mine];
     d.part[part] = o;
+    if ((part & 3) == 0) {
+      if (t_flags & kDraft) valid = part ? 0ull : (t_n >= 64 ? ~0ull : (1ull << t_n) - 1);
+      d.valid[part >> 2] = valid;
+    }
     if (part == 0) {
-      d.valid = (t_flags & kDraft) ? (t_n >= 64 ? ~0ull : (1ull << t_n) - 1) : valid;
       d.unit = t_unit;
       d.n = t_n;
       d.flags = t_flags;
@@ -320,48 +347,50 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
 
 // ----------------------------------------------------------------- the decode
 // Lane (t, g) = 4 t + g of a warp: row t of its 8, key dims 32 i + 8 g + 0..7.
+// A part's 16 rows in registers (dense rows are loaded when they are used).
 struct Rows {
-  uint4 k[4], v[4];
-  uint32_t r, s;     // radius; scales of value rows 2 t4, 2 t4 + 1
+  uint4 k[2], v[4];
+  uint32_t r[2], s[2];   // radius; scales of value rows 2 t4, 2 t4 + 1
+  const uint8_t* page;   // behind the header
+  uint32_t tier;
+  int at, rows;
 };
 
-__device__ __forceinline__ void load_keys(const uint8_t* page, uint32_t tier, int at, int P,
-                                          int lane, Rows& o) {
+__device__ __forceinline__ void load_part(const Part& x, int P, int lane, Rows& o) {
   const int t = lane >> 2, g = lane & 3;
-  const uint8_t* a = page + kHdrBytes;
-  if (tier == SKV_TIER_T0) {
-    a += 256 * (at + t);
+  o.tier = x.tier;
+  o.at = x.at;
+  o.rows = x.rows;
+  o.page = reinterpret_cast<const uint8_t*>(x.page) + kHdrBytes;
+  if (o.tier == SKV_TIER_T1) {
+    const uint8_t* const k = o.page + 2 * P + 64 * (o.at + t) + 16 * g;
+    const uint8_t* const v = o.page + 68 * P + 128 * o.at + 16 * lane;
+    const uint8_t* const r = o.page + 2 * (o.at + t);
+    const uint8_t* const s = o.page + 66 * P + 2 * o.at + 4 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.k[i] = ldg128(a + 16 * ((4 * i + g) ^ (4 * (t & 1))));
-  } else if (tier < 3) {
-    o.r = *reinterpret_cast<const uint16_t*>(a + 2 * (at + t));
-    a += 2 * P;
-    if (tier == SKV_TIER_T1) {
-      o.k[0] = ldg128(a + 64 * (at + t) + 16 * g);
-    } else {
-      a += 48 * (at + t);
-      const uint2 n = *reinterpret_cast<const uint2*>(a + 8 * g);
-      o.k[0].x = n.x;
-      o.k[0].y = n.y;
-      o.k[0].z = *reinterpret_cast<const uint32_t*>(a + 32 + 4 * g);
+    for (int e = 0; e < 2; ++e) {
+      o.k[e] = ldg128(k + 512 * e);
+      o.r[e] = *reinterpret_cast<const uint16_t*>(r + 16 * e);
+      o.v[2 * e] = ldg128(v + 1024 * e);
+      o.v[2 * e + 1] = ldg128(v + 1024 * e + 512);
+      o.s[e] = *reinterpret_cast<const uint32_t*>(s + 16 * e);
     }
-  }
-}
-
-__device__ __forceinline__ void load_values(const uint8_t* page, uint32_t tier, int at, int P,
-                                            int lane, Rows& o) {
-  const uint8_t* a = page + kHdrBytes;
-  if (tier == SKV_TIER_T0) {
-    a += 256 * (P + at) + 16 * lane;
+  } else if (o.tier == SKV_TIER_T2) {
+    const uint8_t* const k = o.page + 2 * P + 48 * (o.at + t);
+    const uint8_t* const v = o.page + 52 * P + 128 * o.at + 16 * lane;
+    const uint8_t* const r = o.page + 2 * (o.at + t);
+    const uint8_t* const s = o.page + 50 * P + 2 * o.at + 4 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = ldg128(a + 512 * i);
-  } else if (tier < 3) {
-    const int cb = tier == SKV_TIER_T1 ? 64 : 48;
-    a += (2 + cb) * P;
-    o.s = *reinterpret_cast<const uint32_t*>(a + 2 * (at + 2 * (lane & 3)));
-    a += 2 * P + 128 * at + 16 * lane;
-    o.v[0] = ldg128(a);
-    o.v[1] = ldg128(a + 512);
+    for (int e = 0; e < 2; ++e) {
+      const uint2 n = *reinterpret_cast<const uint2*>(k + 384 * e + 8 * g);
+      o.k[e].x = n.x;
+      o.k[e].y = n.y;
+      o.k[e].z = *reinterpret_cast<const uint32_t*>(k + 384 * e + 32 + 4 * g);
+      o.r[e] = *reinterpret_cast<const uint16_t*>(r + 16 * e);
+      o.v[2 * e] = ldg128(v + 1024 * e);
+      o.v[2 * e + 1] = ldg128(v + 1024 * e + 512);
+      o.s[e] = *reinterpret_cast<const uint32_t*>(s + 16 * e);
+    }
   }
 }
 
@@ -377,110 +406,126 @@ __device__ __forceinline__ uint32_t t2_at(uint32_t nw, uint32_t cw, int j, uint3
   return (xn & 0xF00u) | (xc & 0x3000u) | tb;
 }
 
-// keys of 8 rows -> fp16 rows T0 .. T0 + 7 of the tile at kb
-__device__ __forceinline__ void store_keys(const Rows& o, uint32_t tier, uint32_t kb, int T0,
-                                           int lane, uint32_t tb) {
+// A part's keys -> fp16 rows T0 .. T0 + 15 of the tile at kb.
+__device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, int lane,
+                                           uint32_t tb) {
   const int t = lane >> 2, g = lane & 3, odd = t & 1;
   // odd rows go through their chunks in the order 1 0 3 2, which spreads a
   // quarter warp's stores over all banks
   const uint32_t row = kb + (uint32_t)(T0 + t) * 128;
   const uint32_t at[2] = {row + (((4 * odd + g) ^ t) << 4), row + (((4 * (odd ^ 1) + g) ^ t) << 4)};
-  if (tier == SKV_TIER_T0) {
+  if (o.tier == SKV_TIER_T1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint4 x;
-      x.x = odd ? o.k[e ^ 1].x : o.k[e].x;
-      x.y = odd ? o.k[e ^ 1].y : o.k[e].y;
-      x.z = odd ? o.k[e ^ 1].z : o.k[e].z;
-      x.w = odd ? o.k[e ^ 1].w : o.k[e].w;
-      sts128(at[e & 1] + (e >> 1) * 8192, x);
-    }
-  } else if (tier == SKV_TIER_T1) {
-    const uint32_t r = o.r | (o.r << 16);
-    const uint32_t w[4] = {odd ? o.k[0].y : o.k[0].x, odd ? o.k[0].x : o.k[0].y,
-                           odd ? o.k[0].w : o.k[0].z, odd ? o.k[0].z : o.k[0].w};
+    for (int h = 0; h < 2; ++h) {
+      const uint4 k = o.k[h];
+      const uint32_t r = o.r[h] | (o.r[h] << 16);
+      const uint32_t w[4] = {odd ? k.y : k.x, odd ? k.x : k.y, odd ? k.w : k.z, odd ? k.z : k.w};
+      uint32_t x[16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint4 x;
-      x.x = hmul2(lds32(t1_at(w[e], 0, tb)), r);
-      x.y = hmul2(lds32(t1_at(w[e], 1, tb)), r);
-      x.z = hmul2(lds32(t1_at(w[e], 2, tb)), r);
-      x.w = hmul2(lds32(t1_at(w[e], 3, tb)), r);
-      sts128(at[e & 1] + (e >> 1) * 8192, x);
+      for (int e = 0; e < 16; ++e) x[e] = lds32(t1_at(w[e >> 2], e & 3, tb));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h,
+               make_uint4(hmul2(x[4 * e], r), hmul2(x[4 * e + 1], r), hmul2(x[4 * e + 2], r),
+                          hmul2(x[4 * e + 3], r)));
     }
-  } else if (tier == SKV_TIER_T2) {
+  } else if (o.tier == SKV_TIER_T2) {
     const uint32_t tb2 = tb + 128;
-    const uint32_t r = o.r | (o.r << 16);
-    // pairs 4 i .. 4 i + 3: nibbles and crumbs 4 i + b; odd rows swap halves
-    const int sw = 16 * odd;
-    const uint32_t n[2] = {__funnelshift_r(o.k[0].x, o.k[0].x, sw),
-                           __funnelshift_r(o.k[0].y, o.k[0].y, sw)};
-    const uint32_t cw = odd ? ((o.k[0].z >> 8) & 0x00FF00FFu) | ((o.k[0].z << 8) & 0xFF00FF00u)
-                            : o.k[0].z;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint4 x;
-      x.x = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e, tb2)), r);
-      x.y = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 1, tb2)), r);
-      x.z = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 2, tb2)), r);
-      x.w = hmul2(lds32(t2_at(n[e >> 1], cw, 4 * e + 3, tb2)), r);
-      sts128(at[e & 1] + (e >> 1) * 8192, x);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t r = o.r[h] | (o.r[h] << 16);
+      // pairs 4 i .. 4 i + 3: nibbles and crumbs 4 i + b; odd rows swap halves
+      const int sw = 16 * odd;
+      const uint32_t n[2] = {__funnelshift_r(o.k[h].x, o.k[h].x, sw),
+                             __funnelshift_r(o.k[h].y, o.k[h].y, sw)};
+      const uint32_t z = o.k[h].z;
+      const uint32_t cw = odd ? ((z >> 8) & 0x00FF00FFu) | ((z << 8) & 0xFF00FF00u) : z;
+      uint32_t x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = lds32(t2_at(n[e >> 3], cw, e, tb2));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h,
+               make_uint4(hmul2(x[4 * e], r), hmul2(x[4 * e + 1], r), hmul2(x[4 * e + 2], r),
+                          hmul2(x[4 * e + 3], r)));
+    }
+  } else if (o.tier == SKV_TIER_T0) {
+    const uint8_t* a = o.page + 256 * (o.at + t);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint4 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = ldg128(a + 2048 * h + 16 * ((4 * (e ^ odd) + g) ^ (4 * odd)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h, x[e]);
     }
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sts128(at[e & 1] + (e >> 1) * 8192, make_uint4(0, 0, 0, 0));
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e)
+      sts128(at[e & 1] + ((e >> 1) & 1) * kHalfDims + 1024 * (e >> 2), make_uint4(0, 0, 0, 0));
   }
 }
 
-// Values of 8 rows -> fp16.  The tile's columns are a permutation of the
+// A part's values -> fp16.  The tile's columns are a permutation of the
 // dims that a lane of the pages' fragment order holds together: column
 // 64 h + 8 g + 2 m + hi is dim 64 h + 16 m + 8 hi + g.
-__device__ __forceinline__ void store_values(const Rows& o, uint32_t tier, int rows, uint32_t vb,
-                                             int T0, int lane) {
+__device__ __forceinline__ void store_values(const Rows& o, int P, uint32_t vb, int T0, int lane) {
   const int g = lane >> 2, a = 2 * (lane & 3), b = a + 1;
   const uint32_t ra = vb + (uint32_t)(T0 + a) * 128 + ((g ^ a) << 4);
   const uint32_t rb = vb + (uint32_t)(T0 + b) * 128 + ((g ^ b) << 4);
-  if (tier == SKV_TIER_T0) {
-    const bool ua = a < rows, ub = b < rows;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 x = o.v[2 * h], y = o.v[2 * h + 1];
-      uint4 p = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
-                           __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
-      uint4 q = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
-                           __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
-      if (!ua) p = make_uint4(0, 0, 0, 0);
-      if (!ub) q = make_uint4(0, 0, 0, 0);
-      sts128(ra + h * 8192, p);
-      sts128(rb + h * 8192, q);
-    }
-  } else if (tier < 3) {
+  if (o.tier == SKV_TIER_T1 || o.tier == SKV_TIER_T2) {
     // v + 128 as the low byte of 1024 + x in fp16, less 1152 (exact), times
     // the scale (rounded once); rows that are not there get the scale 0
-    const uint32_t sa = a < rows ? __byte_perm(o.s, 0u, 0x1010) : 0u;
-    const uint32_t sb = b < rows ? __byte_perm(o.s, 0u, 0x3232) : 0u;
     const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w[4] = {o.v[h].x, o.v[h].y, o.v[h].z, o.v[h].w};
-      uint32_t p[4], q[4];
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sa = a + 8 * e < o.rows ? __byte_perm(o.s[e], 0u, 0x1010) : 0u;
+      const uint32_t sb = b + 8 * e < o.rows ? __byte_perm(o.s[e], 0u, 0x3232) : 0u;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t u = w[m] ^ 0x80808080u;
-        const uint32_t x = __byte_perm(u, 0x64646464u, 0x4240), y = __byte_perm(u, 0x64646464u, 0x4341);
-        const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
-        const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-        p[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hx), sa);
-        q[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hy), sb);
+      for (int h = 0; h < 2; ++h) {
+        const uint4 z = o.v[2 * e + h];
+        const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+        uint32_t p[4], q[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t u = w[m] ^ 0x80808080u;
+          const uint32_t x = __byte_perm(u, 0x64646464u, 0x4240),
+                         y = __byte_perm(u, 0x64646464u, 0x4341);
+          const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
+          const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
+          p[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hx), sa);
+          q[m] = hmul2(*reinterpret_cast<const uint32_t*>(&hy), sb);
+        }
+        sts128(ra + h * kHalfDims + 1024 * e, make_uint4(p[0], p[1], p[2], p[3]));
+        sts128(rb + h * kHalfDims + 1024 * e, make_uint4(q[0], q[1], q[2], q[3]));
       }
-      sts128(ra + h * 8192, make_uint4(p[0], p[1], p[2], p[3]));
-      sts128(rb + h * 8192, make_uint4(q[0], q[1], q[2], q[3]));
+    }
+  } else if (o.tier == SKV_TIER_T0) {
+    const uint8_t* from = o.page + 256 * (P + o.at) + 16 * lane;
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      const bool ua = a + 8 * e < o.rows, ub = b + 8 * e < o.rows;
+      uint4 z[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) z[h] = ldg128(from + 2048 * e + 512 * h);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = z[2 * h], y = z[2 * h + 1];
+        uint4 p = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                             __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
+        uint4 q = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
+                             __byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632));
+        if (!ua) p = make_uint4(0, 0, 0, 0);
+        if (!ub) q = make_uint4(0, 0, 0, 0);
+        sts128(ra + h * kHalfDims + 1024 * e, p);
+        sts128(rb + h * kHalfDims + 1024 * e, q);
+      }
     }
   } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sts128(ra + h * 8192, make_uint4(0, 0, 0, 0));
-      sts128(rb + h * 8192, make_uint4(0, 0, 0, 0));
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      sts128(ra + (e & 1) * kHalfDims + 1024 * (e >> 1), make_uint4(0, 0, 0, 0));
+      sts128(rb + (e & 1) * kHalfDims + 1024 * (e >> 1), make_uint4(0, 0, 0, 0));
     }
   }
 }
@@ -516,7 +561,7 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
       const float2 y = from16x2(w[k], p.kv_bf16);
       w[k] = pack_f16x2(y.x * up, y.y * up);
     }
-    sts128(row + (i >> 1) * 8192 + (((4 * (i & 1) + g) ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+    sts128(row + (i >> 1) * kHalfDims + (((4 * (i & 1) + g) ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
   if (g == 0) cs[j] = pow2i(-e);
   bool out = false;
@@ -539,7 +584,7 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
       }
       w[m] = pack_f16x2(y[0], y[1]);
     }
-    sts128(vb + (uint32_t)j * 128 + hf * 8192 + ((gg ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+    sts128(vb + (uint32_t)j * 128 + hf * kHalfDims + ((gg ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
   if (out) *(volatile int*)bad = 1;
 }
@@ -547,137 +592,147 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
 template <bool BIAS>
 __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t tbl, int wd,
                                             int lane) {
-  const int w = wd & (kTeamWarps - 1), stage = wd / kTeamWarps, P = p.P, T0 = 16 * w;
-  const uint32_t tb = tbl + 4 * lane;
-  const uint32_t kb = tbl + kTblBytes + stage * kStageBytes, vb = kb + kTile * 256;
-  Rows o;
+  const int w = wd & (kTeamWarps - 1), stage = wd / kTeamWarps, P = p.P;
+  const uint32_t tb = tbl + 4 * lane, kb = keys_at(tbl, stage), vb = values_at(tbl, stage);
   int t = stage;
-  uint32_t turn = 0;
+  uint32_t turn = 1;   // of the stage: parity of the tile before
   if (!warp_wait(f.dfull[0], 0, f, p.err)) return;
   uint32_t flags = f.ring[t].flags;
-  Part x = f.ring[t].part[w];
-  const uint8_t* page = reinterpret_cast<const uint8_t*>(x.page);
-  o.r = o.s = 0;
-  load_keys(page, x.tier, x.at, P, lane, o);
-  load_values(page, x.tier, x.at, P, lane, o);
+  Rows o = {}, next = {};
+  load_part(f.ring[t].part[2 * w], P, lane, o);
   while (!(flags & kEnd)) {
-    const Tile& d = f.ring[t & (kRing - 1)];
-    const int rows = x.rows;
-    const uint32_t tier = x.tier;
+    Tile& d = f.ring[t & (kRing - 1)];
     const bool draft = (flags & kDraft) != 0;
-    if (turn > 0 && !warp_wait(f.kempty[stage], (turn - 1) & 1, f, p.err)) return;
-    if (!draft) {
-      store_keys(o, tier, kb, T0, lane, tb);
-      load_keys(page, tier, x.at + 8, P, lane, o);
-    }
-    if (turn > 0 && !warp_wait(f.vempty[stage], (turn - 1) & 1, f, p.err)) return;
-    if (BIAS && lane < 16) {
-      const int b = d.unit / p.Hkv;
-      const int q0 = p.q_pos[(long long)b * p.N];
-      int q = q0;
-      if (draft) {
-        if (T0 + lane < d.n) q = p.q_pos[(long long)b * p.N + T0 + lane];
-      } else if (lane < rows) {
-        q = p.row_pos[(long long)d.first * P + T0 + lane];  // (a tile's pages follow each other)
-      }
-      f.pos[stage][T0 + lane] = (float)(q - q0);
-    }
-    if (!draft) {
-      store_values(o, tier, rows, vb, T0, lane);
-      load_values(page, tier, x.at + 8, P, lane, o);
-      store_keys(o, tier, kb, T0 + 8, lane, tb);
-    } else {
 #pragma unroll 1
-      for (int e = 0; e < 16; e += 8)
-        store_draft(p, d, kb, vb, f.cs[stage], &f.ring[t & (kRing - 1)].bad, T0 + e, lane);
+    for (int u = 0; u < 2; ++u) {
+      const int T0 = 32 * w + 16 * u;
+      // the next part's loads go out before this part's conversion
+      if (u == 0) {
+        load_part(d.part[2 * w + 1], P, lane, next);
+        if (t >= kStages && !warp_wait(f.kempty[stage], turn, f, p.err)) return;
+      } else {
+        const int t2 = t + kStages;
+        if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f, p.err))
+          return;
+        flags = f.ring[t2 & (kRing - 1)].flags;
+        load_part(f.ring[t2 & (kRing - 1)].part[2 * w], P, lane, next);
+      }
+      if (!draft) store_keys(o, kb, T0, lane, tb);
+      if (u == 0 && t >= kStages && !warp_wait(f.vempty[stage], turn, f, p.err)) return;
+      if (BIAS && lane < 16) {
+        const long long b = d.unit / p.Hkv;
+        const int q0 = p.q_pos[b * p.N];
+        int q = q0;
+        if (draft) {
+          if (T0 + lane < d.n) q = p.q_pos[b * p.N + T0 + lane];
+        } else if (lane < o.rows) {
+          q = p.row_pos[(long long)d.first * P + T0 + lane];  // (a tile's pages follow each other)
+        }
+        f.pos[stage][T0 + lane] = (float)(q - q0);
+      }
+      if (u == 1 && !draft) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        warp_arrive(f.kfull[stage]);
+      }
+      if (!draft) {
+        store_values(o, P, vb, T0, lane);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 16; e += 8) store_draft(p, d, kb, vb, f.cs[stage], &d.bad, T0 + e, lane);
+      }
+      o = next;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    warp_arrive(f.kfull[stage]);
-    const int t2 = t + kStages;
-    if ((t2 >> 3) != (t >> 3) && !warp_wait(f.dfull[(t2 >> 3) & 3], (t2 >> 5) & 1, f, p.err)) return;
-    flags = f.ring[t2 & (kRing - 1)].flags;
-    x = f.ring[t2 & (kRing - 1)].part[w];
-    page = reinterpret_cast<const uint8_t*>(x.page);
-    load_keys(page, x.tier, x.at, P, lane, o);
-    if (!draft) store_values(o, tier, rows - 8, vb, T0 + 8, lane);
-    load_values(page, x.tier, x.at, P, lane, o);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (draft) warp_arrive(f.kfull[stage]);
     warp_arrive(f.vfull[stage]);
-    t = t2;
-    ++turn;
+    t += kStages;
+    turn ^= 1;
   }
 }
 
 // ------------------------------------------------------------------- the MMAs
-__device__ __forceinline__ void mma_role(const TreeParams& p, Fixed& f, uint32_t stages,
-                                         uint32_t tm) {
-  const int G = p.Hq / p.Hkv;
-  const bool lead = elect_one();
-  uint32_t stage = 0, turn = 0;       // of the present tile: its stage, the stage's parity
-  uint32_t pturn = 0;                 // bit s: parity of stream s's weights
+// S = Q K^T of every job, as soon as the keys are there and the stream's
+// scores are read (two blocks: its weights used).
+__device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32_t tbl, uint32_t tm) {
+  const int most = 128 * p.Hkv;       // n * Hq above it: two blocks
+  uint32_t turn = 3;                  // bit s: parity of stream s's job before
   uint32_t segs = 0;
-  int nb = 1, j = 0;
-  // the job whose weights are still to come
-  bool pending = false, free_tile = false, free_ring = false;
-  uint32_t ps = 0, pstage = 0, padd = 0, pvt = 0, pbatch = 0;
-  const auto pv = [&]() {
-    if (!warp_wait(f.pfull[ps], (pturn >> ps) & 1, f, p.err)) return false;
-    pturn ^= 1u << ps;
-    if (!warp_wait(f.vfull[pstage], pvt, f, p.err)) return false;
-    tc_fence_after();
-    if (lead) {
-      const uint32_t low = kDescValues | ((stages + pstage * kStageBytes + kTile * 256) >> 4);
-      const uint32_t a = tm + (nb == 2 ? kColS + 64 * ps : kColP + 32 * ps);
-      const uint32_t o = tm + kColO + 128 * ps;
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        tc_mma(o, a + 8 * k, operand(low + 128 * k), kIdescO, k > 0 ? 1u : padd);
-      tc_commit(smem_u32(&f.odone[ps]));
-      if (free_tile) tc_commit(smem_u32(&f.vempty[pstage]));
-      if (free_ring) tc_commit(smem_u32(&f.rfree[pbatch]));
-    }
-    __syncwarp();
-    pending = false;
-    return true;
-  };
+  bool two = false;
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+      return;
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
     if (flags & kFirst) {
       if (!warp_wait(f.qfull, segs & 1, f, p.err)) return;
       ++segs;
-      nb = f.ring[t & (kRing - 1)].n * G > 128 ? 2 : 1;
-      j = 0;
+      two = f.ring[t & (kRing - 1)].n * p.Hq > most;
     }
-    if (!warp_wait(f.kfull[stage], turn, f, p.err)) return;
-    tc_fence_after();
-    for (int b = 0; b < nb; ++b, ++j) {
-      const uint32_t s = j & 1;
-      if (lead) {
-        const uint32_t low = kDescKeys | ((stages + stage * kStageBytes) >> 4);
-        const uint32_t a = tm + kColQ + (nb == 2 ? 64 * s : 0), o = tm + kColS + 64 * s;
+    const uint32_t stage = t & 1;
+    if (!warp_wait(f.kfull[stage], (t >> 1) & 1, f, p.err)) return;
+    const uint32_t keys = kDescKeys | (keys_at(tbl, stage) >> 4);
+    const int jobs = two ? 4 : 2;
+#pragma unroll 1
+    for (int y = 0; y < jobs; ++y) {
+      const uint32_t s = y & 1;
+      if (!warp_wait(f.sfree[s], (turn >> s) & 1, f, p.err)) return;
+      if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f, p.err)) return;
+      turn ^= 1u << s;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t low = keys + (two ? y >> 1 : y) * (kJob * 128 / 16);
+        const uint32_t a = tm + kColQ + (two ? 64 * s : 0), o = tm + kColS + 64 * s;
 #pragma unroll
         for (int k = 0; k < kHeadDim / 16; ++k)
-          tc_mma(o, a + 8 * k, operand(low + (k >> 2) * 512 + (k & 3) * 2), kIdescS, k > 0);
+          tc_mma(o, a + 8 * k, operand(low + (k >> 2) * (kHalfDims / 16) + (k & 3) * 2), kIdescS,
+                 k > 0);
         tc_commit(smem_u32(&f.sfull[s]));
-        if (b == nb - 1) tc_commit(smem_u32(&f.kempty[stage]));
+        if (y == jobs - 1) tc_commit(smem_u32(&f.kempty[stage]));
       }
       __syncwarp();
-      if (pending && !pv()) return;
-      ps = s;
-      pstage = stage;
-      pvt = turn;
-      padd = j > 1 ? 1u : 0u;
-      free_tile = b == nb - 1;
-      free_ring = free_tile && (t & (kBatch - 1)) == kBatch - 1;
-      pbatch = (t / kBatch) & 3;
-      pending = true;
     }
-    if ((flags & kLast) && !pv()) return;
-    if (++stage == kStages) {
-      stage = 0;
-      turn ^= 1;
+  }
+}
+
+// O += P V of every job, as soon as its weights are there.
+__device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t tbl, uint32_t tm) {
+  const int most = 128 * p.Hkv;
+  uint32_t turn = 0;                  // bit s: parity of stream s's job
+  uint32_t add = 0;                   // bit s: stream s has had a job in the segment
+  bool two = false;
+  for (int t = 0;; ++t) {
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+      return;
+    const uint32_t flags = f.ring[t & (kRing - 1)].flags;
+    if (flags & kEnd) return;
+    if (flags & kFirst) {
+      add = 0;
+      two = f.ring[t & (kRing - 1)].n * p.Hq > most;
+    }
+    const uint32_t stage = t & 1;
+    if (!warp_wait(f.vfull[stage], (t >> 1) & 1, f, p.err)) return;
+    const uint32_t values = kDescValues | (values_at(tbl, stage) >> 4);
+    const int jobs = two ? 4 : 2;
+#pragma unroll 1
+    for (int y = 0; y < jobs; ++y) {
+      const uint32_t s = y & 1;
+      if (!warp_wait(f.pfull[s], (turn >> s) & 1, f, p.err)) return;
+      turn ^= 1u << s;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t low = values + (two ? y >> 1 : y) * (kJob * 128 / 16);
+        const uint32_t a = tm + (two ? kColS + 64 * s : kColP + 32 * s), o = tm + kColO + 128 * s;
+#pragma unroll
+        for (int k = 0; k < kJob / 16; ++k)
+          tc_mma(o, a + 8 * k, operand(low + 128 * k), kIdescO, k > 0 ? 1u : (add >> s) & 1);
+        tc_commit(smem_u32(&f.odone[s]));
+        if (y == jobs - 1) {
+          tc_commit(smem_u32(&f.vempty[stage]));
+          if ((t & (kBatch - 1)) == kBatch - 1) tc_commit(smem_u32(&f.rfree[(t / kBatch) & 3]));
+        }
+      }
+      __syncwarp();
+      add |= 1u << s;
     }
   }
 }
@@ -691,83 +746,111 @@ struct Row {           // a lane's row in its stream
   int mine;            // its jobs in the segment
 };
 
-// Columns c0 .. c0 + NC - 1 of a tile: scores to weights.  S at `sa`, the
-// weights' tensor memory at `pa`; bits: the columns this row sees.
-template <int NC, bool CAP, bool BIAS>
+// The maximum of the lanes that need it rises to `top`: their sums, O and the
+// weights of the job's columns before `done` (at pa) follow.
+__device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, float top, uint32_t pa,
+                                      int done, uint32_t oa, int wg) {
+  const float m = top > r.m + kRaise ? top : r.m;
+  const float a = m == r.m ? 1.0f : ex2f(r.m - m);
+  r.l *= a;
+  r.m = m;
+  const uint32_t a2 = pack_f16x2(a, a);
+  tc_wait_st();
+#pragma unroll 1
+  for (int k = 0; k < done; k += 16) {
+    uint32_t w[8];
+    tc_ld8(pa + k / 2, w);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = hmul2(w[e], a2);
+    tc_st8(pa + k / 2, w);
+  }
+  if (r.mine > 0) {
+    if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int k = 0; k < kHeadDim; k += 16) {
+      float o[16];
+      tc_ld16(oa + k, o);
+      tc_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] *= a;
+      tc_st8(oa + k, reinterpret_cast<const uint32_t*>(o));
+      tc_st8(oa + k + 8, reinterpret_cast<const uint32_t*>(o) + 8);
+    }
+  }
+  tc_wait_st();
+  return true;
+}
+
+// n columns (32 or 64) of a job, 32 at a time: scores (at sa) to weights (at
+// pa); bits: the columns this row sees.
+template <bool CAP, bool BIAS>
 __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& r, uint32_t sa,
-                                            uint32_t pa, uint32_t oa, int wg,
+                                            uint32_t pa, uint32_t oa, int wg, int n,
                                             unsigned long long bits, const float* cs,
                                             const float* pos) {
-  float s[NC];
-#pragma unroll
-  for (int k = 0; k < NC; k += 16) tc_ld16(sa + k, s + k);
-  tc_wait_ld();
-  constexpr unsigned long long kAll = NC == 64 ? ~0ull : (1ull << (NC & 63)) - 1;
-  if (cs) {
-#pragma unroll
-    for (int k = 0; k < NC; ++k) s[k] *= cs[k];
-  }
-  if (CAP || BIAS) {
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      if (CAP) {
-        const float e = ex2f(s[k] * r.c);
-        s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
-      } else {
-        s[k] *= r.c;
-      }
-      if (BIAS) s[k] = fmaf(r.slope, pos[k] - r.rel, s[k]);
-    }
-  }
-  if (bits != kAll) {
-#pragma unroll
-    for (int k = 0; k < NC; ++k)
-      if (!((bits >> k) & 1)) s[k] = -INFINITY;
-  }
-  float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-  for (int k = 4; k < NC; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
-  float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  if (!(CAP || BIAS)) top *= r.c;
-  if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise)) {
-    // raise the maximum of the rows that need it; their sums follow
-    const float m = top > r.m + kRaise ? top : r.m;
-    const float a = m == r.m ? 1.0f : ex2f(r.m - m);
-    r.l *= a;
-    r.m = m;
-    if (r.mine > 0) {
-      if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
-      tc_fence_after();
+  float s[32];
+  tc_ld16(sa, s);
+  tc_ld16(sa + 16, s + 16);
 #pragma unroll 1
-      for (int k = 0; k < kHeadDim; k += 16) {
-        float o[16];
-        tc_ld16(oa + k, o);
-        tc_wait_ld();
+  for (int c = 0; c < n; c += 32) {
+    tc_wait_ld();
+    if (c + 32 >= n) {
+      tc_fence_before();
+      warp_arrive(f.sfree[wg]);
+    }
+    if (cs) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] *= a;
-        tc_st8(oa + k, reinterpret_cast<const uint32_t*>(o));
-        tc_st8(oa + k + 8, reinterpret_cast<const uint32_t*>(o) + 8);
+      for (int k = 0; k < 32; ++k) s[k] *= cs[c + k];
+    }
+    if (CAP || BIAS) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        if (CAP) {
+          const float e = ex2f(s[k] * r.c);
+          s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
+        } else {
+          s[k] *= r.c;
+        }
+        if (BIAS) s[k] = fmaf(r.slope, pos[c + k] - r.rel, s[k]);
       }
     }
-  }
-  const float m = r.m == -INFINITY ? 0.0f : r.m;
-  const float2 c2 = make_float2(r.c, r.c), m2 = make_float2(-m, -m);
-  float2 l2 = make_float2(r.l, 0.0f);
+    const uint32_t see = (uint32_t)(bits >> c);
+    if (see != 0xFFFFFFFFu) {
 #pragma unroll
-  for (int k = 0; k < NC; k += 16) {
-    uint32_t w[8];
+      for (int k = 0; k < 32; ++k)
+        if (!((see >> k) & 1)) s[k] = -INFINITY;
+    }
+    float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float2 x = make_float2(s[k + 2 * e], s[k + 2 * e + 1]);
+    for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
+    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    if (!(CAP || BIAS)) top *= r.c;
+    if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise) && !raise(p, f, r, top, pa, c, oa, wg)) return false;
+    const float m = r.m == -INFINITY ? 0.0f : r.m;
+    const float2 c2 = make_float2(r.c, r.c), m2 = make_float2(-m, -m);
+    float2 l2 = make_float2(r.l, 0.0f);
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float2 x = make_float2(s[2 * e], s[2 * e + 1]);
       x = (CAP || BIAS) ? add2(x, m2) : fma2(x, c2, m2);
       x.x = ex2f(x.x);
       x.y = ex2f(x.y);
       l2 = add2(l2, x);
       w[e] = pack_f16x2(x.x, x.y);
     }
-    tc_st8(pa + k / 2, w);
+    r.l = l2.x + l2.y;
+    if (c + 32 < n) {
+      tc_ld16(sa + c + 32, s);
+      tc_ld16(sa + c + 48, s + 16);
+    }
+    // (the product before may still read its weights)
+    if (c == 0 && r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
+    tc_st8(pa + c / 2, w);
+    tc_st8(pa + c / 2 + 8, w + 8);
   }
-  r.l = l2.x + l2.y;
   tc_wait_st();
   return true;
 }
@@ -781,7 +864,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
   const uint32_t oa = tm + kColO + 128 * wg;
   Row r = {};
   uint32_t syncs = 0;
-  int nb = 1, rc = 128, j = 0, row = 0, copy = 0, R = 0;
+  const int lgG = __ffs(G) - 1;
+  int nb = 1, rc = 128, copy = 0, R = 0;
   bool busy = true;  // the warp has rows
   unsigned long long see = 0;
   const auto meet = [&]() {
@@ -789,18 +873,19 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     return warp_wait(f.sync, syncs++ & 1, f, p.err);
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t >> 3) & 3], (t >> 5) & 1, f, p.err)) return;
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+      return;
     const Tile& d = f.ring[t & (kRing - 1)];
     const uint32_t flags = d.flags;
     if (flags & kEnd) return;
     if (flags & kFirst) {
       R = d.n * G;
       nb = R > 128 ? 2 : 1;
-      rc = R <= 32 ? 32 : (R <= 64 ? 64 : 128);
-      row = nb == 2 ? 128 * wg + tl : (tl & (rc - 1));
+      rc = R <= 64 ? 64 : 128;
+      const int row = nb == 2 ? 128 * wg + tl : (tl & (rc - 1));
       copy = nb == 2 ? 0 : tl / rc;
       const int b = d.unit / p.Hkv, h = d.unit - b * p.Hkv;
-      const int i = row / G, hq = h * G + (row - i * G);
+      const int i = row >> lgG, hq = h * G + (row & (G - 1));
       const bool live = row < R;
       busy = __any_sync(0xFFFFFFFFu, live);
       const long long tok = (long long)b * p.N + i;
@@ -808,7 +893,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
                                                       tok * p.q_stride + (long long)hq * kHeadDim);
       // the row as fp16 scaled by a power of two (bf16 converts exactly)
       uint32_t mx = 0;
-#pragma unroll
+#pragma unroll 4
       for (int k = 0; k < 16; ++k) {
         uint4 x = make_uint4(0, 0, 0, 0);
         if (live) x = q[k];
@@ -817,6 +902,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       const int e = scale_exp(mx, p.q_bf16);
       const float up = pow2i(e);
       // one block: both streams use it, each group writes half its dims
+#pragma unroll 1
       for (int k = 0; k < 16; k += 2) {
         if (nb == 1 && (k >> 3) != wg) continue;
         uint32_t w[8];
@@ -858,44 +944,37 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       r.m = -INFINITY;
       r.l = 0.0f;
       r.mine = 0;
-      j = 0;
       see = 0;
       if (live && p.K)
         see = p.mask ? p.mask[tok] : (i >= 63 ? ~0ull : (2ull << i) - 1);
     }
-    for (int b = 0; b < nb; ++b, ++j) {
-      if ((j & 1) != wg) continue;
+    // one block: the stream's half; two: both halves
+#pragma unroll 1
+    for (int y = nb == 1 ? wg : 0; y < (nb == 1 ? wg + 1 : 2); ++y) {
       if (!warp_wait(f.sfull[wg], r.turn, f, p.err)) return;
       tc_fence_after();
       if (busy) {
-        const int stage = t % kStages;
-        unsigned long long bits = d.valid;
-        const int c0 = nb == 2 ? 0 : copy * (kTile * rc / 128);
+        const int stage = t & 1, n = kJob * rc / 128, c0 = copy * n;
+        unsigned long long bits = d.valid[y];
         const float* cs = nullptr;
         if (flags & kDraft) {
           bits &= see;
-          cs = f.cs[stage] + c0;
+          cs = f.cs[stage] + kJob * y + c0;
         }
-        const float* pos = f.pos[stage] + c0;
         const uint32_t sa = tm + kColS + 64 * wg + c0;
         const uint32_t pa = nb == 2 ? sa : tm + kColP + 32 * wg + c0 / 2;
-        bool ok;
-        if (rc == 128)
-          ok = softmax_job<64, CAP, BIAS>(p, f, r, sa, pa, oa, wg, bits, cs, pos);
-        else if (rc == 64)
-          ok = softmax_job<32, CAP, BIAS>(p, f, r, sa, pa, oa, wg, (bits >> c0) & 0xFFFFFFFFull, cs,
-                                          pos);
-        else
-          ok = softmax_job<16, CAP, BIAS>(p, f, r, sa, pa, oa, wg, (bits >> c0) & 0xFFFFull, cs, pos);
-        if (!ok) return;
+        if (!softmax_job<CAP, BIAS>(p, f, r, sa, pa, oa, wg, n, bits >> c0, cs,
+                                    f.pos[stage] + kJob * y + c0))
+          return;
       }
+      if (!busy) warp_arrive(f.sfree[wg]);
       tc_fence_before();
       warp_arrive(f.pfull[wg]);
       r.turn ^= 1;
       ++r.mine;
     }
     if (!(flags & kLast)) continue;
-    // the segment's end: the streams' and copies' sums meet, 64 dims at a time
+    // the segment's end: the streams' and copies' sums meet, 32 dims at a time
     if (r.mine > 0) {
       if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return;
       tc_fence_after();
@@ -914,16 +993,16 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
     }
 #pragma unroll 1
-    for (int step = 0; step < 4; ++step) {
-      // one block: both streams' halves in turn, the second adds to the
-      // first's; two blocks: a block's halves in turn
-      const int hf = nb == 1 ? step >> 1 : step & 1, s = nb == 1 ? 1 - (step & 1) : step >> 1;
+    for (int step = 0; step < 8; ++step) {
+      // one block: the streams in turn, the second adds to the first's; two
+      // blocks: a block's quarters in turn
+      const int qt = nb == 1 ? step >> 1 : step & 3, s = nb == 1 ? 1 - (step & 1) : step >> 2;
       if (wg == s && busy) {
 #pragma unroll 1
-        for (int k = 0; k < 64; k += 16) {
+        for (int k = 0; k < 32; k += 16) {
           float o[16];
           if (r.mine > 0) {
-            tc_ld16(oa + 64 * hf + k, o);
+            tc_ld16(oa + 32 * qt + k, o);
             tc_wait_ld();
           }
 #pragma unroll
@@ -945,12 +1024,15 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       }
       if (!meet()) return;
       if (nb == 1 && s == 1) continue;
-      const int l = lane & 15, top = nb == 1 ? R : min(128, R - 128 * s);
-      for (int x = 2 * warp + (lane >> 4); x < top; x += 2 * kSoftWarps) {
+      // a quarter's columns 32 qt .. + 31: dims 64 h + 16 m + 8 hi + g of four
+      // g, column 8 (g & 3) + 2 m + hi of the buffer.  Lane l of 8 has the
+      // dims of (m, hi)
+      const int l = lane & 7, top = nb == 1 ? R : min(128, R - 128 * s);
+      for (int x = 4 * warp + (lane >> 3); x < top; x += 4 * kSoftWarps) {
         float Mx = -INFINITY, Lx = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < copies; ++k) {
           const int z = x + rc * k;
-          const float* from = buf + z * kBufRow + 32 * (l & 1) + 2 * ((l >> 2) & 3) + ((l >> 1) & 1);
+          const float* from = buf + z * kBufRow + l;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += from[8 * e];
           Mx = nb == 2 ? f.m[s][z] : fmaxf(Mx, fmaxf(f.m[0][z], f.m[1][z]));
@@ -968,10 +1050,11 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
             }
           }
         }
-        write_row<CAP, BIAS>(p, d.unit, d.n, d.slot, bad, nb == 1 ? x : 128 * s + x, Mx, Lx, v,
-                             64 * hf + 4 * l, lane);
+        const int d0 = 64 * (qt >> 1) + 16 * (l >> 1) + 8 * (l & 1) + 4 * (qt & 1);
+        write_row<CAP, BIAS, 8>(p, d.unit, d.n, d.slot, bad, nb == 1 ? x : 128 * s + x, Mx, Lx, v, d0,
+                                lane);
       }
-      if (step < 3 && !meet()) return;
+      if (step < 7 && !meet()) return;
     }
   }
 }
@@ -982,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   Fixed& f = *reinterpret_cast<Fixed*>(raw);
   const uint32_t at = smem_u32(raw), tbl = (at + kLowBytes + kTblBytes - 1) & ~(kTblBytes - 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tbl + kTblBytes + kStages * kStageBytes > at + kSmemBytes) {
+  if (tbl + kTblBytes + 3 * kOperand > at + kSmemBytes) {
     // (the window starts at 1 KB: it fits)
     if (tid == 0) report(p.err, SKV_ERR_CUDA);
     return;
@@ -998,19 +1081,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&f.sfull[k]), 1);
+      mbar_init(smem_u32(&f.sfree[k]), 4);
       mbar_init(smem_u32(&f.pfull[k]), 4);
       mbar_init(smem_u32(&f.odone[k]), 1);
     }
     mbar_init(smem_u32(&f.qfull), kSoftWarps);
     mbar_init(smem_u32(&f.sync), kSoftWarps);
-    mbar_init(smem_u32(&f.fin), 1);
+    mbar_init(smem_u32(&f.fin[0]), 1);
+    mbar_init(smem_u32(&f.fin[1]), 1);
     for (int k = 0; k < kRing / kBatch; ++k) {
       mbar_init(smem_u32(&f.dfull[k]), 1);
       mbar_init(smem_u32(&f.rfree[k]), 1);
     }
     fence_mbar_init();
   }
-  if (warp == kMma) {
+  if (warp == kMmaS) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&f.tmem))
                  : "memory");
@@ -1023,28 +1108,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t tm = *(volatile uint32_t*)&f.tmem;
 
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(raw + kAtBuf), tm, warp, lane);
   } else if (warp < kPlanner) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     decode_role<BIAS>(p, f, tbl, warp - kSoftWarps, lane);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
     if (warp == kPlanner) {
       planner(p, f, blockIdx.x, lane);
-    } else if (warp == kMma) {
-      mma_role(p, f, tbl + kTblBytes, tm);
+    } else if (warp == kMmaS || warp == kMmaO) {
+      if (warp == kMmaS)
+        mma_scores(p, f, tbl, tm);
+      else
+        mma_sums(p, f, tbl, tm);
       // nothing in flight when tensor memory is given back
-      if (elect_one()) tc_commit(smem_u32(&f.fin));
+      unsigned long long& fin = f.fin[warp - kMmaS];
+      if (elect_one()) tc_commit(smem_u32(&fin));
       __syncwarp();
       int none = 0;
-      if (!mbar_wait_bounded(smem_u32(&f.fin), 0, &none) && lane == 0) report(p.err, SKV_ERR_TIMEOUT);
+      if (!mbar_wait_bounded(smem_u32(&fin), 0, &none) && lane == 0) report(p.err, SKV_ERR_TIMEOUT);
       __syncwarp();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMma) {
+  if (warp == kMmaS) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
   }

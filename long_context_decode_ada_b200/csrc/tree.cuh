@@ -8,7 +8,6 @@
 namespace skv {
 namespace tree {
 
-constexpr int kTile = 64;            // tokens of a tile
 constexpr float kRaise = 8.0f;       // log2 units a score may pass the running maximum
 
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
@@ -126,7 +125,8 @@ __device__ __forceinline__ void prefetch_page(const uint8_t* a, int P, int tier)
 // ------------------------------------------------------------------ the split
 // Pages of a unit by tier and their costs.  A dense page's bytes take 2.6
 // times a coded one's, but its conversion less: it counts twice.  A unit's
-// rows count by the kernel's own measure (rows_cost).
+// rows count by the kernel's own measure (rows_cost, with the tokens of its
+// tiles, kTile).
 struct Unit {
   long long first;     // index of the first page
   int np, n;           // pages, drafted tokens
@@ -157,7 +157,7 @@ __device__ __forceinline__ Unit unit_of(const TreeParams& p, int u, Cost rows_co
   x.w[0] = 2 * f;
   x.w[1] = x.w[2] = f;
   x.pages = (unsigned long long)x.w[0] * x.nt[0] + (unsigned long long)f * (x.nt[1] + x.nt[2]);
-  const int ipp = kTile / p.P;
+  const int ipp = Cost::kTile / p.P;
   if (x.n == 0) {
     x.pages = x.last = x.cost = 0;
   } else if (p.K || x.np == 0) {
@@ -225,7 +225,7 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
     tot += scan[k];
   }
   // a run has a tile of the least cost at least
-  const unsigned long long tiles = tot / (unsigned)(rows_cost(1) * (kTile / p.P));
+  const unsigned long long tiles = tot / (unsigned)(rows_cost(1) * (Cost::kTile / p.P));
   const int S = (int)min((unsigned long long)p.S, max(1ull, tiles));
   const bool live = c < S && tot > 0;
   unsigned long long from = 0, to = 0;
@@ -262,10 +262,9 @@ struct Share {
   int last;        // the last run of the unit
   bool starts;     // the run is the unit's first of several
 };
-__device__ __forceinline__ bool part_of(const TreeParams& p, const Unit& x, const Run& r, int c,
-                                        unsigned long long cc, Share& o) {
+__device__ __forceinline__ bool share_of(const TreeParams& p, const Unit& x, const Run& r, int c,
+                                         unsigned long long cc, int ipp, Share& o) {
   if (x.cost == 0 || cc + x.last < r.from) return false;
-  const int ipp = kTile / p.P;
   o.k = tile_at(x, (long long)(r.from - cc), ipp);
   o.kend = tile_at(x, (long long)(r.to - cc), ipp);
   o.draft = p.K != nullptr && cc + x.last < r.to;
@@ -276,18 +275,19 @@ __device__ __forceinline__ bool part_of(const TreeParams& p, const Unit& x, cons
   return true;
 }
 
-// Four dims (d0 ..) of one row of the result, by one of the 16 lanes l that
+// Four dims (d0 ..) of one row of the result, by one of LANES lanes that
 // share the row: v is O relative to M, L the row's sum.  Drafted values
 // outside fp16's range are added here.
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, int LANES>
 __device__ __forceinline__ void write_row(const TreeParams& p, int unit, int n, int slot, bool bad,
                                           int r, float M, float L, float (&v)[4], int d0, int lane) {
   const int G = p.Hq / p.Hkv, i = r / G, g = r - i * G;
   const int b = unit / p.Hkv, h = unit - b * p.Hkv, hq = h * G + g;
   const long long tok = (long long)b * p.N + i;
   if (bad) {
-    const uint32_t half = 0xFFFFu << (lane & 16);
-    const int l = lane & 15;
+    const uint32_t group = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1) << (lane & ~(LANES - 1) & 31);
+    const int l = lane & (LANES - 1);
+    constexpr int kEach = kHeadDim / LANES;
     unsigned long long bits = p.mask ? p.mask[tok] : (i == 63 ? ~0ull : (2ull << i) - 1);
     if (n < 64) bits &= (1ull << n) - 1;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + tok * p.q_stride + (long long)hq * kHeadDim;
@@ -305,11 +305,11 @@ __device__ __forceinline__ void write_row(const TreeParams& p, int unit, int n, 
         else
           out = true;
       }
-      if (!__any_sync(half, out)) continue;
-      for (int e = 8 * l; e < 8 * l + 8; ++e)
+      if (!__any_sync(group, out)) continue;
+      for (int e = kEach * l; e < kEach * (l + 1); ++e)
         s += from16(q[e], p.q_bf16) * from16(static_cast<const uint16_t*>(p.K)[at + e], p.kv_bf16);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(half, s, o);
+      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o);
       s *= p.qk_scale;
       if (CAP) s = p.softcap * tanhf(s / p.softcap);
       if (BIAS)

@@ -25,7 +25,8 @@ namespace {
 using namespace tree;
 
 constexpr int kWindow = 2048;                  // pages whose entries are held at once
-constexpr int kAhead = 16 * kTile;             // tokens asked for in L2 ahead
+constexpr int kRunTile = 64;                   // tokens a run is cut by
+constexpr int kAhead = 16 * kRunTile;             // tokens asked for in L2 ahead
 constexpr int kObufRow = kHeadDim + 4;         // floats
 constexpr uint32_t kRowsTbl = 65536;
 constexpr uint32_t kRowsSmem = 232448;
@@ -37,6 +38,7 @@ struct Shape {
   static constexpr int kRows = 8 * NT;         // rows of a warp
   // cost of a tile by the rows: one or two warps take its tokens
   struct Cost {
+    static constexpr int kTile = kRunTile;
     __device__ __forceinline__ int operator()(int rows) const {
       return NT == 1 || rows <= kRows ? 2 : 4;
     }
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   }
   float* const obuf = reinterpret_cast<float*>(raw + (tbl + kRowsTbl - base));
   key_tables(p, tbl, tid, S::kThreads);
-  const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kTile / P;
+  const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kRunTile / P;
   const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
   const uint32_t tb = tbl + 4 * lane;
   find_run<S::kThreads>(p, c, f.scan, &f.run, typename S::Cost());
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     f.u = -1;
     while (u < U && cc < f.run.to) {
       f.unit = unit_of(p, u, typename S::Cost());
-      if (part_of(p, f.unit, f.run, c, cc, f.share)) {
+      if (share_of(p, f.unit, f.run, c, cc, kRunTile / p.P, f.share)) {
         f.u = u;
         f.before = cc;
         if (f.share.starts) p.join[c] = make_int2(u, f.share.last);
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         v[2] += ak * x.z;
         v[3] += ak * x.w;
       }
-      write_row<CAP, BIAS>(p, u, n, slot, bad, r, M, L, v, 4 * lane, lane);
+      write_row<CAP, BIAS, 32>(p, u, n, slot, bad, r, M, L, v, 4 * lane, lane);
     }
     __syncthreads();
   }
