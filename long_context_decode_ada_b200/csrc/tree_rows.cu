@@ -24,18 +24,21 @@ namespace {
 
 using namespace tree;
 
-constexpr int kWindow = 2048;                  // pages whose entries are held at once
+constexpr int kWindow = 512;                   // pages whose entries are held at once
 constexpr int kRunTile = 64;                   // tokens a run is cut by
 constexpr int kAhead = 16 * kRunTile;             // tokens asked for in L2 ahead
 constexpr int kObufRow = kHeadDim + 4;         // floats
 constexpr uint32_t kRowsTbl = 65536;
-constexpr uint32_t kRowsSmem = 232448;
+// Shared memory ends behind the tables (128 KB): what is left of the SM's
+// 256 KB is the L1 that the loads in flight pass through.
+constexpr uint32_t kRowsSmem = 131072;
 
 template <int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 ? 16 : 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;         // rows of a warp
+  static constexpr int kHalf = kWarps / 2;     // warps whose sums meet in shared memory
   // cost of a tile by the rows: one or two warps take its tokens
   struct Cost {
     static constexpr int kTile = kRunTile;
@@ -60,7 +63,8 @@ struct __align__(16) RowsFixed {
   int u;                          // the segment's unit, -1: no more
   int bad[2];                     // a drafted value lies outside fp16 (segments in turn)
   unsigned long long before;      // cost before unit u
-  float m[Shape<NT>::kWarps][Shape<NT>::kRows], l[Shape<NT>::kWarps][Shape<NT>::kRows];
+  float m[Shape<NT>::kHalf][Shape<NT>::kRows], l[Shape<NT>::kHalf][Shape<NT>::kRows];
+  __align__(16) float o[Shape<NT>::kHalf][Shape<NT>::kRows][kObufRow];
 };
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -113,7 +117,8 @@ __device__ __forceinline__ void raw_values(const uint8_t* page, uint32_t tier, i
 
 template <int NT>
 struct Frag {
-  uint32_t q[NT][16];     // B fragments of the rows
+  uint32_t q[16];         // B fragments of the rows (one block; two: in shared memory at qs)
+  uint32_t qs;
   float acc[NT][8][4];    // O^T: dims 16 mt + g (+ 8), rows 2 t, 2 t + 1
   float m[NT][2], l[NT][2];
 };
@@ -122,9 +127,13 @@ struct Frag {
 template <int NT>
 __device__ __forceinline__ void qk(float (&c)[NT][4], const Frag<NT>& f, int s, uint32_t a0,
                                    uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-    mma_16816k16_f16(c[n], a0, a1, a2, a3, f.q[n][2 * s], f.q[n][2 * s + 1]);
+  if constexpr (NT == 1) {
+    mma_16816k16_f16(c[0], a0, a1, a2, a3, f.q[2 * s], f.q[2 * s + 1]);
+  } else {
+    const uint4 q = lds128(f.qs + 1024 * s);
+    mma_16816k16_f16(c[0], a0, a1, a2, a3, q.x, q.y);
+    mma_16816k16_f16(c[NT - 1], a0, a1, a2, a3, q.z, q.w);
+  }
 }
 
 __device__ __forceinline__ uint32_t tbl1(uint32_t w, int k, uint32_t tb) {
@@ -154,13 +163,13 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
                                         float rA, float rB, float posA, float posB, uint32_t see,
                                         uint32_t (&b)[NT][2]) {
   constexpr uint32_t kAll = (1u << (4 * NT)) - 1;
-  bool raise = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int j = e & 1;
-      float x = c[n][e] * (e < 2 ? rA : rB) * sc.c[n][j];
+      float x = c[n][e] * (e < 2 ? rA : rB);
+      if (CAP || BIAS) x *= sc.c[n][j];
       if (CAP) x = fmaf(-2.0f * sc.cap, rcpf(1.0f + ex2f(x)), sc.cap);
       if (BIAS) x = fmaf(sc.slope[n][j], (e < 2 ? posA : posB) - sc.rel[n][j], x);
       c[n][e] = x;
@@ -171,17 +180,26 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
     for (int k = 0; k < 4 * NT; ++k)
       if (!((see >> k) & 1)) c[k >> 2][k & 3] = -INFINITY;
   }
+  // z = score - maximum; above kRaise (or without a maximum: not a number or
+  // infinite) the maximum rises first
+  float z[NT][4], top = -INFINITY;
+  const auto less = [&](int n, int e, float m) {
+    return CAP || BIAS ? c[n][e] - m : fmaf(c[n][e], sc.c[n][e & 1], -m);
+  };
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) raise |= fmaxf(c[n][j], c[n][j + 2]) > f.m[n][j] + kRaise;
-  if (__any_sync(0xFFFFFFFFu, raise)) {
+    for (int e = 0; e < 4; ++e) {
+      z[n][e] = less(n, e, f.m[n][e & 1]);
+      top = fmaxf(top, z[n][e]);
+    }
+  if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float a[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = fmaxf(c[n][j], c[n][j + 2]);
+        float x = fmaxf(less(n, j, 0.0f), less(n, j + 2, 0.0f));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
@@ -198,13 +216,22 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
         f.acc[n][mt][3] *= a[1];
       }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        z[n][e] = less(n, e, f.m[n][e & 1] == -INFINITY ? 0.0f : f.m[n][e & 1]);
+  } else if (see != kAll) {
+    // a row that has seen nothing so far
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c[n][e] == -INFINITY) z[n][e] = -INFINITY;
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float m0 = f.m[n][0] == -INFINITY ? 0.0f : f.m[n][0];
-    const float m1 = f.m[n][1] == -INFINITY ? 0.0f : f.m[n][1];
-    const float w0 = ex2f(c[n][0] - m0), w1 = ex2f(c[n][1] - m1);
-    const float w2 = ex2f(c[n][2] - m0), w3 = ex2f(c[n][3] - m1);
+    const float w0 = ex2f(z[n][0]), w1 = ex2f(z[n][1]), w2 = ex2f(z[n][2]), w3 = ex2f(z[n][3]);
     f.l[n][0] += w0 + w2;
     f.l[n][1] += w1 + w3;
     b[n][0] = transposed(pack_f16x2(w0, w1));
@@ -329,14 +356,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   Fixed& f = *reinterpret_cast<Fixed*>(raw);
   const uint32_t base = smem_u32(raw);
   const uint32_t tbl = (base + (uint32_t)sizeof(Fixed) + kRowsTbl - 1) & ~(kRowsTbl - 1);
-  constexpr uint32_t kObuf = S::kWarps * S::kRows * kObufRow * 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  if (tbl + kRowsTbl + kObuf > base + kRowsSmem) {
+  if (tbl + kRowsTbl > base + kRowsSmem) {
     // (the window starts at 1 KB: it fits)
     if (tid == 0) report(p.err, SKV_ERR_CUDA);
     return;
   }
-  float* const obuf = reinterpret_cast<float*>(raw + (tbl + kRowsTbl - base));
   key_tables(p, tbl, tid, S::kThreads);
   const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kRunTile / P;
   const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
@@ -384,6 +409,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     Frag<NT> fr;
     Score<NT> sc;
     sc.cap = p.softcap * 1.4426950408889634f;
+    // (two column blocks: k-step s of a row block at 1 KB steps, in the halves
+    // that the tables leave free; a warp's fragments serve all streams)
+    fr.qs = tbl + 256 * (64 + 32 * (row0 != 0) + (lane >> 3)) + 128 + 16 * (lane & 7);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
       const int r = row0 + 8 * k + g, i = r / G;
@@ -409,7 +437,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float2 a = from16x2(w[v], p.q_bf16);
-          fr.q[k][4 * y + v] = pack_f16x2(a.x * up, a.y * up);
+          const uint32_t q = pack_f16x2(a.x * up, a.y * up);
+          if (NT == 1)
+            fr.q[4 * y + v] = q;
+          else if (stream == 0)
+            sts32(fr.qs + 1024 * (2 * y + (v >> 1)) + 8 * k + 4 * (v & 1), q);
         }
       }
       // of the lane's two score columns
@@ -500,7 +532,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           raw_values(page, tier, at, P, t, lane, o);
           continue;
         }
-        float cc[NT][4] = {}, cd[NT][4] = {};
+        // (one column block: two chains of products, which halves their latency)
+        float cc[NT][4] = {}, cd[NT == 1 ? 1 : NT][4] = {};
+        float(&co)[NT][4] = NT == 1 ? cd : cc;
         float rA = 1.0f, rB = 1.0f, posA = 0.0f, posB = 0.0f;
         if (BIAS) {
           const int32_t* at_pos = p.row_pos + (first + w0 + (q >> lgp)) * P + a0;
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             qk<NT>(cc, fr, 2 * i, tbl1(wa[i], 0, tb), tbl1(wb[i], 0, tb), tbl1(wa[i], 1, tb),
                    tbl1(wb[i], 1, tb));
-            qk<NT>(cd, fr, 2 * i + 1, tbl1(wa[i], 2, tb), tbl1(wb[i], 2, tb), tbl1(wa[i], 3, tb),
+            qk<NT>(co, fr, 2 * i + 1, tbl1(wa[i], 2, tb), tbl1(wb[i], 2, tb), tbl1(wa[i], 3, tb),
                    tbl1(wb[i], 3, tb));
           }
         } else if (ti == SKV_TIER_T2) {
@@ -522,7 +556,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           for (int i = 0; i < 4; ++i) {
             qk<NT>(cc, fr, 2 * i, tbl2(o.k[0], 4 * i, tb + 128), tbl2(o.k[1], 4 * i, tb + 128),
                    tbl2(o.k[0], 4 * i + 1, tb + 128), tbl2(o.k[1], 4 * i + 1, tb + 128));
-            qk<NT>(cd, fr, 2 * i + 1, tbl2(o.k[0], 4 * i + 2, tb + 128),
+            qk<NT>(co, fr, 2 * i + 1, tbl2(o.k[0], 4 * i + 2, tb + 128),
                    tbl2(o.k[1], 4 * i + 2, tb + 128), tbl2(o.k[0], 4 * i + 3, tb + 128),
                    tbl2(o.k[1], 4 * i + 3, tb + 128));
           }
@@ -533,7 +567,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             const int ch = 16 * ((4 * i + t) ^ (4 * (g & 1)));
             const uint4 x = ldg128(a + ch), y = ldg128(a + 2048 + ch);
             qk<NT>(cc, fr, 2 * i, x.x, y.x, x.y, y.y);
-            qk<NT>(cd, fr, 2 * i + 1, x.z, y.z, x.w, y.w);
+            qk<NT>(co, fr, 2 * i + 1, x.z, y.z, x.w, y.w);
           }
         }
         if (ti != SKV_TIER_T0) {
@@ -545,10 +579,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         uint32_t see = ~0u, w[NT][2];
         if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
         see &= (1u << (4 * NT)) - 1;
+        if (NT == 1) {
 #pragma unroll
-        for (int k = 0; k < NT; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) cc[k][e] += cd[k][e];
+          for (int e = 0; e < 4; ++e) cc[0][e] += cd[0][e];
+        }
         weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, posA, posB, see, w);
         const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
         if (ti != SKV_TIER_T0) {
@@ -577,28 +611,54 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       }
     }
 
-    // the warps' sums meet
+    // the warps' sums meet: the second half's in the first half's registers,
+    // those in shared memory (a warp and the one kHalf behind it have the
+    // same rows)
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float l = fr.l[k][j];
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-        if (g == 0) {
-          f.m[warp][8 * k + 2 * t + j] = fr.m[k][j];
-          f.l[warp][8 * k + 2 * t + j] = l;
-        }
-        float* to = obuf + (warp * S::kRows + 8 * k + 2 * t + j) * kObufRow + g;
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          to[16 * mt] = fr.acc[k][mt][j];
-          to[16 * mt + 8] = fr.acc[k][mt][j + 2];
-        }
+        fr.l[k][j] += __shfl_xor_sync(0xFFFFFFFFu, fr.l[k][j], 4);
+        fr.l[k][j] += __shfl_xor_sync(0xFFFFFFFFu, fr.l[k][j], 8);
+        fr.l[k][j] += __shfl_xor_sync(0xFFFFFFFFu, fr.l[k][j], 16);
       }
     }
-    __syncthreads();
+    const int slot0 = warp < S::kHalf ? warp : warp - S::kHalf;
+    for (int half = 1; half >= 0; --half) {
+      if (warp / S::kHalf == half) {
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = 8 * k + 2 * t + j;
+            float* const to = &f.o[slot0][r][g];
+            if (half == 0) {
+              const float m1 = f.m[slot0][r], l1 = f.l[slot0][r], m0 = fr.m[k][j];
+              const float m = fmaxf(m0, m1);
+              const float a0 = m0 == m ? 1.0f : ex2f(m0 - m), a1 = m1 == m ? 1.0f : ex2f(m1 - m);
+              fr.m[k][j] = m;
+              fr.l[k][j] = fr.l[k][j] * a0 + l1 * a1;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                fr.acc[k][mt][j] = fr.acc[k][mt][j] * a0 + to[16 * mt] * a1;
+                fr.acc[k][mt][j + 2] = fr.acc[k][mt][j + 2] * a0 + to[16 * mt + 8] * a1;
+              }
+              __syncwarp();   // (every lane has read the row's m and l)
+            }
+            if (g == 0) {
+              f.m[slot0][r] = fr.m[k][j];
+              f.l[slot0][r] = fr.l[k][j];
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              to[16 * mt] = fr.acc[k][mt][j];
+              to[16 * mt + 8] = fr.acc[k][mt][j + 2];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
     if (tid == S::kThreads - 1) {
       f.bad[seg ^ 1] = 0;
       open(u + 1, f.before + f.unit.cost);
@@ -607,7 +667,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     for (int r = warp; r < R; r += S::kWarps) {
       const int blk = r >= S::kRows ? 1 : 0, lr = r - S::kRows * blk;
       float m = -INFINITY, l = 0.0f;
-      if (lane < streams) {
+      if (lane < S::kHalf / blocks) {
         const int w = blocks * lane + blk;
         m = f.m[w][lr];
         l = f.l[w][lr];
@@ -621,10 +681,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 #pragma unroll
       for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = 0; k < streams; ++k) {
+      for (int k = 0; k < S::kHalf / blocks; ++k) {
         const float ak = __shfl_sync(0xFFFFFFFFu, a, k);
-        const float4 x = *reinterpret_cast<const float4*>(
-            obuf + ((blocks * k + blk) * S::kRows + lr) * kObufRow + 4 * lane);
+        const float4 x = *reinterpret_cast<const float4*>(&f.o[blocks * k + blk][lr][4 * lane]);
         v[0] += ak * x.x;
         v[1] += ak * x.y;
         v[2] += ak * x.z;
