@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 struct SelShared {
-  uint32_t hist[3][kBins];
+  __align__(16) uint32_t hist[3][kBins];
   uint32_t scan[kSelWarps];
   uint32_t part[4];             // this block's totals, read by the cluster
   uint32_t part2[4];
@@ -65,11 +65,253 @@ __device__ __forceinline__ void cluster_sum(Cluster& cl, uint32_t* word, uint32_
   }
 }
 
+// The bin of digit d (summed over the cluster's blocks) that holds the left-th
+// highest key, and the keys above it: sm.bin, sm.above.  (Block-wide, between
+// barriers.)
+template <class Cluster>
+__device__ __forceinline__ void find_bin(Cluster& cl, SelShared& sm, int d, uint32_t left) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  // bins from the highest: thread t holds bins 4 t' .. 4 t' + 3, t' from the top
+  uint32_t c[4] = {0, 0, 0, 0};
+  const int b0 = kBins - 4 - 4 * tid;
+  const unsigned me = cl.block_rank(), blocks = cl.num_blocks();
+#pragma unroll 4
+  for (unsigned k = 0; k < blocks; ++k) {
+    // every block starts at another one's histogram: no block serves all at once
+    const unsigned r = me + k < blocks ? me + k : me + k - blocks;
+    const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(&sm.hist[d][b0], r));
+    c[3] += x.x;
+    c[2] += x.y;
+    c[1] += x.z;
+    c[0] += x.w;
+  }
+  const uint32_t tot = c[0] + c[1] + c[2] + c[3];
+  uint32_t inc = tot;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sm.scan[w] = inc;
+  __syncthreads();
+  // the totals of the warps before this one
+  uint32_t ex = lane < w ? sm.scan[lane & (kSelWarps - 1)] : 0u;
+  ex = warp_sum(ex) + inc - tot;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (ex < left && left <= ex + c[e]) {
+      sm.bin = (uint32_t)(b0 + 3 - e);
+      sm.above = ex;
+    }
+    ex += c[e];
+  }
+  __syncthreads();
+}
+
+// Select for sequences of up to 16 blocks of 512 PT positions: a thread holds
+// PT consecutive positions in registers from its loads to its stores.
+constexpr int kSelBlocks = 16;   // of a cluster (above 8 by opt-in)
+
+template <int PT, class T>
+__device__ __forceinline__ void load_run(T (&x)[PT], const T* from, int n) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (n >= PT && (reinterpret_cast<uintptr_t>(from) & 15) == 0 && PT % kVec == 0) {
+#pragma unroll
+    for (int i = 0; i < PT; i += kVec) *reinterpret_cast<uint4*>(&x[i]) = *reinterpret_cast<const uint4*>(from + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) x[i] = i < n ? from[i] : T(0);
+  }
+}
+template <int PT, class T>
+__device__ __forceinline__ void store_run(const T (&x)[PT], T* to, int n) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (n >= PT && (reinterpret_cast<uintptr_t>(to) & 15) == 0 && PT % kVec == 0) {
+#pragma unroll
+    for (int i = 0; i < PT; i += kVec) *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(&x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PT; ++i)
+      if (i < n) to[i] = x[i];
+  }
+}
+
+template <int PT>
+__global__ void __launch_bounds__(kSelThreads, 2)
+    evict_select_regs_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ __align__(16) SelShared sm;
+  __shared__ unsigned long long warp64[kSelWarps], part64;
+  cg::cluster_group cl = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const unsigned me = cl.block_rank(), blocks = cl.num_blocks();
+  const long long u = blockIdx.x / blocks;
+  const int b = (int)(u / p.Hkv);
+  const long long T = min(max((long long)p.seq_lens[b], 0ll), p.Tmax);
+  const long long keep = p.keep[b];
+  const long long lo = ((long long)me * kSelThreads + tid) * PT;   // the thread's positions
+  const int len = (int)min((long long)PT, max(0ll, p.Tmax - lo));
+  const long long base = u * p.Tmax + lo;
+
+  __align__(16) float sc[PT];
+  __align__(16) int32_t old[PT];
+  __align__(16) uint8_t ti[PT];
+  load_run<PT>(ti, p.tier + base, len);
+  load_run<PT>(sc, p.score + base, len);
+  load_run<PT>(old, p.row_of + base, len);
+  for (int i = tid; i < 3 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4*>(&sm.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
+  uint32_t cand = 0, held = 0, key[PT];
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const long long t = lo + i;
+    key[i] = score_key(sc[i]);
+    if (i >= len || t >= T || ti[i] >= kGone) continue;
+    if (t < p.sink || t >= T - p.recent || (p.protect && p.protect[base + i]))
+      held |= 1u << i;
+    else
+      cand |= 1u << i;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PT; ++i)
+    if ((cand >> i) & 1) atomicAdd(&sm.hist[0][key[i] >> 21], 1u);
+  const uint32_t n_cand = warp_sum(__popc(cand)), n_held = warp_sum(__popc(held));
+  if (lane == 0) {
+    sm.warp[0][w] = n_cand;
+    sm.warp[1][w] = n_held;
+  }
+  __syncthreads();
+  if (w == 0) {
+    const uint32_t a = warp_sum(lane < kSelWarps ? sm.warp[0][lane] : 0u);
+    const uint32_t c = warp_sum(lane < kSelWarps ? sm.warp[1][lane] : 0u);
+    if (lane == 0) {
+      sm.part[0] = a;
+      sm.part[1] = c;
+    }
+  }
+  cl.sync();
+  uint32_t before, cands, helds;
+  cluster_sum(cl, &sm.part[0], before, cands);
+  cluster_sum(cl, &sm.part[1], before, helds);
+  const long long want = keep - helds;
+  // all candidates stay, none does, or the `need` highest
+  const uint32_t need = want <= 0 ? 0u : (uint32_t)min(want, (long long)cands);
+  uint32_t stay = held | (need > 0 ? cand : 0u);
+  if (need > 0 && need < cands) {
+    uint32_t left = need, prefix = 0;
+    for (int d = 0; d < 3; ++d) {
+      const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
+      const int up = d == 1 ? 21 : 10;   // bits of the prefix from here
+      if (d > 0) {
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+          if (((cand >> i) & 1) && (key[i] >> up) == (prefix >> up))
+            atomicAdd(&sm.hist[d][(key[i] >> shift) & (d == 2 ? 1023u : 2047u)], 1u);
+        cl.sync();
+      }
+      find_bin(cl, sm, d, left);
+      prefix |= sm.bin << shift;
+      left -= sm.above;
+      __syncthreads();
+    }
+    // keys above the cut stay, and the first `left` equal to it
+    uint32_t above = 0, tie = 0;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      if (key[i] > prefix) above |= 1u << i;
+      if (key[i] == prefix) tie |= 1u << i;
+    }
+    above &= cand;
+    tie &= cand;
+    const uint32_t n = __popc(tie);
+    uint32_t inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) sm.warp[0][w] = inc;
+    __syncthreads();
+    const uint32_t x = lane < kSelWarps ? sm.warp[0][lane] : 0u;
+    uint32_t at = warp_sum(lane < w ? x : 0u) + inc - n;
+    const uint32_t all = warp_sum(x);
+    if (tid == 0) sm.part2[3] = all;
+    cl.sync();
+    uint32_t total;
+    cluster_sum(cl, &sm.part2[3], before, total);
+    at += before;
+    const uint32_t room = left > at ? left - at : 0u;
+    while ((uint32_t)__popc(tie) > room) tie ^= 0x80000000u >> __clz(tie);  // the last ones go
+    stay = held | above | tie;
+  }
+
+  // ranks of the kept tokens by tier (three counts of 21 bits)
+  unsigned long long n3 = 0;
+#pragma unroll
+  for (int i = 0; i < PT; ++i)
+    if ((stay >> i) & 1) n3 += 1ull << (21 * ti[i]);
+  unsigned long long inc3 = n3;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, inc3, o);
+    if (lane >= o) inc3 += y;
+  }
+  if (lane == 31) warp64[w] = inc3;
+  __syncthreads();
+  unsigned long long at3 = inc3 - n3, all3 = 0;
+#pragma unroll
+  for (int k = 0; k < kSelWarps; ++k) {
+    if (k < w) at3 += warp64[k];
+    all3 += warp64[k];
+  }
+  if (tid == 0) part64 = all3;
+  cl.sync();
+  unsigned long long total3 = 0;
+  for (unsigned r = 0; r < blocks; ++r) {
+    const unsigned long long x = *cl.map_shared_rank(&part64, r);
+    if (r < me) at3 += x;
+    total3 += x;
+  }
+  const uint32_t P = (uint32_t)p.P;
+  uint32_t at[3], total[3];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    at[t] = (uint32_t)(at3 >> (21 * t)) & 0x1FFFFFu;
+    total[t] = (uint32_t)(total3 >> (21 * t)) & 0x1FFFFFu;
+  }
+  // the tiers' first rows in the unit's page list
+  at[1] += (total[0] + P - 1) / P * P;
+  at[2] += (total[0] + P - 1) / P * P + (total[1] + P - 1) / P * P;
+  if (tid == 0 && me == 0)
+    for (int t = 0; t < 3; ++t) p.counts[3 * u + t] = (int32_t)total[t];
+  int32_t* const src = p.src + u * p.src_stride;
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    int row = -1;
+    const int t = ti[i];
+    ti[i] = (uint8_t)SKV_TIER_DROP;
+    if ((stay >> i) & 1) {
+      row = (int)(t == 0 ? at[0] : (t == 1 ? at[1] : at[2]));
+      at[0] += t == 0;
+      at[1] += t == 1;
+      at[2] += t == 2;
+      src[row] = old[i];
+      ti[i] = (uint8_t)t;
+    }
+    old[i] = row;
+  }
+  store_run<PT>(old, p.row_of_out + base, len);
+  store_run<PT>(ti, p.tier_out + base, len);
+  cl.sync();  // no block leaves while another reads its shared memory
+}
+
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ SelShared sm;
   cg::cluster_group cl = cg::this_cluster();
+  asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const long long u = blockIdx.x / p.clusters;
   const int b = (int)(u / p.Hkv);
@@ -140,39 +382,7 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         cl.sync();
       }
-      // bins from the highest: thread t holds bins 4 t' .. 4 t' + 3, t' from the top
-      uint32_t c[4], tot = 0;
-      const int b0 = kBins - 4 - 4 * tid;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = 0;
-      for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-        const uint4 x = *reinterpret_cast<const uint4*>(cl.map_shared_rank(&sm.hist[d][b0], r));
-        c[3] += x.x;
-        c[2] += x.y;
-        c[1] += x.z;
-        c[0] += x.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tot += c[e];
-      uint32_t inc = tot;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sm.scan[w] = inc;
-      __syncthreads();
-      uint32_t ex = inc - tot;
-      for (int k = 0; k < w; ++k) ex += sm.scan[k];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (ex < left && left <= ex + c[e]) {
-          sm.bin = (uint32_t)(b0 + 3 - e);
-          sm.above = ex;
-        }
-        ex += c[e];
-      }
-      __syncthreads();
+      find_bin(cl, sm, d, left);
       prefix |= sm.bin << shift;
       left -= sm.above;
       __syncthreads();
@@ -277,16 +487,21 @@ __global__ void __launch_bounds__(kSelThreads)
 // entry, by a scan of the units' page counts.
 __global__ void __launch_bounds__(1024) evict_plan_kernel(const __grid_constant__ EvictParams p) {
   __shared__ long long sc[32][4];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int U = p.B * p.Hkv, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int per = (U + 1023) / 1024;
+  const int per = (U + 1023) / 1024, lgP = __ffs(p.P) - 1;
   const int a = min(U, tid * per), z = min(U, a + per);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   long long n[4] = {0, 0, 0, 0};
   for (int u = a; u < z; ++u)
-    for (int t = 0; t < 3; ++t) n[t] += (p.counts[3 * u + t] + p.P - 1) / p.P;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) n[t] += (p.counts[3 * u + t] + p.P - 1) >> lgP;
   n[3] = n[0] + n[1] + n[2];
-  long long ex[4];
+  long long ex[4], tot[4];
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
     long long x = n[k];
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
@@ -295,18 +510,23 @@ __global__ void __launch_bounds__(1024) evict_plan_kernel(const __grid_constant_
     ex[k] = x - n[k];
   }
   __syncthreads();
-  long long tot[4];
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    tot[k] = 0;
-    for (int j = 0; j < 32; ++j) {
-      if (j < w) ex[k] += sc[j][k];
-      tot[k] += sc[j][k];
+    // the totals of the warps, summed up to this one
+    long long x = sc[lane][k];
+    tot[k] = x;
+    if (lane >= w) x = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+      tot[k] += __shfl_xor_sync(0xFFFFFFFFu, tot[k], o);
     }
+    ex[k] += x;
   }
   for (int u = a; u < z; ++u) {
     p.indptr_out[u] = (int32_t)ex[3];
     for (int t = 0; t < 3; ++t) {
-      const long long c = (p.counts[3 * u + t] + p.P - 1) / p.P;
+      const long long c = (p.counts[3 * u + t] + p.P - 1) >> lgP;
       if (p.tier_indptr_out) p.tier_indptr_out[3 * u + t] = (int32_t)ex[3];
       p.tbase[3 * u + t] = (int32_t)ex[t];
       ex[3] += c;
@@ -347,6 +567,7 @@ __device__ __forceinline__ uint4 load4(const uint8_t* at) {
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
   const int U = p.B * p.Hkv, P = p.P, lane = threadIdx.x & 31;
   const int oct = P >> 3, lo3 = __ffs(oct) - 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = min((long long)p.indptr_out[U], p.out_cap) << lo3;
   const long long nw = ((long long)gridDim.x * blockDim.x) >> 5;
   const long long me = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -488,34 +709,61 @@ void evict_carve(EvictParams& p, void* ws) {
 cudaError_t launch_evict(EvictParams& p, cudaStream_t stream) {
   const long long U = (long long)p.B * p.Hkv;
   if (U == 0) return cudaSuccess;
-  p.clusters = evict_clusters(p.Tmax);
-  p.chunk = (int)((p.Tmax + p.clusters - 1) / p.clusters + 15) / 16 * 16;
-  constexpr int kMaxSmem = 160 * 1024;
-  p.cached = 5ll * p.chunk <= kMaxSmem;
-  const long long smem = (p.cached ? 5ll : 1ll) * p.chunk;
-  if (smem > 200 * 1024) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(U * p.clusters));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.clusters;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  const auto blocks_of = [&](int span) {
+    int c = 1;
+    while (c < kSelBlocks && p.Tmax > (long long)span * c) c *= 2;
+    return c;
+  };
+  constexpr int kWide = kSelThreads * 16, kNarrow = kSelThreads * 8;
+  if (p.Tmax <= (long long)kWide * kSelBlocks) {
+    // 8 positions a thread where that still leaves every block its own SM
+    // (half the latency of a block's phases), else 16
+    const bool narrow = p.Tmax <= (long long)kNarrow * kSelBlocks && U * blocks_of(kNarrow) <= 148;
+    p.clusters = blocks_of(narrow ? kNarrow : kWide);
+    const auto kernel = narrow ? evict_select_regs_kernel<8> : evict_select_regs_kernel<16>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(U * p.clusters));
+    attr[0].val.clusterDim.x = (unsigned)p.clusters;
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+  } else {
+    p.clusters = evict_clusters(p.Tmax);
+    p.chunk = (int)((p.Tmax + p.clusters - 1) / p.clusters + 15) / 16 * 16;
+    constexpr int kMaxSmem = 160 * 1024;
+    p.cached = 5ll * p.chunk <= kMaxSmem;
+    const long long smem = (p.cached ? 5ll : 1ll) * p.chunk;
+    if (smem > 200 * 1024) return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             200 * 1024);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(U * p.clusters));
+    cfg.dynamicSmemBytes = (size_t)smem;
+    attr[0].val.clusterDim.x = (unsigned)p.clusters;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  }
   if (e != cudaSuccess) return e;
-  evict_plan_kernel<<<1, 1024, 0, stream>>>(p);
-  e = cudaGetLastError();
+  // plan and move: their launches overlap the grid before them, their work
+  // waits for it
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.dynamicSmemBytes = 0;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  e = cudaLaunchKernelEx(&cfg, evict_plan_kernel, p);
   if (e != cudaSuccess) return e;
-  evict_move_kernel<<<148 * 8, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  cfg.gridDim = dim3(148 * 8);
+  cfg.blockDim = dim3(256);
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
 }
 
 }  // namespace skv
