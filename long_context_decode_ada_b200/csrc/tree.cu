@@ -7,34 +7,35 @@
 //
 // Work split: the page list is cut into runs of about equal cost, one per
 // CTA; a run is a list of segments (a unit = (sequence, kv head), or a part
-// of one), a segment a list of tiles of 128 tokens (128 / P pages), the
+// of one), a segment a list of tiles of 64 tokens (64 / P pages), the
 // unit's drafted tokens being one more tile behind its pages.  A unit that
 // lies in one run is finished there; the parts of a unit that several runs
 // share go to the workspace as (m, l, O) and a second grid joins them.
 //
 // Roles of a CTA (one per SM):
-//   planner (1 warp)   turns the page list into tile descriptors (a ring of 16
+//   planner (1 warp)   turns the page list into tile descriptors (a ring of 32
 //                      in shared memory), checks ids and headers, and asks for
 //                      the pages' bytes in L2 (bulk prefetch)
-//   decode (8 warps)   two teams of 4 take the tiles in turn, a warp 32 rows
-//                      in steps of 8: codes to fp16 keys by gathers from a
-//                      replicated table (one conflict-free wavefront a
-//                      gather), int8 values to fp16, both written as swizzled
-//                      operand tiles (64 KB a tile, two in flight).  The loads
-//                      of the rows 16 further on are issued as soon as the
-//                      registers of the present ones are free
+//   copier (1 warp)    brings the pages into shared memory by bulk copies, five
+//                      coded tiles (or one dense and two coded) in flight: with
+//                      the shared memory that the tiles take the L1 is too
+//                      small for as many loads in flight
+//   decode (8 warps)   two teams of 4 take the tiles in turn, a warp 16 rows:
+//                      codes to fp16 keys by gathers from a replicated table
+//                      (one conflict-free wavefront a gather), int8 values to
+//                      fp16, both written as swizzled operand tiles (32 KB a
+//                      tile, three in flight)
 //   mma (2 warps)      S = Q K^T, and O += P V, by tcgen05.mma (fp16, fp32
-//                      accumulators), 64 tokens a job; Q and P are read from
+//                      accumulators), a tile a job; Q and P are read from
 //                      tensor memory, so that shared memory feeds K and V only
 //   softmax (8 warps)  two groups of 4, one per stream: scores from tensor
 //                      memory, running maximum and sum, weights back as fp16
 //
-// The two streams have accumulators of their own.  With at most 128 rows each
-// takes one half of every tile, and with at most 64 rows the rows are
-// entered twice, each copy handling half of a job's columns: every lane of
+// The two streams have accumulators of their own.  With at most 128 rows they
+// take the tiles in turn, and with at most 64 rows the rows are entered twice, each copy handling half of a job's columns: every lane of
 // tensor memory then has work, and the copies' sums meet at the segment's
 // end.  With more than 128 rows stream b has the rows
-// 128 b .. 128 b + 127 of both halves.  The running maximum is raised (and O
+// 128 b .. 128 b + 127 of every tile.  The running maximum is raised (and O
 // rescaled) only when a score passes it by more than 2^8, so weights stay
 // within fp16.
 //
@@ -56,18 +57,22 @@ namespace {
 
 using namespace tree;
 
-constexpr int kTile = 128;           // tokens of a tile
-constexpr int kJob = 64;             // tokens of a job (a tile's half)
-constexpr int kStages = 2;           // tiles of keys and values in flight, one a team
-constexpr int kRing = 16;            // tile descriptors
-constexpr int kBatch = 4;            // tiles the planner publishes at once
-constexpr int kTeamWarps = 4;        // decode warps of a team (32 rows each)
+constexpr int kTile = 64;            // tokens of a tile (a job of the products)
+constexpr int kStages = 3;           // tiles of keys and values in flight
+constexpr int kRing = 32;            // tile descriptors
+constexpr int kBatch = 8;            // tiles the planner publishes at once
+constexpr int kTeams = 2;            // of decode warps, taking the tiles in turn
+constexpr int kTeamWarps = 4;        // 16 rows each
 constexpr int kSoftWarps = 8;
-constexpr int kDecodeWarps = kStages * kTeamWarps;
-constexpr int kPlanner = kSoftWarps + kDecodeWarps;
-constexpr int kMmaS = kPlanner + 1, kMmaO = kPlanner + 2;
+constexpr int kDecodeWarps = kTeams * kTeamWarps;
+constexpr int kPlanner = kSoftWarps + kDecodeWarps, kCopier = kPlanner + 1;
+constexpr int kMmaS = kPlanner + 2;  // (and the warp behind it)
 constexpr int kThreads = (kSoftWarps + kDecodeWarps + 4) * 32;
 constexpr int kBufRow = 36;          // floats of a row of the output buffer (32 dims)
+// pages as they are stored: slots of one coded tile (a dense tile takes three)
+constexpr uint32_t kRawSlot = kTile * 196 + 4 * kHdrBytes;
+constexpr int kRawSlots = 5, kRawTiles = 8;
+static_assert(kTile * 512 + 4 * kHdrBytes <= 3 * kRawSlot && kRawSlot % 16 == 0, "raw slots");
 
 enum : uint32_t { kFirst = 1, kLast = 2, kDraft = 4, kEnd = 8 };
 
@@ -76,18 +81,20 @@ constexpr uint32_t kColQ = 0, kColP = 64, kColS = 128, kColO = 256;
 
 struct __align__(16) Part {     // 16 rows of a tile
   unsigned long long page;      // address (tier < 3)
-  uint16_t at, rows;            // first row within the page, rows in use
-  uint32_t tier;                // 3: no row
+  uint32_t off;                 // of the page's bytes in the tile's raw bytes
+  uint8_t at, rows, tier;       // first row within the page, rows in use; tier 3: none
+  uint8_t zero;
 };
 
 struct __align__(16) Tile {
-  Part part[8];
-  unsigned long long valid[2];  // of the halves: bit c: column c holds a token
+  Part part[4];
+  unsigned long long valid;     // bit c: column c holds a token
   int unit, n;                  // (sequence, kv head) and its drafted tokens
   uint32_t flags;
   int first;                    // index of the first page in the page list
   int slot;                     // partial slot, -1: the unit lies in this run
   int bad;                      // a drafted value lies outside fp16
+  uint32_t bytes;               // raw bytes
 };
 
 struct __align__(16) Fixed {
@@ -95,6 +102,8 @@ struct __align__(16) Fixed {
   unsigned long long sfull[2], sfree[2], pfull[2], odone[2];
   unsigned long long qfull, sync, fin[2];
   unsigned long long dfull[kRing / kBatch], rfree[kRing / kBatch];
+  unsigned long long rawfull[kRawTiles], rawfree[kRawTiles];
+  uint32_t raw[kRawTiles];      // where a tile's raw bytes lie
   unsigned long long scan[kThreads / 32];
   Run run;
   int abort;
@@ -102,23 +111,32 @@ struct __align__(16) Fixed {
   __align__(16) Tile ring[kRing];
   __align__(16) float pos[kStages][kTile];   // positions (from the unit's first q_pos)
   __align__(16) float cs[kStages][kTile];    // drafted keys: what a score is scaled by
+};
+
+// behind the output buffer
+struct Sums {
   float m[2][128], l[2][128];
 };
 
-// Shared memory: [fixed block, output buffer][keys 0][tables][values 0, keys 1,
-// values 1]; the tables start on a 64 KB boundary.
-constexpr uint32_t kTblBytes = 65536;
+// Shared memory: [fixed block][stages][T2 table][T1 table][raw slots][output
+// buffer, sums]; the stages start on an 8 KB boundary.  Entry e of a table
+// (T1: the code byte; T2: angle | share << 4) is at 128 e, in 32 copies of 4
+// bytes (copy L is read by lane L), so that a warp's gathers never conflict.
 constexpr uint32_t kOperand = kTile * 256;                // a tile's keys or values
-constexpr uint32_t kBufBytes = 128 * kBufRow * 4;
-constexpr uint32_t kAtBuf = (sizeof(Fixed) + 127) / 128 * 128;
-constexpr uint32_t kLowBytes = kAtBuf + kBufBytes + kOperand;
+constexpr uint32_t kTbl2 = 64 * 128, kTbl1 = 256 * 128;
+constexpr uint32_t kAtTbl2 = kStages * 2 * kOperand, kAtTbl1 = kAtTbl2 + kTbl2;
+constexpr uint32_t kAtRaw = kAtTbl1 + kTbl1;
+constexpr uint32_t kAtBuf = kAtRaw + kRawSlots * kRawSlot;
+constexpr uint32_t kAtSums = kAtBuf + 128 * kBufRow * 4;
+constexpr uint32_t kHighBytes = kAtSums + sizeof(Sums);
 constexpr uint32_t kSmemBytes = 232448;
-static_assert(kLowBytes + 1024 <= 65536, "the tables start at 64 KB");
-__device__ __forceinline__ uint32_t keys_at(uint32_t tbl, uint32_t stage) {
-  return stage == 0 ? tbl - kOperand : tbl + kTblBytes + kOperand;
+static_assert(sizeof(Fixed) + 1024 <= 8192, "the stages start at 8 KB");
+static_assert(kHighBytes + 8192 <= kSmemBytes + 1024 && kAtTbl2 % 8192 == 0 && kAtBuf % 16 == 0, "layout");
+__device__ __forceinline__ uint32_t keys_at(uint32_t base, uint32_t stage) {
+  return base + stage * 2 * kOperand;
 }
-__device__ __forceinline__ uint32_t values_at(uint32_t tbl, uint32_t stage) {
-  return tbl + kTblBytes + (stage == 0 ? 0 : 2 * kOperand);
+__device__ __forceinline__ uint32_t values_at(uint32_t base, uint32_t stage) {
+  return base + stage * 2 * kOperand + kOperand;
 }
 
 // ------------------------------------------------------------ tensor memory
@@ -177,12 +195,12 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, unsigned long lon
 }
 
 // fp16 A and B, fp32 D, M = 128; B's values contiguous along k, or along n
-constexpr uint32_t kIdescS = (1u << 4) | ((kJob / 8) << 17) | (8u << 24);
+constexpr uint32_t kIdescS = (1u << 4) | ((kTile / 8) << 17) | (8u << 24);
 constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((kHeadDim / 8) << 17) | (8u << 24);
 
 // Operand tiles in shared memory: rows of 128 bytes, their 16-byte chunks
 // permuted by the row's low three bits (128-byte swizzle), groups of 8 rows
-// 1024 bytes apart; the second 64 dims follow 16 KB behind.
+// 1024 bytes apart; the second 64 dims follow 8 KB behind.
 constexpr uint32_t kHalfDims = kTile * 128;   // from dims 0-63 of a tile to dims 64-127
 constexpr uint32_t kDescHigh = (1024 / 16) | (1u << 14) | (2u << 29);
 constexpr uint32_t kDescKeys = 1u << 16, kDescValues = (kHalfDims / 16) << 16;
@@ -223,7 +241,7 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
 
 // More than 128 rows cost half as much again (decoded once, multiplied twice).
 struct RowsCost {
-  static constexpr int kTile = 128;
+  static constexpr int kTile = 64;
   __device__ __forceinline__ int operator()(int rows) const { return rows > 128 ? 3 : 2; }
 };
 static_assert(RowsCost::kTile == kTile, "tiles");
@@ -231,7 +249,7 @@ static_assert(RowsCost::kTile == kTile, "tiles");
 // ---------------------------------------------------------------- the planner
 __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int lane) {
   const int U = p.B * p.Hkv, ipp = kTile / p.P, lgP = __ffs(p.P) - 1;
-  const int mine = lane >> 3, part = lane & 7;      // the lane's tile of a batch, its 16 rows
+  const int mine = lane >> 2, part = lane & 3;      // the lane's tile of a batch, its 16 rows
   const int pg = 16 * part >> lgP, at = 16 * part & (p.P - 1);
   const Run run = f.run;
   int u = run.unit, k = 0, kend = 0, slot = -1, ends = 0;
@@ -240,7 +258,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
   int2 join = make_int2(-1, 0);
   Unit x = {};
   // (an end for each team)
-  for (int batch = 0; ends < kStages; ++batch) {
+  for (int batch = 0; ends < kTeams; ++batch) {
     if (batch >= 2 &&
         !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f, p.err))
       break;
@@ -299,11 +317,10 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
       }
     }
     // a lane per 16 rows
-    Part o;
-    o.page = 0;
-    o.at = (uint16_t)at;
-    o.rows = 0;
+    Part o = {};
+    o.at = (uint8_t)at;
     o.tier = 3;
+    uint32_t bytes = 0;          // of the page, at its first part
     if (pg < t_np) {
       const uint32_t id = p.ids[t_first + pg], sl = id & 0x3FFFFFFFu;
       const int t = (int)(id >> 30);
@@ -318,144 +335,172 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
           report(p.err, SKV_ERR_CORRUPT);
         } else if (rows > at) {
           o.page = reinterpret_cast<unsigned long long>(a);
-          o.rows = (uint16_t)min(rows - at, 16);
-          o.tier = (uint32_t)t;
+          o.rows = (uint8_t)min(rows - at, 16);
+          o.tier = (uint8_t)t;
+          if (at == 0) bytes = (uint32_t)(kHdrBytes + p.P * tier_row_bytes(t));
         }
       }
     }
-    unsigned long long valid = (unsigned long long)((1u << o.rows) - 1) << (16 * (part & 3));
+    // where the part's page lies behind the tile's pages before it
+    uint32_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t x = __shfl_sync(0xFFFFFFFFu, bytes, (lane & ~3) + k);
+      if (k < part - (at >> 4)) o.off += x;
+      sum += x;
+    }
+    unsigned long long valid = (unsigned long long)((1u << o.rows) - 1) << (16 * part);
     valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 1);
     valid |= __shfl_xor_sync(0xFFFFFFFFu, valid, 2);
     Tile& d = f.ring[(batch & 3) * kBatch + mine];
     d.part[part] = o;
-    if ((part & 3) == 0) {
-      if (t_flags & kDraft) valid = part ? 0ull : (t_n >= 64 ? ~0ull : (1ull << t_n) - 1);
-      d.valid[part >> 2] = valid;
-    }
     if (part == 0) {
+      d.valid = (t_flags & kDraft) ? (t_n >= 64 ? ~0ull : (1ull << t_n) - 1) : valid;
       d.unit = t_unit;
       d.n = t_n;
       d.flags = t_flags;
       d.first = (int)t_first;
       d.slot = t_slot;
       d.bad = 0;
+      d.bytes = sum;
     }
     warp_arrive(f.dfull[batch & 3]);
   }
   if (lane == 0) p.join[c] = join;
 }
 
-// ----------------------------------------------------------------- the decode
-// Lane (t, g) = 4 t + g of a warp: row t of its 8, key dims 32 i + 8 g + 0..7.
-// A part's 16 rows in registers (dense rows are loaded when they are used).
-struct Rows {
-  uint4 k[2], v[4];
-  uint32_t r[2], s[2];   // radius; scales of value rows 2 t4, 2 t4 + 1
-  const uint8_t* page;   // behind the header
-  uint32_t tier;
-  int at, rows;
-};
-
-__device__ __forceinline__ void load_part(const Part& x, int P, int lane, Rows& o) {
-  const int t = lane >> 2, g = lane & 3;
-  o.tier = x.tier;
-  o.at = x.at;
-  o.rows = x.rows;
-  o.page = reinterpret_cast<const uint8_t*>(x.page) + kHdrBytes;
-  if (o.tier == SKV_TIER_T1) {
-    const uint8_t* const k = o.page + 2 * P + 64 * (o.at + t) + 16 * g;
-    const uint8_t* const v = o.page + 68 * P + 128 * o.at + 16 * lane;
-    const uint8_t* const r = o.page + 2 * (o.at + t);
-    const uint8_t* const s = o.page + 66 * P + 2 * o.at + 4 * g;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      o.k[e] = ldg128(k + 512 * e);
-      o.r[e] = *reinterpret_cast<const uint16_t*>(r + 16 * e);
-      o.v[2 * e] = ldg128(v + 1024 * e);
-      o.v[2 * e + 1] = ldg128(v + 1024 * e + 512);
-      o.s[e] = *reinterpret_cast<const uint32_t*>(s + 16 * e);
+// ----------------------------------------------------------------- the copier
+// Brings the tiles' pages into the raw slots by bulk copies, whole pages in
+// the order of the tiles.
+__device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t base, int lane) {
+  uint32_t used = 0;                 // slots of the last 8 tiles, 4 bits each
+  int head = 0, held = 0, pos = 0;   // first tile not given back, slots in use, next slot
+  // the copies in flight end before the block does
+  const auto drain = [&](int t) {
+    int none = 0;
+    for (; head < t; ++head) mbar_wait_bounded(smem_u32(&f.rawfull[head & 7]), (head >> 3) & 1, &none);
+  };
+  for (int t = 0;; ++t) {
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err)) {
+      drain(t);
+      return;
     }
-  } else if (o.tier == SKV_TIER_T2) {
-    const uint8_t* const k = o.page + 2 * P + 48 * (o.at + t);
-    const uint8_t* const v = o.page + 52 * P + 128 * o.at + 16 * lane;
-    const uint8_t* const r = o.page + 2 * (o.at + t);
-    const uint8_t* const s = o.page + 50 * P + 2 * o.at + 4 * g;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint2 n = *reinterpret_cast<const uint2*>(k + 384 * e + 8 * g);
-      o.k[e].x = n.x;
-      o.k[e].y = n.y;
-      o.k[e].z = *reinterpret_cast<const uint32_t*>(k + 384 * e + 32 + 4 * g);
-      o.r[e] = *reinterpret_cast<const uint16_t*>(r + 16 * e);
-      o.v[2 * e] = ldg128(v + 1024 * e);
-      o.v[2 * e + 1] = ldg128(v + 1024 * e + 512);
-      o.s[e] = *reinterpret_cast<const uint32_t*>(s + 16 * e);
+    const Tile& d = f.ring[t & (kRing - 1)];
+    if (d.flags & kEnd) return;
+    const uint32_t bytes = d.bytes;
+    int need = (int)((bytes + kRawSlot - 1) / kRawSlot), skip = 0;
+    if (pos + need > kRawSlots) {
+      skip = kRawSlots - pos;
+      pos = 0;
     }
+    while (held + need + skip > kRawSlots || t - head >= kRawTiles) {
+      if (!warp_wait(f.rawfree[head & 7], (head >> 3) & 1, f, p.err)) {
+        drain(t);
+        return;
+      }
+      held -= (int)(used >> (4 * (head & 7))) & 15;
+      ++head;
+    }
+    const int x = t & 7;
+    used = (used & ~(15u << (4 * x))) | ((uint32_t)(need + skip) << (4 * x));
+    held += need + skip;
+    const uint32_t to = base + kAtRaw + pos * kRawSlot, bar = smem_u32(&f.rawfull[x]);
+    if (lane == 0) {
+      f.raw[x] = to;
+      if (bytes)
+        mbar_arrive_expect_tx(bar, bytes);
+      else
+        mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (lane < 4) {
+      const Part o = d.part[lane];
+      if (o.tier < 3 && o.at == 0)
+        bulk_g2s(to + o.off, reinterpret_cast<const void*>(o.page),
+                 (uint32_t)(kHdrBytes + p.P * tier_row_bytes(o.tier)), bar);
+    }
+    __syncwarp();
+    pos += need;
+    if (pos == kRawSlots) pos = 0;
   }
 }
 
-// Address of a code's entry in the lane's copy: byte k of w as the second
-// byte of the table's address (T1); T2 pair j of nibbles nw, crumbs cw.
+// ----------------------------------------------------------------- the decode
+// Lane (t, g) = 4 t + g of a warp: row t of its 8, key dims 32 i + 8 g + 0..7.
+// Address of a code's entry in the lane's copy: byte k of w (T1); T2 pair j of
+// nibbles nw, crumbs cw (the T2 table's address bits are disjoint from the
+// index bits).
 __device__ __forceinline__ uint32_t t1_at(uint32_t w, int k, uint32_t tb) {
-  return __byte_perm(w, tb, 0x7604u | (uint32_t)(k << 4));
+  return tb + (__byte_perm(w, 0u, 0x4440u | (uint32_t)k) << 7);
 }
 __device__ __forceinline__ uint32_t t2_at(uint32_t nw, uint32_t cw, int j, uint32_t tb) {
-  const int sn = 4 * (j & 7) - 8, sc = 2 * j - 12;
+  const int sn = 4 * (j & 7) - 7, sc = 2 * j - 11;
   const uint32_t xn = sn >= 0 ? (nw >> sn) : (nw << -sn);
   const uint32_t xc = sc >= 0 ? (cw >> sc) : (cw << -sc);
-  return (xn & 0xF00u) | (xc & 0x3000u) | tb;
+  return (xn & 0x780u) | (xc & 0x1800u) | tb;
 }
 
-// A part's keys -> fp16 rows T0 .. T0 + 15 of the tile at kb.
-__device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, int lane,
-                                           uint32_t tb) {
+// A part's keys (page: behind the header, in shared memory) -> fp16 rows
+// T0 .. T0 + 15 of the tile at kb.
+__device__ __forceinline__ void store_keys(uint32_t page, uint32_t tier, int at0, int P, uint32_t kb,
+                                           int T0, int lane, uint32_t base) {
   const int t = lane >> 2, g = lane & 3, odd = t & 1;
   // odd rows go through their chunks in the order 1 0 3 2, which spreads a
   // quarter warp's stores over all banks
   const uint32_t row = kb + (uint32_t)(T0 + t) * 128;
   const uint32_t at[2] = {row + (((4 * odd + g) ^ t) << 4), row + (((4 * (odd ^ 1) + g) ^ t) << 4)};
-  if (o.tier == SKV_TIER_T1) {
+  if (tier == SKV_TIER_T1) {
+    const uint32_t tb = base + kAtTbl1 + 4 * lane;
+    const uint32_t from = page + 2 * P + 64 * (at0 + t) + 16 * g, rad = page + 2 * (at0 + t);
+    uint4 k[2];
+    uint32_t r[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 k = o.k[h];
-      const uint32_t r = o.r[h] | (o.r[h] << 16);
-      const uint32_t w[4] = {odd ? k.y : k.x, odd ? k.x : k.y, odd ? k.w : k.z, odd ? k.z : k.w};
+      k[h] = lds128(from + 512 * h);
+      r[h] = lds16(rad + 16 * h);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t r2 = r[h] | (r[h] << 16);
+      const uint32_t w[4] = {odd ? k[h].y : k[h].x, odd ? k[h].x : k[h].y, odd ? k[h].w : k[h].z,
+                             odd ? k[h].z : k[h].w};
       uint32_t x[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = lds32(t1_at(w[e >> 2], e & 3, tb));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h,
-               make_uint4(hmul2(x[4 * e], r), hmul2(x[4 * e + 1], r), hmul2(x[4 * e + 2], r),
-                          hmul2(x[4 * e + 3], r)));
+               make_uint4(hmul2(x[4 * e], r2), hmul2(x[4 * e + 1], r2), hmul2(x[4 * e + 2], r2),
+                          hmul2(x[4 * e + 3], r2)));
     }
-  } else if (o.tier == SKV_TIER_T2) {
-    const uint32_t tb2 = tb + 128;
+  } else if (tier == SKV_TIER_T2) {
+    const uint32_t tb = base + kAtTbl2 + 4 * lane;
+    const uint32_t from = page + 2 * P + 48 * (at0 + t), rad = page + 2 * (at0 + t);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t r = o.r[h] | (o.r[h] << 16);
+      const uint2 k = lds64(from + 384 * h + 8 * g);
+      const uint32_t z = lds32(from + 384 * h + 32 + 4 * g);
+      const uint32_t r = lds16(rad + 16 * h), r2 = r | (r << 16);
       // pairs 4 i .. 4 i + 3: nibbles and crumbs 4 i + b; odd rows swap halves
       const int sw = 16 * odd;
-      const uint32_t n[2] = {__funnelshift_r(o.k[h].x, o.k[h].x, sw),
-                             __funnelshift_r(o.k[h].y, o.k[h].y, sw)};
-      const uint32_t z = o.k[h].z;
+      const uint32_t n[2] = {__funnelshift_r(k.x, k.x, sw), __funnelshift_r(k.y, k.y, sw)};
       const uint32_t cw = odd ? ((z >> 8) & 0x00FF00FFu) | ((z << 8) & 0xFF00FF00u) : z;
       uint32_t x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = lds32(t2_at(n[e >> 3], cw, e, tb2));
+      for (int e = 0; e < 16; ++e) x[e] = lds32(t2_at(n[e >> 3], cw, e, tb));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h,
-               make_uint4(hmul2(x[4 * e], r), hmul2(x[4 * e + 1], r), hmul2(x[4 * e + 2], r),
-                          hmul2(x[4 * e + 3], r)));
+               make_uint4(hmul2(x[4 * e], r2), hmul2(x[4 * e + 1], r2), hmul2(x[4 * e + 2], r2),
+                          hmul2(x[4 * e + 3], r2)));
     }
-  } else if (o.tier == SKV_TIER_T0) {
-    const uint8_t* a = o.page + 256 * (o.at + t);
-#pragma unroll 1
+  } else if (tier == SKV_TIER_T0) {
+    const uint32_t from = page + 256 * (at0 + t);
+#pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = ldg128(a + 2048 * h + 16 * ((4 * (e ^ odd) + g) ^ (4 * odd)));
+      for (int e = 0; e < 4; ++e) x[e] = lds128(from + 2048 * h + 16 * ((4 * (e ^ odd) + g) ^ (4 * odd)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) sts128(at[e & 1] + (e >> 1) * kHalfDims + 1024 * h, x[e]);
     }
@@ -469,22 +514,30 @@ __device__ __forceinline__ void store_keys(const Rows& o, uint32_t kb, int T0, i
 // A part's values -> fp16.  The tile's columns are a permutation of the
 // dims that a lane of the pages' fragment order holds together: column
 // 64 h + 8 g + 2 m + hi is dim 64 h + 16 m + 8 hi + g.
-__device__ __forceinline__ void store_values(const Rows& o, int P, uint32_t vb, int T0, int lane) {
+__device__ __forceinline__ void store_values(uint32_t page, uint32_t tier, int at0, int rows, int P,
+                                             uint32_t vb, int T0, int lane) {
   const int g = lane >> 2, a = 2 * (lane & 3), b = a + 1;
   const uint32_t ra = vb + (uint32_t)(T0 + a) * 128 + ((g ^ a) << 4);
   const uint32_t rb = vb + (uint32_t)(T0 + b) * 128 + ((g ^ b) << 4);
-  if (o.tier == SKV_TIER_T1 || o.tier == SKV_TIER_T2) {
+  if (tier == SKV_TIER_T1 || tier == SKV_TIER_T2) {
     // v + 128 as the low byte of 1024 + x in fp16, less 1152 (exact), times
     // the scale (rounded once); rows that are not there get the scale 0
     const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t sec = page + (tier == SKV_TIER_T1 ? 66 : 50) * P;
+    const uint32_t from = sec + 2 * P + 128 * at0 + 16 * lane;
+    uint4 z[4];
+    uint32_t s[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = lds128(from + 512 * e);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) s[e] = lds32(sec + 2 * at0 + 2 * a + 16 * e);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t sa = a + 8 * e < o.rows ? __byte_perm(o.s[e], 0u, 0x1010) : 0u;
-      const uint32_t sb = b + 8 * e < o.rows ? __byte_perm(o.s[e], 0u, 0x3232) : 0u;
+      const uint32_t sa = a + 8 * e < rows ? __byte_perm(s[e], 0u, 0x1010) : 0u;
+      const uint32_t sb = b + 8 * e < rows ? __byte_perm(s[e], 0u, 0x3232) : 0u;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 z = o.v[2 * e + h];
-        const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+        const uint32_t w[4] = {z[2 * e + h].x, z[2 * e + h].y, z[2 * e + h].z, z[2 * e + h].w};
         uint32_t p[4], q[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -500,17 +553,14 @@ __device__ __forceinline__ void store_values(const Rows& o, int P, uint32_t vb, 
         sts128(rb + h * kHalfDims + 1024 * e, make_uint4(q[0], q[1], q[2], q[3]));
       }
     }
-  } else if (o.tier == SKV_TIER_T0) {
-    const uint8_t* from = o.page + 256 * (P + o.at) + 16 * lane;
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-      const bool ua = a + 8 * e < o.rows, ub = b + 8 * e < o.rows;
-      uint4 z[4];
+  } else if (tier == SKV_TIER_T0) {
+    const uint32_t from = page + 256 * (P + at0) + 16 * lane;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) z[h] = ldg128(from + 2048 * e + 512 * h);
+    for (int e = 0; e < 2; ++e) {
+      const bool ua = a + 8 * e < rows, ub = b + 8 * e < rows;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 x = z[2 * h], y = z[2 * h + 1];
+        const uint4 x = lds128(from + 2048 * e + 1024 * h), y = lds128(from + 2048 * e + 1024 * h + 512);
         uint4 p = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
                              __byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410));
         uint4 q = make_uint4(__byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632),
@@ -590,73 +640,70 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
 }
 
 template <bool BIAS>
-__device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t tbl, int wd,
+__device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t base, int wd,
                                             int lane) {
-  const int w = wd & (kTeamWarps - 1), stage = wd / kTeamWarps, P = p.P;
-  const uint32_t tb = tbl + 4 * lane, kb = keys_at(tbl, stage), vb = values_at(tbl, stage);
-  int t = stage;
-  uint32_t turn = 1;   // of the stage: parity of the tile before
+  const int w = wd & (kTeamWarps - 1), P = p.P, T0 = 16 * w;
+  int t = wd / kTeamWarps;
+  uint32_t stage = t, use = 0;   // of tile t: its stage, the stage's tiles before
   if (!warp_wait(f.dfull[0], 0, f, p.err)) return;
-  uint32_t flags = f.ring[t].flags;
-  Rows o = {}, next = {};
-  load_part(f.ring[t].part[2 * w], P, lane, o);
-  while (!(flags & kEnd)) {
+  for (;;) {
     Tile& d = f.ring[t & (kRing - 1)];
+    const uint32_t flags = d.flags;
+    if (flags & kEnd) return;
+    const Part x = d.part[w];
+    const uint32_t kb = keys_at(base, stage), vb = values_at(base, stage);
+    const int y = t & (kRawTiles - 1);
+    if (!warp_wait(f.rawfull[y], (t / kRawTiles) & 1, f, p.err)) return;
+    const uint32_t page = f.raw[y] + x.off + kHdrBytes;
+    if (use > 0 && !warp_wait(f.kempty[stage], (use - 1) & 1, f, p.err)) return;
     const bool draft = (flags & kDraft) != 0;
-#pragma unroll 1
-    for (int u = 0; u < 2; ++u) {
-      const int T0 = 32 * w + 16 * u;
-      // the next part's loads go out before this part's conversion
-      if (u == 0) {
-        load_part(d.part[2 * w + 1], P, lane, next);
-        if (t >= kStages && !warp_wait(f.kempty[stage], turn, f, p.err)) return;
-      } else {
-        const int t2 = t + kStages;
-        if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f, p.err))
-          return;
-        flags = f.ring[t2 & (kRing - 1)].flags;
-        load_part(f.ring[t2 & (kRing - 1)].part[2 * w], P, lane, next);
-      }
-      if (!draft) store_keys(o, kb, T0, lane, tb);
-      if (u == 0 && t >= kStages && !warp_wait(f.vempty[stage], turn, f, p.err)) return;
+    if (!draft) store_keys(page, x.tier, x.at, P, kb, T0, lane, base);
+    if (BIAS || draft) {
+      // (positions and scales are in use until the stage's values are free)
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, p.err)) return;
       if (BIAS && lane < 16) {
         const long long b = d.unit / p.Hkv;
         const int q0 = p.q_pos[b * p.N];
         int q = q0;
         if (draft) {
           if (T0 + lane < d.n) q = p.q_pos[b * p.N + T0 + lane];
-        } else if (lane < o.rows) {
+        } else if (lane < x.rows) {
           q = p.row_pos[(long long)d.first * P + T0 + lane];  // (a tile's pages follow each other)
         }
         f.pos[stage][T0 + lane] = (float)(q - q0);
       }
-      if (u == 1 && !draft) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        warp_arrive(f.kfull[stage]);
-      }
-      if (!draft) {
-        store_values(o, P, vb, T0, lane);
-      } else {
+      if (draft) {
 #pragma unroll 1
         for (int e = 0; e < 16; e += 8) store_draft(p, d, kb, vb, f.cs[stage], &d.bad, T0 + e, lane);
       }
-      o = next;
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (draft) warp_arrive(f.kfull[stage]);
+    warp_arrive(f.kfull[stage]);
+    if (!draft) {
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, p.err)) return;
+      store_values(page, x.tier, x.at, x.rows, P, vb, T0, lane);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     warp_arrive(f.vfull[stage]);
-    t += kStages;
-    turn ^= 1;
+    if (lane == 0) mbar_arrive(smem_u32(&f.rawfree[y]));
+    const int t2 = t + kTeams;
+    if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f, p.err)) return;
+    t = t2;
+    stage += kTeams;
+    if (stage >= kStages) {
+      stage -= kStages;
+      ++use;
+    }
   }
 }
 
 // ------------------------------------------------------------------- the MMAs
 // S = Q K^T of every job, as soon as the keys are there and the stream's
 // scores are read (two blocks: its weights used).
-__device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32_t tbl, uint32_t tm) {
+__device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
   const int most = 128 * p.Hkv;       // n * Hq above it: two blocks
   uint32_t turn = 3;                  // bit s: parity of stream s's job before
-  uint32_t segs = 0;
+  uint32_t segs = 0, stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
     if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
@@ -667,38 +714,41 @@ __device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32
       if (!warp_wait(f.qfull, segs & 1, f, p.err)) return;
       ++segs;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
+      s = 0;
     }
-    const uint32_t stage = t & 1;
-    if (!warp_wait(f.kfull[stage], (t >> 1) & 1, f, p.err)) return;
-    const uint32_t keys = kDescKeys | (keys_at(tbl, stage) >> 4);
-    const int jobs = two ? 4 : 2;
+    if (!warp_wait(f.kfull[stage], use & 1, f, p.err)) return;
+    const uint32_t low = kDescKeys | (keys_at(base, stage) >> 4);
 #pragma unroll 1
-    for (int y = 0; y < jobs; ++y) {
-      const uint32_t s = y & 1;
+    for (int y = two ? 1 : 0; y >= 0; --y) {
       if (!warp_wait(f.sfree[s], (turn >> s) & 1, f, p.err)) return;
       if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f, p.err)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t low = keys + (two ? y >> 1 : y) * (kJob * 128 / 16);
         const uint32_t a = tm + kColQ + (two ? 64 * s : 0), o = tm + kColS + 64 * s;
 #pragma unroll
         for (int k = 0; k < kHeadDim / 16; ++k)
           tc_mma(o, a + 8 * k, operand(low + (k >> 2) * (kHalfDims / 16) + (k & 3) * 2), kIdescS,
                  k > 0);
         tc_commit(smem_u32(&f.sfull[s]));
-        if (y == jobs - 1) tc_commit(smem_u32(&f.kempty[stage]));
+        if (y == 0) tc_commit(smem_u32(&f.kempty[stage]));
       }
       __syncwarp();
+      s ^= 1;
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      ++use;
     }
   }
 }
 
 // O += P V of every job, as soon as its weights are there.
-__device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t tbl, uint32_t tm) {
+__device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
   const int most = 128 * p.Hkv;
   uint32_t turn = 0;                  // bit s: parity of stream s's job
   uint32_t add = 0;                   // bit s: stream s has had a job in the segment
+  uint32_t stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
     if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
@@ -706,33 +756,34 @@ __device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
     if (flags & kFirst) {
-      add = 0;
+      add = s = 0;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
     }
-    const uint32_t stage = t & 1;
-    if (!warp_wait(f.vfull[stage], (t >> 1) & 1, f, p.err)) return;
-    const uint32_t values = kDescValues | (values_at(tbl, stage) >> 4);
-    const int jobs = two ? 4 : 2;
+    if (!warp_wait(f.vfull[stage], use & 1, f, p.err)) return;
+    const uint32_t low = kDescValues | (values_at(base, stage) >> 4);
 #pragma unroll 1
-    for (int y = 0; y < jobs; ++y) {
-      const uint32_t s = y & 1;
+    for (int y = two ? 1 : 0; y >= 0; --y) {
       if (!warp_wait(f.pfull[s], (turn >> s) & 1, f, p.err)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t low = values + (two ? y >> 1 : y) * (kJob * 128 / 16);
         const uint32_t a = tm + (two ? kColS + 64 * s : kColP + 32 * s), o = tm + kColO + 128 * s;
 #pragma unroll
-        for (int k = 0; k < kJob / 16; ++k)
+        for (int k = 0; k < kTile / 16; ++k)
           tc_mma(o, a + 8 * k, operand(low + 128 * k), kIdescO, k > 0 ? 1u : (add >> s) & 1);
         tc_commit(smem_u32(&f.odone[s]));
-        if (y == jobs - 1) {
+        if (y == 0) {
           tc_commit(smem_u32(&f.vempty[stage]));
           if ((t & (kBatch - 1)) == kBatch - 1) tc_commit(smem_u32(&f.rfree[(t / kBatch) & 3]));
         }
       }
       __syncwarp();
       add |= 1u << s;
+      s ^= 1;
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      ++use;
     }
   }
 }
@@ -856,8 +907,8 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
 }
 
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, float* buf, uint32_t tm0,
-                                             int warp, int lane) {
+__device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, float* buf, Sums& sum,
+                                             uint32_t tm0, int warp, int lane) {
   const int G = p.Hq / p.Hkv;
   const int wg = warp >> 2, part = warp & 3, tl = 32 * part + lane;
   const uint32_t tm = tm0 + ((uint32_t)(32 * part) << 16);
@@ -867,6 +918,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
   const int lgG = __ffs(G) - 1;
   int nb = 1, rc = 128, copy = 0, R = 0;
   bool busy = true;  // the warp has rows
+  int next = 0;      // jobs to the stream's next one
+  uint32_t stage = kStages - 1;
   unsigned long long see = 0;
   const auto meet = [&]() {
     warp_arrive(f.sync);
@@ -944,35 +997,37 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       r.m = -INFINITY;
       r.l = 0.0f;
       r.mine = 0;
+      next = wg;
       see = 0;
       if (live && p.K)
         see = p.mask ? p.mask[tok] : (i >= 63 ? ~0ull : (2ull << i) - 1);
     }
-    // one block: the stream's half; two: both halves
-#pragma unroll 1
-    for (int y = nb == 1 ? wg : 0; y < (nb == 1 ? wg + 1 : 2); ++y) {
+    if (++stage == kStages) stage = 0;
+    // one block: the streams take the tiles in turn; two: every tile
+    if (nb == 2 || next == 0) {
       if (!warp_wait(f.sfull[wg], r.turn, f, p.err)) return;
       tc_fence_after();
       if (busy) {
-        const int stage = t & 1, n = kJob * rc / 128, c0 = copy * n;
-        unsigned long long bits = d.valid[y];
+        const int n = kTile * rc / 128, c0 = copy * n;
+        unsigned long long bits = d.valid;
         const float* cs = nullptr;
         if (flags & kDraft) {
           bits &= see;
-          cs = f.cs[stage] + kJob * y + c0;
+          cs = f.cs[stage] + c0;
         }
         const uint32_t sa = tm + kColS + 64 * wg + c0;
         const uint32_t pa = nb == 2 ? sa : tm + kColP + 32 * wg + c0 / 2;
-        if (!softmax_job<CAP, BIAS>(p, f, r, sa, pa, oa, wg, n, bits >> c0, cs,
-                                    f.pos[stage] + kJob * y + c0))
+        if (!softmax_job<CAP, BIAS>(p, f, r, sa, pa, oa, wg, n, bits >> c0, cs, f.pos[stage] + c0))
           return;
+      } else {
+        warp_arrive(f.sfree[wg]);
       }
-      if (!busy) warp_arrive(f.sfree[wg]);
       tc_fence_before();
       warp_arrive(f.pfull[wg]);
       r.turn ^= 1;
       ++r.mine;
     }
+    next ^= 1;
     if (!(flags & kLast)) continue;
     // the segment's end: the streams' and copies' sums meet, 32 dims at a time
     if (r.mine > 0) {
@@ -980,8 +1035,8 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       tc_fence_after();
     }
     const bool bad = *(const volatile int*)&d.bad != 0;
-    f.m[wg][tl] = r.m;
-    f.l[wg][tl] = r.l;
+    sum.m[wg][tl] = r.m;
+    sum.l[wg][tl] = r.l;
     if (!meet()) return;
     float* const mine = buf + tl * kBufRow;
     const int copies = 128 / rc, sub = tl & (rc - 1);
@@ -989,7 +1044,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     if (nb == 1) {
       float M = -INFINITY;
       for (int k = 0; k < copies; ++k)
-        M = fmaxf(M, fmaxf(f.m[0][sub + rc * k], f.m[1][sub + rc * k]));
+        M = fmaxf(M, fmaxf(sum.m[0][sub + rc * k], sum.m[1][sub + rc * k]));
       a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
     }
 #pragma unroll 1
@@ -1035,17 +1090,17 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
           const float* from = buf + z * kBufRow + l;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] += from[8 * e];
-          Mx = nb == 2 ? f.m[s][z] : fmaxf(Mx, fmaxf(f.m[0][z], f.m[1][z]));
+          Mx = nb == 2 ? sum.m[s][z] : fmaxf(Mx, fmaxf(sum.m[0][z], sum.m[1][z]));
         }
         if (nb == 2) {
-          Lx = f.l[s][x];
+          Lx = sum.l[s][x];
           if (Mx == -INFINITY) v[0] = v[1] = v[2] = v[3] = 0.0f;
         } else {
           for (int k = 0; k < copies; ++k) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               // (a sum without a maximum: 0, or NaN where every score is NaN)
-              const float mz = f.m[y][x + rc * k], lz = f.l[y][x + rc * k];
+              const float mz = sum.m[y][x + rc * k], lz = sum.l[y][x + rc * k];
               if (lz != 0.0f) Lx += mz == -INFINITY ? lz : lz * ex2f(mz - Mx);
             }
           }
@@ -1063,9 +1118,10 @@ template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   Fixed& f = *reinterpret_cast<Fixed*>(raw);
-  const uint32_t at = smem_u32(raw), tbl = (at + kLowBytes + kTblBytes - 1) & ~(kTblBytes - 1);
+  const uint32_t at = smem_u32(raw), base = (at + (uint32_t)sizeof(Fixed) + 8191u) & ~8191u;
+  uint8_t* const mem = raw + (base - at);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tbl + kTblBytes + 3 * kOperand > at + kSmemBytes) {
+  if (base + kHighBytes > at + kSmemBytes) {
     // (the window starts at 1 KB: it fits)
     if (tid == 0) report(p.err, SKV_ERR_CUDA);
     return;
@@ -1089,6 +1145,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     mbar_init(smem_u32(&f.sync), kSoftWarps);
     mbar_init(smem_u32(&f.fin[0]), 1);
     mbar_init(smem_u32(&f.fin[1]), 1);
+    for (int k = 0; k < kRawTiles; ++k) {
+      mbar_init(smem_u32(&f.rawfull[k]), 1);
+      mbar_init(smem_u32(&f.rawfree[k]), kTeamWarps);
+    }
     for (int k = 0; k < kRing / kBatch; ++k) {
       mbar_init(smem_u32(&f.dfull[k]), 1);
       mbar_init(smem_u32(&f.rfree[k]), 1);
@@ -1101,24 +1161,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  key_tables(p, tbl, tid, kThreads);
+  key_tables(p, base + kAtTbl1, 128, base + kAtTbl2, tid, kThreads);
   tc_fence_before();
   find_run<kThreads>(p, blockIdx.x, f.scan, &f.run, RowsCost());  // (block-wide barriers)
   tc_fence_after();
   const uint32_t tm = *(volatile uint32_t*)&f.tmem;
 
   if (warp < kSoftWarps) {
-    softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(raw + kAtBuf), tm, warp, lane);
+    softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(mem + kAtBuf),
+                            *reinterpret_cast<Sums*>(mem + kAtSums), tm, warp, lane);
   } else if (warp < kPlanner) {
-    decode_role<BIAS>(p, f, tbl, warp - kSoftWarps, lane);
+    decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane);
   } else {
     if (warp == kPlanner) {
       planner(p, f, blockIdx.x, lane);
-    } else if (warp == kMmaS || warp == kMmaO) {
+    } else if (warp == kCopier) {
+      copier(p, f, base, lane);
+    } else {
       if (warp == kMmaS)
-        mma_scores(p, f, tbl, tm);
+        mma_scores(p, f, base, tm);
       else
-        mma_sums(p, f, tbl, tm);
+        mma_sums(p, f, base, tm);
       // nothing in flight when tensor memory is given back
       unsigned long long& fin = f.fin[warp - kMmaS];
       if (elect_one()) tc_commit(smem_u32(&fin));

@@ -27,6 +27,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
@@ -99,12 +109,12 @@ __device__ __forceinline__ int scale_exp(uint32_t m, int bf16) {
   return b >= 0x7F800000u ? 0 : min(100, e);
 }
 
-// The tables start on a 64 KB boundary: entry e of T1's (the code byte) is at
-// 256 e, in 32 copies of 4 bytes (copy L is read by lane L), so that one byte
-// permutation forms a gather's address; T2's entries (angle | share << 4) fill
-// the other halves.  An entry is the code's key pair at radius 1 (share times
-// cosine and sine) in fp16.
-__device__ __forceinline__ void key_tables(const TreeParams& p, uint32_t tbl, int tid, int threads) {
+// The key pairs of the codes at radius 1 (share times cosine and sine) in
+// fp16: T1 entry e (the code byte) at tbl1 + step e, T2 entry e (angle |
+// share << 4) at tbl2 + step e, each in 32 copies of 4 bytes (copy L is read by
+// lane L).
+__device__ __forceinline__ void key_tables(const TreeParams& p, uint32_t tbl1, int step,
+                                           uint32_t tbl2, int tid, int threads) {
   for (int i = tid; i < 8 * (256 + 64); i += threads) {
     const int e = i >> 3;
     float cs, sn, w;
@@ -122,7 +132,7 @@ __device__ __forceinline__ void key_tables(const TreeParams& p, uint32_t tbl, in
       w = p.rho[(e - 256) >> 4];
     }
     const uint32_t h = pack_f16x2(w * cs, w * sn);
-    sts128(tbl + (e < 256 ? 256 * e : 256 * (e - 256) + 128) + 16 * (i & 7), make_uint4(h, h, h, h));
+    sts128((e < 256 ? tbl1 + step * e : tbl2 + step * (e - 256)) + 16 * (i & 7), make_uint4(h, h, h, h));
   }
 }
 

@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     if (tid == 0) report(p.err, SKV_ERR_CUDA);
     return;
   }
-  key_tables(p, tbl, tid, S::kThreads);
+  // (entry e of T1's table at 256 e, T2's in the other halves)
+  key_tables(p, tbl, 256, tbl + 128, tid, S::kThreads);
   const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kRunTile / P;
   const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
   const uint32_t tb = tbl + 4 * lane;
