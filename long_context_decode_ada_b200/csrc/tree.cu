@@ -68,6 +68,11 @@ constexpr int kDecodeWarps = kTeams * kTeamWarps;
 constexpr int kPlanner = kSoftWarps + kDecodeWarps, kCopier = kPlanner + 1;
 constexpr int kMmaS = kPlanner + 2;  // (and the warp behind it)
 constexpr int kThreads = (kSoftWarps + kDecodeWarps + 4) * 32;
+// registers a thread (softmax, decode, the others); their sum over the threads
+// is what the block is launched with
+constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDecode = 80, kRegsHelp = 64;
+static_assert(kSoftWarps * kRegsSoft + kDecodeWarps * kRegsDecode + 4 * kRegsHelp <=
+                  kThreads / 32 * kRegsLaunch, "registers");
 constexpr int kBufRow = 36;          // floats of a row of the output buffer (32 dims)
 // pages as they are stored: slots of one coded tile (a dense tile takes three)
 constexpr uint32_t kRawSlot = kTile * 196 + 4 * kHdrBytes;
@@ -241,7 +246,7 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
 
 // More than 128 rows cost half as much again (decoded once, multiplied twice).
 struct RowsCost {
-  static constexpr int kTile = 64;
+  static constexpr int kTile = 64, kBegin = 512;
   __device__ __forceinline__ int operator()(int rows) const { return rows > 128 ? 3 : 2; }
 };
 static_assert(RowsCost::kTile == kTile, "tiles");
@@ -1168,11 +1173,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   const uint32_t tm = *(volatile uint32_t*)&f.tmem;
 
   if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(mem + kAtBuf),
                             *reinterpret_cast<Sums*>(mem + kAtSums), tm, warp, lane);
   } else if (warp < kPlanner) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
     decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane);
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
     if (warp == kPlanner) {
       planner(p, f, blockIdx.x, lane);
     } else if (warp == kCopier) {

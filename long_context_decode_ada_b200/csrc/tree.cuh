@@ -78,10 +78,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
-// floor(a / b), b > 0: below 2^52 by one double division, off by at most one
-// and corrected with exact products
+// floor(a / b) for a < 2^52, 0 < b < 2^52 (2^20 units of 2^25 pages in 2^16 runs
+// stay below): one double division, off by at most one, corrected with exact
+// products
 __device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned long long b) {
-  if (a >= (1ull << 52) || b >= (1ull << 52)) return a / b;
   unsigned long long q = (unsigned long long)((double)a / (double)b);
   if (q * b > a)
     --q;
@@ -146,13 +146,14 @@ __device__ __forceinline__ void prefetch_page(const uint8_t* a, int P, int tier)
 // Pages of a unit by tier and their costs.  A dense page's bytes take 2.6
 // times a coded one's, but its conversion less: it counts twice.  A unit's
 // rows count by the kernel's own measure (rows_cost, with the tokens of its
-// tiles, kTile).
+// tiles, kTile; taking up a unit counts as kBegin coded tokens of few rows).
 struct Unit {
   long long first;     // index of the first page
   int np, n;           // pages, drafted tokens
   int nt[3];
   int w[3];
-  unsigned long long pages, last, cost;  // cost of the pages, start of the last item, all
+  int begin;           // cost of taking the unit up, before its first tile
+  unsigned long long last, cost;  // start of the last item, all
 };
 
 template <class Cost>
@@ -176,24 +177,27 @@ __device__ __forceinline__ Unit unit_of(const TreeParams& p, int u, Cost rows_co
   const int f = rows_cost(x.n * (p.Hq / p.Hkv));
   x.w[0] = 2 * f;
   x.w[1] = x.w[2] = f;
-  x.pages = (unsigned long long)x.w[0] * x.nt[0] + (unsigned long long)f * (x.nt[1] + x.nt[2]);
+  const unsigned long long pages =
+      (unsigned long long)x.w[0] * x.nt[0] + (unsigned long long)f * (x.nt[1] + x.nt[2]);
   const int ipp = Cost::kTile / p.P;
+  x.begin = 2 * Cost::kBegin / p.P;
   if (x.n == 0) {
-    x.pages = x.last = x.cost = 0;
+    x.last = x.cost = 0;
   } else if (p.K || x.np == 0) {
-    x.last = x.pages;
-    x.cost = x.pages + (unsigned long long)(f * ipp);
+    x.last = x.begin + pages;
+    x.cost = x.last + (unsigned long long)(f * ipp);
   } else {
     const int k = (x.np - 1) & ~(ipp - 1);  // the last tile's first page
     const int a0 = min(k, n0);
-    x.last = (unsigned long long)x.w[0] * a0 + (unsigned long long)f * (k - a0);
-    x.cost = x.pages;
+    x.last = x.begin + (unsigned long long)x.w[0] * a0 + (unsigned long long)f * (k - a0);
+    x.cost = x.begin + pages;
   }
   return x;
 }
 
 // The first tile of the unit that starts at cost y or above.
 __device__ __forceinline__ int tile_at(const Unit& x, long long y, int ipp) {
+  y -= x.begin;
   if (y <= 0) return 0;
   long long g = 0;
 #pragma unroll
@@ -245,7 +249,8 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
     tot += scan[k];
   }
   // a run has a tile of the least cost at least
-  const unsigned long long tiles = tot / (unsigned)(rows_cost(1) * (Cost::kTile / p.P));
+  const unsigned long long tiles =
+      divide(tot, (unsigned long long)(rows_cost(1) * (Cost::kTile / p.P)));
   const int S = (int)min((unsigned long long)p.S, max(1ull, tiles));
   const bool live = c < S && tot > 0;
   unsigned long long from = 0, to = 0;

@@ -35,13 +35,13 @@ constexpr uint32_t kRowsSmem = 131072;
 
 template <int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 12;
+  static constexpr int kWarps = 12;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;         // rows of a warp
   static constexpr int kHalf = kWarps / 2;     // warps whose sums meet in shared memory
   // cost of a tile by the rows: one or two warps take its tokens
   struct Cost {
-    static constexpr int kTile = kRunTile;
+    static constexpr int kTile = kRunTile, kBegin = 512;
     __device__ __forceinline__ int operator()(int rows) const {
       return NT == 1 || rows <= kRows ? 2 : 4;
     }
@@ -53,16 +53,22 @@ struct __align__(16) Entry {      // a page
   uint32_t tier, rows;            // 3: unusable
 };
 
+struct __align__(16) Segment {   // a unit, or the part of it that lies in the run
+  long long first;                // page of the list
+  int pages, dparts;              // pages, 16-row parts of drafted tokens
+  int u, n, slot;                 // unit, drafted tokens, partial slot (-1: all here)
+};
+
 template <int NT>
 struct __align__(16) RowsFixed {
   Entry page[kWindow];
   unsigned long long scan[Shape<NT>::kWarps];
   Run run;
-  Share share;
-  Unit unit;
-  int u;                          // the segment's unit, -1: no more
+  Segment seg[32];                // the next segments
+  int nseg;                       // of them
+  int unit;                       // the first unit not looked at, and the cost before it
+  unsigned long long before;
   int bad[2];                     // a drafted value lies outside fp16 (segments in turn)
-  unsigned long long before;      // cost before unit u
   float m[Shape<NT>::kHalf][Shape<NT>::kRows], l[Shape<NT>::kHalf][Shape<NT>::kRows];
   __align__(16) float o[Shape<NT>::kHalf][Shape<NT>::kRows][kObufRow];
 };
@@ -78,6 +84,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 struct Raw {
   uint4 k[2], v[4];
   uint32_t r[2], s[2];
+  int pos[2];
 };
 
 __device__ __forceinline__ void raw_keys(const uint8_t* page, uint32_t tier, int at, int P, int g,
@@ -275,10 +282,12 @@ __device__ __forceinline__ float draft_value(const TreeParams& p, long long at, 
 // 16 drafted tokens from j0 on.
 template <int NT, bool CAP, bool BIAS>
 __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, const Score<NT>& sc,
-                                             int b, int h, int n, int j0, int row0, int R, int G,
-                                             int q0, int lane, int* bad) {
-  const int g = lane >> 2, t = lane & 3;
+                                             const Segment& sg, int j0, int row0, int G, int lane,
+                                             int* bad) {
+  const int g = lane >> 2, t = lane & 3, n = sg.n, R = n * G;
+  const int b = sg.u / p.Hkv, h = sg.u - b * p.Hkv;
   const long long tok0 = (long long)b * p.N, off = (long long)h * kHeadDim;
+  const int q0 = BIAS ? p.q_pos[tok0] : 0;
   const uint16_t* K = static_cast<const uint16_t*>(p.K);
   float c[NT][4] = {}, up[2], down[2], pos[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -368,41 +377,110 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
   const uint32_t tb = tbl + 4 * lane;
   find_run<S::kThreads>(p, c, f.scan, &f.run, typename S::Cost());
-  // the next unit with a part in this run, by one thread
-  const auto open = [&](int u, unsigned long long cc) {
-    const int U = p.B * p.Hkv;
-    f.u = -1;
-    while (u < U && cc < f.run.to) {
-      f.unit = unit_of(p, u, typename S::Cost());
-      if (share_of(p, f.unit, f.run, c, cc, kRunTile / p.P, f.share)) {
-        f.u = u;
-        f.before = cc;
-        if (f.share.starts) p.join[c] = make_int2(u, f.share.last);
-        return;
+  // the next segments, by one warp: a lane per unit
+  const auto look_ahead = [&]() {
+    const int U = p.B * p.Hkv, u = f.unit + lane;
+    Unit x = {};
+    if (u < U) x = unit_of(p, u, typename S::Cost());
+    unsigned long long cc = x.cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, cc, o);
+      if (lane >= o) cc += y;
+    }
+    cc += f.before;                      // behind the unit
+    const Run run = f.run;
+    Share y;
+    const bool mine = u < U && cc - x.cost < run.to && share_of(p, x, run, c, cc - x.cost, ipp, y);
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, mine);
+    if (mine) {
+      Segment g;
+      g.first = x.first + (long long)y.k * ipp;
+      g.pages = max(0, min(y.kend * ipp, x.np) - y.k * ipp);
+      g.dparts = y.draft ? (x.n + 15) >> 4 : 0;
+      g.u = u;
+      g.n = x.n;
+      g.slot = y.slot;
+      f.seg[__popc(all & ((1u << lane) - 1))] = g;
+      if (y.starts) p.join[c] = make_int2(u, y.last);
+    }
+    __syncwarp();
+    if (lane == 31) {
+      f.nseg = __popc(all);
+      f.before = cc;
+      f.unit = cc < run.to ? u + 1 : U;
+    }
+    __syncwarp();
+  };
+  // the next segments, while there are units: the count in f.nseg (block-wide
+  // between barriers; whole batches of units may lie outside the run)
+  const auto refill = [&]() {
+    if (warp == 0) {
+      do {
+        look_ahead();
+      } while (f.nseg == 0 && f.unit < p.B * p.Hkv);
+    }
+  };
+  // A page's entry, in two steps: its id, then its header.
+  constexpr int kEach = (kWindow + S::kThreads - 1) / S::kThreads;
+  uint32_t id[kEach];
+  const auto load_ids = [&](const Segment& g, int w0) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int k = tid + e * S::kThreads;
+      id[e] = k < min(kWindow, g.pages - w0) ? p.ids[g.first + w0 + k] : 0xFFFFFFFFu;
+    }
+  };
+  const auto make_entries = [&](const Segment& g, int w0) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int k = tid + e * S::kThreads;
+      if (k >= min(kWindow, g.pages - w0)) continue;
+      const int ti = (int)(id[e] >> 30);
+      const uint32_t sl = id[e] & 0x3FFFFFFFu;
+      Entry o = {0, 3, 0};
+      if (ti > 2 || (long long)sl >= p.slots[ti]) {
+        report(p.err, SKV_ERR_CORRUPT);
+      } else {
+        const uint8_t* a = p.pool[ti] + (long long)sl * p.stride[ti];
+        if (k < kAhead / P) prefetch_page(a, P, ti);
+        const uint32_t hd = *reinterpret_cast<const uint32_t*>(a);
+        const uint32_t rows = hd & 0xFFFFu;
+        if ((hd >> 16) != ((uint32_t)ti | ((uint32_t)kPageMagic << 8)) || rows > (uint32_t)P) {
+          report(p.err, SKV_ERR_CORRUPT);
+        } else {
+          o.page = reinterpret_cast<unsigned long long>(a);
+          o.tier = (uint32_t)ti;
+          o.rows = rows;
+        }
       }
-      cc += f.unit.cost;
-      ++u;
+      f.page[k] = o;
     }
   };
   if (tid == 0) {
     p.join[c] = make_int2(-1, 0);
     f.bad[0] = f.bad[1] = 0;
-    open(f.run.unit, f.run.before);
+    f.unit = f.run.unit;
+    f.before = f.run.before;
+    f.nseg = 0;
   }
+  __syncthreads();
+  refill();
+  __syncthreads();
+  int at_seg = 0, nseg = f.nseg;
+  if (nseg == 0) return;
+  load_ids(f.seg[0], 0);
+  make_entries(f.seg[0], 0);
   __syncthreads();
 
   for (int seg = 0;; seg ^= 1) {
-    const int u = f.u;
-    if (u < 0) break;
-    const int n = f.unit.n, slot = f.share.slot, R = n * G;
-    const int b = u / p.Hkv, h = u - b * p.Hkv;
+    // (read again where it is used: registers are short)
+    const Segment& sg = f.seg[at_seg];
+    const int b = sg.u / p.Hkv, h = sg.u - b * p.Hkv, R = sg.n * G;
     const int blocks = R > S::kRows ? 2 : 1;      // (at most 2 S::kRows rows)
     const int streams = S::kWarps / blocks;
     const int stream = blocks == 2 ? warp >> 1 : warp;
     const int row0 = blocks == 2 ? S::kRows * (warp & 1) : 0;
-    const long long first = f.unit.first + (long long)f.share.k * ipp;
-    const int pages = max(0, min(f.share.kend * ipp, f.unit.np) - f.share.k * ipp);
-    const int dparts = f.share.draft ? (n + 15) >> 4 : 0;
     const long long tok0 = (long long)b * p.N;
     const int q0 = BIAS ? p.q_pos[tok0] : 0;
 
@@ -466,36 +544,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         fr.acc[k][mt][0] = fr.acc[k][mt][1] = fr.acc[k][mt][2] = fr.acc[k][mt][3] = 0.0f;
     }
 
-    for (int w0 = 0; w0 < pages || w0 == 0; w0 += kWindow) {
-      const int held = min(kWindow, pages - w0);
+    for (int w0 = 0; w0 < sg.pages || w0 == 0; w0 += kWindow) {
+      const int held = min(kWindow, sg.pages - w0);
       const int ahead = kAhead / P;
-      if (w0 > 0) __syncthreads();
-      for (int k = tid; k < held; k += S::kThreads) {
-        const uint32_t id = p.ids[first + w0 + k], sl = id & 0x3FFFFFFFu;
-        const int ti = (int)(id >> 30);
-        Entry e = {0, 3, 0};
-        if (ti > 2 || (long long)sl >= p.slots[ti]) {
-          report(p.err, SKV_ERR_CORRUPT);
-        } else {
-          const uint8_t* a = p.pool[ti] + (long long)sl * p.stride[ti];
-          if (k < ahead) prefetch_page(a, P, ti);
-          const uint32_t hd = *reinterpret_cast<const uint32_t*>(a);
-          const uint32_t rows = hd & 0xFFFFu;
-          if ((hd >> 16) != ((uint32_t)ti | ((uint32_t)kPageMagic << 8)) || rows > (uint32_t)P) {
-            report(p.err, SKV_ERR_CORRUPT);
-          } else {
-            e.page = reinterpret_cast<unsigned long long>(a);
-            e.tier = (uint32_t)ti;
-            e.rows = rows;
-          }
-        }
-        f.page[k] = e;
+      if (w0 > 0) {
+        load_ids(sg, w0);
+        __syncthreads();
+        make_entries(sg, w0);
+        __syncthreads();
       }
-      __syncthreads();
       const int store = held << lgp;
-      const int total = store + (w0 + kWindow >= pages ? dparts : 0);
+      const int total = store + (w0 + kWindow >= sg.pages ? sg.dparts : 0);
       Raw o;
       o.r[0] = o.r[1] = o.s[0] = o.s[1] = 0;
+      o.pos[0] = o.pos[1] = q0;
       const uint8_t* page = nullptr;
       uint32_t tier = 3;
       int rows = 0, at = 0;
@@ -510,12 +572,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           tier = rows > 0 ? e.tier : 3u;
         }
       };
+      const auto raw_pos = [&](int q) {
+        if (BIAS && q < store) {
+          const int32_t* a = p.row_pos + ((sg.first + w0 + (q >> lgp)) * P + at + g);
+          if (g < rows) o.pos[0] = a[0];
+          if (g + 8 < rows) o.pos[1] = a[8];
+        }
+      };
       look(stream);
+      raw_pos(stream);
       raw_keys(page, tier, at, P, g, t, o);
       raw_values(page, tier, at, P, t, lane, o);
       for (int q = stream; q < total; q += streams) {
         if (q >= store) {
-          draft_tokens<NT, CAP, BIAS>(p, fr, sc, b, h, n, 16 * (q - store), row0, R, G, q0, lane,
+          draft_tokens<NT, CAP, BIAS>(p, fr, sc, sg, 16 * (q - store), row0, G, lane,
                                       &f.bad[seg]);
           continue;
         }
@@ -529,6 +599,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         }
         if (ti == 3) {
           look(q + streams);
+          raw_pos(q + streams);
           raw_keys(page, tier, at, P, g, t, o);
           raw_values(page, tier, at, P, t, lane, o);
           continue;
@@ -538,9 +609,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         float(&co)[NT][4] = NT == 1 ? cd : cc;
         float rA = 1.0f, rB = 1.0f, posA = 0.0f, posB = 0.0f;
         if (BIAS) {
-          const int32_t* at_pos = p.row_pos + (first + w0 + (q >> lgp)) * P + a0;
-          if (g < nr) posA = (float)(at_pos[g] - q0);
-          if (g + 8 < nr) posB = (float)(at_pos[g + 8] - q0);
+          posA = (float)(o.pos[0] - q0);
+          posB = (float)(o.pos[1] - q0);
         }
         if (ti == SKV_TIER_T1) {
           const uint32_t wa[4] = {o.k[0].x, o.k[0].y, o.k[0].z, o.k[0].w};
@@ -576,6 +646,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           rB = __half2float(__ushort_as_half((uint16_t)o.r[1]));
         }
         look(q + streams);
+        raw_pos(q + streams);
         raw_keys(page, tier, at, P, g, t, o);
         uint32_t see = ~0u, w[NT][2];
         if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
@@ -612,6 +683,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       }
     }
 
+    // (the next segment's page ids are on their way meanwhile)
+    const bool more = at_seg + 1 < nseg;
+    if (more) load_ids(f.seg[at_seg + 1], 0);
     // the warps' sums meet: the second half's in the first half's registers,
     // those in shared memory (a warp and the one kHalf behind it have the
     // same rows)
@@ -659,13 +733,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         }
       }
       __syncthreads();
+      if (half == 1 && more) make_entries(f.seg[at_seg + 1], 0);
     }
-    if (tid == S::kThreads - 1) {
-      f.bad[seg ^ 1] = 0;
-      open(u + 1, f.before + f.unit.cost);
-    }
+    if (tid == 0) f.bad[seg ^ 1] = 0;
     const bool bad = *(volatile int*)&f.bad[seg] != 0;
-    for (int r = warp; r < R; r += S::kWarps) {
+    for (int r = warp; r < sg.n * G; r += S::kWarps) {
       const int blk = r >= S::kRows ? 1 : 0, lr = r - S::kRows * blk;
       float m = -INFINITY, l = 0.0f;
       if (lane < S::kHalf / blocks) {
@@ -690,8 +762,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         v[2] += ak * x.z;
         v[3] += ak * x.w;
       }
-      write_row<CAP, BIAS, 32>(p, u, n, slot, bad, r, M, L, v, 4 * lane, lane);
+      write_row<CAP, BIAS, 32>(p, sg.u, sg.n, sg.slot, bad, r, M, L, v, 4 * lane, lane);
     }
+    __syncthreads();
+    if (more) {
+      ++at_seg;
+      continue;
+    }
+    refill();
+    __syncthreads();
+    at_seg = 0;
+    nseg = f.nseg;
+    if (nseg == 0) break;
+    load_ids(f.seg[0], 0);
+    make_entries(f.seg[0], 0);
     __syncthreads();
   }
 }
