@@ -1223,24 +1223,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
   const auto at = [&](int k) {
     return (long long)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * rows + r;
   };
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, p.part_ml[at(k)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float L = 0.0f;
+  // 16 parts' loads at once
+  float M = -INFINITY, L = 0.0f;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const float2 ml = p.part_ml[at(k)];
-    const float4 x = *reinterpret_cast<const float4*>(p.part + at(k) * kHeadDim + 4 * lane);
-    const float a = ml.x == -INFINITY ? 0.0f : ex2f(ml.x - M);
-    L += a * ml.y;
-    v.x += a * x.x;
-    v.y += a * x.y;
-    v.z += a * x.z;
-    v.w += a * x.w;
+  constexpr int kAtOnce = 16;
+  for (int k0 = 0; k0 < parts; k0 += kAtOnce) {
+    float2 ml[kAtOnce];
+    float4 x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k0 + k < parts) {
+        ml[k] = p.part_ml[at(k0 + k)];
+        x[k] = *reinterpret_cast<const float4*>(p.part + at(k0 + k) * kHeadDim + 4 * lane);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) m = fmaxf(m, ml[k].x);
+    const float keep = M == m ? 1.0f : ex2f(M - m);
+    M = m;
+    L *= keep;
+    v = make_float4(v.x * keep, v.y * keep, v.z * keep, v.w * keep);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float a = ml[k].x == -INFINITY ? 0.0f : ex2f(ml[k].x - M);
+      L += ml[k].x == -INFINITY ? ml[k].y : a * ml[k].y;
+      v.x += a * x[k].x;
+      v.y += a * x[k].y;
+      v.z += a * x[k].z;
+      v.w += a * x[k].w;
+    }
   }
-  const int i = r / G, hq = h * G + (r - i * G);
+  const int i = r >> (__ffs(G) - 1), hq = h * G + (r & (G - 1));
   const long long tok = (long long)b * p.N + i;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   uint2 w;

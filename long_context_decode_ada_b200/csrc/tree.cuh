@@ -306,7 +306,7 @@ __device__ __forceinline__ bool share_of(const TreeParams& p, const Unit& x, con
 template <bool CAP, bool BIAS, int LANES>
 __device__ __forceinline__ void write_row(const TreeParams& p, int unit, int n, int slot, bool bad,
                                           int r, float M, float L, float (&v)[4], int d0, int lane) {
-  const int G = p.Hq / p.Hkv, i = r / G, g = r - i * G;
+  const int G = p.Hq / p.Hkv, i = r >> (__ffs(G) - 1), g = r & (G - 1);
   const int b = unit / p.Hkv, h = unit - b * p.Hkv, hq = h * G + g;
   const long long tok = (long long)b * p.N + i;
   if (bad) {

@@ -122,6 +122,15 @@ __device__ __forceinline__ void raw_values(const uint8_t* page, uint32_t tier, i
   }
 }
 
+// Asks for part `sub` of a page's bytes in L2 (a warp; one page line a lane).
+__device__ __forceinline__ void prefetch_part(const Entry& e, int P, int sub, int parts, int lane) {
+  if (e.tier > 2) return;
+  const int bytes = kHdrBytes + P * tier_row_bytes((int)e.tier), each = (bytes + parts - 1) / parts;
+  const uint8_t* a = reinterpret_cast<const uint8_t*>(e.page) + sub * each;
+  for (int o = 128 * lane; o < each; o += 4096)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a + min(o, bytes - 1 - sub * each)));
+}
+
 template <int NT>
 struct Frag {
   uint32_t q[16];         // B fragments of the rows (one block; two: in shared memory at qs)
@@ -333,7 +342,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
   for (int e = 0; e < 4 * NT; ++e) {
     const int r = row0 + 8 * (e >> 2) + 2 * t + (e & 1), j = j0 + g + 8 * ((e >> 1) & 1);
     if (r < R && j < n) {
-      const int i = r / G;
+      const int i = r >> (__ffs(G) - 1);
       if (p.mask ? (p.mask[tok0 + i] >> j) & 1 : j <= i) see |= 1u << e;
     }
   }
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   }
   // (entry e of T1's table at 256 e, T2's in the other halves)
   key_tables(p, tbl, 256, tbl + 128, tid, S::kThreads);
-  const int c = blockIdx.x, G = p.Hq / p.Hkv, P = p.P, ipp = kRunTile / P;
+  const int c = blockIdx.x, G = p.Hq / p.Hkv, lgG = __ffs(G) - 1, P = p.P, ipp = kRunTile / P;
   const int lgp = __ffs(P) - 5, ppp = 1 << lgp;   // 16-row parts of a page
   const uint32_t tb = tbl + 4 * lane;
   find_run<S::kThreads>(p, c, f.scan, &f.run, typename S::Cost());
@@ -443,7 +452,6 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         report(p.err, SKV_ERR_CORRUPT);
       } else {
         const uint8_t* a = p.pool[ti] + (long long)sl * p.stride[ti];
-        if (k < kAhead / P) prefetch_page(a, P, ti);
         const uint32_t hd = *reinterpret_cast<const uint32_t*>(a);
         const uint32_t rows = hd & 0xFFFFu;
         if ((hd >> 16) != ((uint32_t)ti | ((uint32_t)kPageMagic << 8)) || rows > (uint32_t)P) {
@@ -478,9 +486,13 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     const Segment& sg = f.seg[at_seg];
     const int b = sg.u / p.Hkv, h = sg.u - b * p.Hkv, R = sg.n * G;
     const int blocks = R > S::kRows ? 2 : 1;      // (at most 2 S::kRows rows)
-    const int streams = S::kWarps / blocks;
+    const int streams = blocks == 2 ? S::kHalf : S::kWarps;
     const int stream = blocks == 2 ? warp >> 1 : warp;
     const int row0 = blocks == 2 ? S::kRows * (warp & 1) : 0;
+    const int ahead = (kAhead / 16 + streams - 1) / streams * streams;   // parts
+    if (row0 == 0)
+      for (int q = stream; q < min(ahead, min(sg.pages, kWindow) << lgp); q += streams)
+        prefetch_part(f.page[q >> lgp], P, q & (ppp - 1), ppp, lane);
     const long long tok0 = (long long)b * p.N;
     const int q0 = BIAS ? p.q_pos[tok0] : 0;
 
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     fr.qs = tbl + 256 * (64 + 32 * (row0 != 0) + (lane >> 3)) + 128 + 16 * (lane & 7);
 #pragma unroll
     for (int k = 0; k < NT; ++k) {
-      const int r = row0 + 8 * k + g, i = r / G;
+      const int r = row0 + 8 * k + g, i = r >> lgG;
       uint4 x[4];
       uint32_t mx = 0;
 #pragma unroll
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         sc.slope[k][j] = sc.rel[k][j] = 0.0f;
         const int rr = row0 + 8 * k + 2 * t + j;
         if (BIAS && rr < R) {
-          const int ii = rr / G;
+          const int ii = rr >> lgG;
           sc.slope[k][j] = p.slopes[h * G + rr - ii * G] * 1.4426950408889634f;
           sc.rel[k][j] = (float)(p.q_pos[tok0 + ii] - q0);
         }
@@ -546,7 +558,6 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 
     for (int w0 = 0; w0 < sg.pages || w0 == 0; w0 += kWindow) {
       const int held = min(kWindow, sg.pages - w0);
-      const int ahead = kAhead / P;
       if (w0 > 0) {
         load_ids(sg, w0);
         __syncthreads();
@@ -592,11 +603,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         const uint8_t* const pg = page;
         const uint32_t ti = tier;
         const int nr = rows, a0 = at;
-        if (row0 == 0 && lane == 0 && a0 == 0) {
-          const int k = (q >> lgp) + ahead;
-          if (k < held && f.page[k].tier < 3)
-            prefetch_page(reinterpret_cast<const uint8_t*>(f.page[k].page), P, (int)f.page[k].tier);
-        }
+        if (row0 == 0 && q + ahead < store)
+          prefetch_part(f.page[(q + ahead) >> lgp], P, (q + ahead) & (ppp - 1), ppp, lane);
         if (ti == 3) {
           look(q + streams);
           raw_pos(q + streams);
