@@ -195,26 +195,17 @@ __device__ __forceinline__ Unit unit_of(const TreeParams& p, int u, Cost rows_co
   return x;
 }
 
-// The first tile of the unit that starts at cost y or above.
+// The first tile of the unit that starts at cost y or above (T1 and T2 pages
+// cost the same).
 __device__ __forceinline__ int tile_at(const Unit& x, long long y, int ipp) {
   y -= x.begin;
   if (y <= 0) return 0;
-  long long g = 0;
-#pragma unroll
-  for (int t = 0; t < 3; ++t) {
-    const long long c = (long long)x.nt[t] * x.w[t];
-    if (y > c) {
-      y -= c;
-      g += x.nt[t];
-    } else {
-      g += (long long)divide((unsigned long long)(y + x.w[t] - 1), (unsigned long long)x.w[t]);
-      y = 0;
-      break;
-    }
-  }
-  if (y > 0) g = x.np;
-  const int sh = __ffs(ipp) - 1;
-  return (int)min((long long)((x.np + ipp - 1) >> sh), (g + ipp - 1) >> sh);
+  const long long dense = (long long)x.nt[0] * x.w[0];
+  const bool first = y <= dense;
+  const uint32_t w = first ? x.w[0] : x.w[1];
+  const uint32_t z = (uint32_t)min(first ? y : y - dense, 0x7FFFFFF0ll);
+  const int g = min((first ? 0 : x.nt[0]) + (int)((z + w - 1) / w), x.np);
+  return (g + ipp - 1) >> (__ffs(ipp) - 1);
 }
 
 // The split as one run sees it.
@@ -234,6 +225,7 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
   const int per = (U + THREADS - 1) / THREADS;
   const int u0 = min(U, tid * per), u1 = min(U, u0 + per);
   unsigned long long mine = 0;
+#pragma unroll 1
   for (int u = u0; u < u1; ++u) mine += unit_of(p, u, rows_cost).cost;
   unsigned long long x = mine;
 #pragma unroll
@@ -244,6 +236,7 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
   if (lane == 31) scan[w] = x;
   __syncthreads();
   unsigned long long before = x - mine, tot = 0;
+#pragma unroll 1
   for (int k = 0; k < THREADS / 32; ++k) {
     if (k < w) before += scan[k];
     tot += scan[k];
@@ -255,8 +248,11 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
   const bool live = c < S && tot > 0;
   unsigned long long from = 0, to = 0;
   if (live) {
-    from = divide((unsigned long long)c * tot + S - 1, S);
-    to = divide((unsigned long long)(c + 1) * tot + S - 1, S);
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      from = to;
+      to = divide((unsigned long long)(c + k) * tot + S - 1, S);
+    }
   }
   if (tid == 0) {
     out->tot = tot;
@@ -267,6 +263,7 @@ __device__ __forceinline__ void find_run(const TreeParams& p, int c, unsigned lo
   }
   if (live) {
     unsigned long long cc = before;
+#pragma unroll 1
     for (int u = u0; u < u1; ++u) {
       const unsigned long long k = per == 1 ? mine : unit_of(p, u, rows_cost).cost;
       if (cc <= from && from < cc + k) {
@@ -293,10 +290,10 @@ __device__ __forceinline__ bool share_of(const TreeParams& p, const Unit& x, con
   o.k = tile_at(x, (long long)(r.from - cc), ipp);
   o.kend = tile_at(x, (long long)(r.to - cc), ipp);
   o.draft = p.K != nullptr && cc + x.last < r.to;
-  const int r0 = (int)divide(cc * r.S, r.tot);
-  o.last = (int)divide((cc + x.last) * r.S, r.tot);
-  o.slot = r0 == o.last ? -1 : (c == r0 ? 2 * c + 1 : 2 * c);
-  o.starts = c == r0 && o.last > r0;
+  const bool begins = cc >= r.from, ends = cc + x.last < r.to;
+  o.slot = begins ? (ends ? -1 : 2 * c + 1) : 2 * c;
+  o.starts = begins && !ends;
+  o.last = o.starts ? (int)divide((cc + x.last) * r.S, r.tot) : c;
   return true;
 }
 

@@ -24,9 +24,8 @@ namespace {
 
 using namespace tree;
 
-constexpr int kWindow = 512;                   // pages whose entries are held at once
+constexpr int kWindow = 512;                   // page ids held at once
 constexpr int kRunTile = 64;                   // tokens a run is cut by
-constexpr int kAhead = 16 * kRunTile;             // tokens asked for in L2 ahead
 constexpr int kObufRow = kHeadDim + 4;         // floats
 constexpr uint32_t kRowsTbl = 65536;
 // Shared memory ends behind the tables (128 KB): what is left of the SM's
@@ -48,11 +47,6 @@ struct Shape {
   };
 };
 
-struct __align__(16) Entry {      // a page
-  unsigned long long page;
-  uint32_t tier, rows;            // 3: unusable
-};
-
 struct __align__(16) Segment {   // a unit, or the part of it that lies in the run
   long long first;                // page of the list
   int pages, dparts;              // pages, 16-row parts of drafted tokens
@@ -61,7 +55,7 @@ struct __align__(16) Segment {   // a unit, or the part of it that lies in the r
 
 template <int NT>
 struct __align__(16) RowsFixed {
-  Entry page[kWindow];
+  uint32_t ids[2][kWindow];       // page ids of this segment and the next, in turn
   unsigned long long scan[Shape<NT>::kWarps];
   Run run;
   Segment seg[32];                // the next segments
@@ -84,11 +78,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 struct Raw {
   uint4 k[2], v[4];
   uint32_t r[2], s[2];
+  uint32_t hd;           // the page's header word
   int pos[2];
 };
 
 __device__ __forceinline__ void raw_keys(const uint8_t* page, uint32_t tier, int at, int P, int g,
                                          int t, Raw& o) {
+  if (tier < 3) o.hd = *reinterpret_cast<const uint32_t*>(page);
   const uint8_t* a = page + kHdrBytes;
   if (tier == SKV_TIER_T1 || tier == SKV_TIER_T2) {
     o.r[0] = *reinterpret_cast<const uint16_t*>(a + 2 * (at + g));
@@ -122,19 +118,16 @@ __device__ __forceinline__ void raw_values(const uint8_t* page, uint32_t tier, i
   }
 }
 
-// Asks for part `sub` of a page's bytes in L2 (a warp; one page line a lane).
-__device__ __forceinline__ void prefetch_part(const Entry& e, int P, int sub, int parts, int lane) {
-  if (e.tier > 2) return;
-  const int bytes = kHdrBytes + P * tier_row_bytes((int)e.tier), each = (bytes + parts - 1) / parts;
-  const uint8_t* a = reinterpret_cast<const uint8_t*>(e.page) + sub * each;
-  for (int o = 128 * lane; o < each; o += 4096)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a + min(o, bytes - 1 - sub * each)));
+// Asks for 16 dense rows' keys or values (4 KB, a line a lane) in L2: dense rows
+// are loaded when they are used.
+__device__ __forceinline__ void prefetch_rows(const uint8_t* a, int lane) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 128 * lane));
 }
 
 template <int NT>
 struct Frag {
-  uint32_t q[16];         // B fragments of the rows (one block; two: in shared memory at qs)
-  uint32_t qs;
+  uint32_t q[16];         // B fragments of the rows (one column block; two: from qs)
+  uint32_t qs;            // the same in shared memory
   float acc[NT][8][4];    // O^T: dims 16 mt + g (+ 8), rows 2 t, 2 t + 1
   float m[NT][2], l[NT][2];
 };
@@ -276,41 +269,28 @@ __device__ __forceinline__ uint32_t scaled(uint32_t u, uint32_t sel, uint32_t s)
   return hmul2(*reinterpret_cast<const uint32_t*>(&h), s);
 }
 
-// A value of a drafted token: 0 when fp16 does not hold it (added by
-// write_row) or the token is not there.
-__device__ __forceinline__ float draft_value(const TreeParams& p, long long at, bool live, bool& out) {
-  float y = 0.0f;
-  if (live) y = from16(static_cast<const uint16_t*>(p.V)[at], p.kv_bf16);
-  if (!(fabsf(y) <= 65504.0f)) {
-    y = 0.0f;
-    out = true;
-  }
-  return y;
-}
-
-// 16 drafted tokens from j0 on.
+// 16 drafted tokens from j0 on (scratch: 2 KB of shared memory of the warp).
+// Rolled loops: a unit's drafted tokens are few, their code should be too.
 template <int NT, bool CAP, bool BIAS>
 __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, const Score<NT>& sc,
                                              const Segment& sg, int j0, int row0, int G, int lane,
-                                             int* bad) {
+                                             uint32_t scratch, int* bad) {
   const int g = lane >> 2, t = lane & 3, n = sg.n, R = n * G;
   const int b = sg.u / p.Hkv, h = sg.u - b * p.Hkv;
   const long long tok0 = (long long)b * p.N, off = (long long)h * kHeadDim;
-  const int q0 = BIAS ? p.q_pos[tok0] : 0;
-  const uint16_t* K = static_cast<const uint16_t*>(p.K);
+  const uint16_t* K = static_cast<const uint16_t*>(p.K) + off + 8 * t;
   float c[NT][4] = {}, up[2], down[2], pos[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int y = 0; y < 2; ++y) {
     const int j = j0 + g + 8 * y;
     uint32_t mx = 0;
     if (j < n) {
-      const uint16_t* k = K + (tok0 + j) * p.kv_stride + off + 8 * t;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(k + 32 * i);
+        const uint4 x = *reinterpret_cast<const uint4*>(K + (tok0 + j) * p.kv_stride + 32 * i);
         mx = max_bits(max_bits(max_bits(max_bits(mx, x.x), x.y), x.z), x.w);
       }
-      if (BIAS) pos[y] = (float)(p.q_pos[tok0 + j] - q0);
+      if (BIAS) pos[y] = (float)(p.q_pos[tok0 + j] - p.q_pos[tok0]);
     }
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
@@ -318,15 +298,14 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
     up[y] = pow2i(e);
     down[y] = pow2i(-e);
   }
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     uint32_t a[2][4];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       const int j = j0 + g + 8 * y;
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (j < n)
-        x = *reinterpret_cast<const uint4*>(K + (tok0 + j) * p.kv_stride + off + 8 * t + 32 * i);
+      if (j < n) x = *reinterpret_cast<const uint4*>(K + (tok0 + j) * p.kv_stride + 32 * i);
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -334,11 +313,16 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
         a[y][k] = pack_f16x2(z.x * up[y], z.y * up[y]);
       }
     }
-    qk<NT>(c, f, 2 * i, a[0][0], a[1][0], a[0][1], a[1][1]);
-    qk<NT>(c, f, 2 * i + 1, a[0][2], a[1][2], a[0][3], a[1][3]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 q = lds128(f.qs + 1024 * (2 * i + k));
+      mma_16816k16_f16(c[0], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], q.x, q.y);
+      if (NT == 2)
+        mma_16816k16_f16(c[NT - 1], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], q.z, q.w);
+    }
   }
   uint32_t see = 0, w[NT][2];
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 4 * NT; ++e) {
     const int r = row0 + 8 * (e >> 2) + 2 * t + (e & 1), j = j0 + g + 8 * ((e >> 1) & 1);
     if (r < R && j < n) {
@@ -347,19 +331,46 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
     }
   }
   weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], pos[0], pos[1], see, w);
+  // values: 64 dims at a time as fp16 rows of 128 bytes (16-byte chunks permuted
+  // by the token's low bits), read back transposed.  A value that fp16 does
+  // not hold enters as 0 and is added by write_row.
   bool out = false;
+  const int tok = lane >> 1, m = lane >> 3, from = (lane & 7) + 8 * (m >> 1);
 #pragma unroll
-  for (int mt = 0; mt < 8; ++mt) {
-    uint32_t a[4];
+  for (int hv = 0; hv < 2; ++hv) {
+    __syncwarp();
+#pragma unroll 1
+    for (int k = 4 * (lane & 1); k < 4 * (lane & 1) + 4; ++k) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (j0 + tok < n)
+        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.V) +
+                                            (tok0 + j0 + tok) * p.kv_stride + off + 64 * hv + 8 * k);
+      uint32_t z[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 y = from16x2(z[e], p.kv_bf16);
+        if (!(fabsf(y.x) <= 65504.0f)) {
+          y.x = 0.0f;
+          out = true;
+        }
+        if (!(fabsf(y.y) <= 65504.0f)) {
+          y.y = 0.0f;
+          out = true;
+        }
+        z[e] = pack_f16x2(y.x, y.y);
+      }
+      sts128(scratch + 128 * tok + ((k ^ (tok & 7)) << 4), make_uint4(z[0], z[1], z[2], z[3]));
+    }
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int j = j0 + 2 * t + 8 * (k >> 1);
-      const long long at = (tok0 + j) * p.kv_stride + off + 16 * mt + 8 * (k & 1) + g;
-      const float x = draft_value(p, at, j < n, out);
-      const float y = draft_value(p, at + p.kv_stride, j + 1 < n, out);
-      a[k] = pack_f16x2(x, y);
+      uint32_t a[4];
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                   : "r"(scratch + 128 * from + (((2 * k + (m & 1)) ^ (from & 7)) << 4))
+                   : "memory");
+      pv<NT>(f, 4 * hv + k, a[0], a[1], a[2], a[3], w);
     }
-    pv<NT>(f, mt, a[0], a[1], a[2], a[3], w);
   }
   if (out) *(volatile int*)bad = 1;
 }
@@ -370,6 +381,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   using S = Shape<NT>;
   using Fixed = RowsFixed<NT>;
   static_assert(sizeof(Fixed) + 1024 <= kRowsTbl, "the tables start at 64 KB");
+  constexpr uint32_t kScratch = sizeof(Fixed::o) / S::kWarps / 16 * 16;   // a warp's, for drafted values
+  static_assert(kScratch >= 2048, "16 tokens, 64 dims");
   extern __shared__ __align__(128) uint8_t raw[];
   Fixed& f = *reinterpret_cast<Fixed*>(raw);
   const uint32_t base = smem_u32(raw);
@@ -430,41 +443,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       } while (f.nseg == 0 && f.unit < p.B * p.Hkv);
     }
   };
-  // A page's entry, in two steps: its id, then its header.
   constexpr int kEach = (kWindow + S::kThreads - 1) / S::kThreads;
-  uint32_t id[kEach];
-  const auto load_ids = [&](const Segment& g, int w0) {
+  const auto load_ids = [&](const Segment& g, int w0, uint32_t (&id)[kEach]) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int k = tid + e * S::kThreads;
       id[e] = k < min(kWindow, g.pages - w0) ? p.ids[g.first + w0 + k] : 0xFFFFFFFFu;
     }
   };
-  const auto make_entries = [&](const Segment& g, int w0) {
+  const auto keep_ids = [&](int buf, const uint32_t (&id)[kEach]) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int k = tid + e * S::kThreads;
-      if (k >= min(kWindow, g.pages - w0)) continue;
-      const int ti = (int)(id[e] >> 30);
-      const uint32_t sl = id[e] & 0x3FFFFFFFu;
-      Entry o = {0, 3, 0};
-      if (ti > 2 || (long long)sl >= p.slots[ti]) {
-        report(p.err, SKV_ERR_CORRUPT);
-      } else {
-        const uint8_t* a = p.pool[ti] + (long long)sl * p.stride[ti];
-        const uint32_t hd = *reinterpret_cast<const uint32_t*>(a);
-        const uint32_t rows = hd & 0xFFFFu;
-        if ((hd >> 16) != ((uint32_t)ti | ((uint32_t)kPageMagic << 8)) || rows > (uint32_t)P) {
-          report(p.err, SKV_ERR_CORRUPT);
-        } else {
-          o.page = reinterpret_cast<unsigned long long>(a);
-          o.tier = (uint32_t)ti;
-          o.rows = rows;
-        }
-      }
-      f.page[k] = o;
-    }
+    for (int e = 0; e < kEach; ++e)
+      if (tid + e * S::kThreads < kWindow) f.ids[buf][tid + e * S::kThreads] = id[e];
   };
+  uint32_t id[kEach];
   if (tid == 0) {
     p.join[c] = make_int2(-1, 0);
     f.bad[0] = f.bad[1] = 0;
@@ -477,8 +469,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   __syncthreads();
   int at_seg = 0, nseg = f.nseg;
   if (nseg == 0) return;
-  load_ids(f.seg[0], 0);
-  make_entries(f.seg[0], 0);
+  load_ids(f.seg[0], 0, id);
+  keep_ids(0, id);
   __syncthreads();
 
   for (int seg = 0;; seg ^= 1) {
@@ -489,18 +481,16 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     const int streams = blocks == 2 ? S::kHalf : S::kWarps;
     const int stream = blocks == 2 ? warp >> 1 : warp;
     const int row0 = blocks == 2 ? S::kRows * (warp & 1) : 0;
-    const int ahead = (kAhead / 16 + streams - 1) / streams * streams;   // parts
-    if (row0 == 0)
-      for (int q = stream; q < min(ahead, min(sg.pages, kWindow) << lgp); q += streams)
-        prefetch_part(f.page[q >> lgp], P, q & (ppp - 1), ppp, lane);
     const long long tok0 = (long long)b * p.N;
     const int q0 = BIAS ? p.q_pos[tok0] : 0;
 
+    const bool more = at_seg + 1 < nseg;
+    if (more) load_ids(f.seg[at_seg + 1], 0, id);
     // the rows as B fragments: fp16 scaled by a power of two a row
     Frag<NT> fr;
     Score<NT> sc;
     sc.cap = p.softcap * 1.4426950408889634f;
-    // (two column blocks: k-step s of a row block at 1 KB steps, in the halves
+    // (also in shared memory: k-step s of a row block at 1 KB steps, in the halves
     // that the tables leave free; a warp's fragments serve all streams)
     fr.qs = tbl + 256 * (64 + 32 * (row0 != 0) + (lane >> 3)) + 128 + 16 * (lane & 7);
 #pragma unroll
@@ -529,10 +519,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         for (int v = 0; v < 4; ++v) {
           const float2 a = from16x2(w[v], p.q_bf16);
           const uint32_t q = pack_f16x2(a.x * up, a.y * up);
-          if (NT == 1)
-            fr.q[4 * y + v] = q;
-          else if (stream == 0)
-            sts32(fr.qs + 1024 * (2 * y + (v >> 1)) + 8 * k + 4 * (v & 1), q);
+          if (NT == 1) fr.q[4 * y + v] = q;
+          if (stream == 0) sts32(fr.qs + 1024 * (2 * y + (v >> 1)) + 8 * k + 4 * (v & 1), q);
         }
       }
       // of the lane's two score columns
@@ -556,61 +544,69 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         fr.acc[k][mt][0] = fr.acc[k][mt][1] = fr.acc[k][mt][2] = fr.acc[k][mt][3] = 0.0f;
     }
 
+    if (more) keep_ids(seg ^ 1, id);
     for (int w0 = 0; w0 < sg.pages || w0 == 0; w0 += kWindow) {
       const int held = min(kWindow, sg.pages - w0);
       if (w0 > 0) {
-        load_ids(sg, w0);
+        load_ids(sg, w0, id);
         __syncthreads();
-        make_entries(sg, w0);
+        keep_ids(seg, id);
         __syncthreads();
       }
       const int store = held << lgp;
       const int total = store + (w0 + kWindow >= sg.pages ? sg.dparts : 0);
       Raw o;
-      o.r[0] = o.r[1] = o.s[0] = o.s[1] = 0;
+      o.r[0] = o.r[1] = o.s[0] = o.s[1] = o.hd = 0;
       o.pos[0] = o.pos[1] = q0;
       const uint8_t* page = nullptr;
       uint32_t tier = 3;
-      int rows = 0, at = 0;
+      int at = 0;
+      // the pages' headers come with their rows: a pass over the headers
+      // alone would wait for a translation per page
       const auto look = [&](int q) {
         tier = 3;
-        rows = 0;
         if (q < store) {
-          const Entry e = f.page[q >> lgp];
+          const uint32_t x = f.ids[seg][q >> lgp], sl = x & 0x3FFFFFFFu;
           at = 16 * (q & (ppp - 1));
-          page = reinterpret_cast<const uint8_t*>(e.page);
-          rows = min((int)e.rows - at, 16);
-          tier = rows > 0 ? e.tier : 3u;
+          tier = x >> 30;
+          if (tier > 2 || (long long)sl >= p.slots[tier]) {
+            if (lane == 0) report(p.err, SKV_ERR_CORRUPT);
+            tier = 3;
+            return;
+          }
+          page = p.pool[tier] + (long long)sl * p.stride[tier];
+          if (tier == SKV_TIER_T0) {
+            if (blocks == 1 || row0 == 0) prefetch_rows(page + kHdrBytes + 256 * at, lane);
+            if (blocks == 1 || row0 > 0) prefetch_rows(page + kHdrBytes + 256 * (P + at), lane);
+          }
         }
       };
       const auto raw_pos = [&](int q) {
         if (BIAS && q < store) {
           const int32_t* a = p.row_pos + ((sg.first + w0 + (q >> lgp)) * P + at + g);
-          if (g < rows) o.pos[0] = a[0];
-          if (g + 8 < rows) o.pos[1] = a[8];
+          o.pos[0] = a[0];   // (of a row that is not there: unused)
+          o.pos[1] = a[8];
         }
       };
-      look(stream);
-      raw_pos(stream);
-      raw_keys(page, tier, at, P, g, t, o);
-      raw_values(page, tier, at, P, t, lane, o);
-      for (int q = stream; q < total; q += streams) {
+      // (the first turn only loads)
+#pragma unroll 1
+      for (int q = stream - streams; q < total; q += streams) {
         if (q >= store) {
           draft_tokens<NT, CAP, BIAS>(p, fr, sc, sg, 16 * (q - store), row0, G, lane,
+                                      smem_u32(&f.o[0][0][0]) + warp * kScratch,
                                       &f.bad[seg]);
           continue;
         }
         const uint8_t* const pg = page;
         const uint32_t ti = tier;
-        const int nr = rows, a0 = at;
-        if (row0 == 0 && q + ahead < store)
-          prefetch_part(f.page[(q + ahead) >> lgp], P, (q + ahead) & (ppp - 1), ppp, lane);
-        if (ti == 3) {
-          look(q + streams);
-          raw_pos(q + streams);
-          raw_keys(page, tier, at, P, g, t, o);
-          raw_values(page, tier, at, P, t, lane, o);
-          continue;
+        const int a0 = at;
+        int nr = 0;
+        if (ti < 3) {
+          if ((o.hd >> 16) != (ti | ((uint32_t)kPageMagic << 8)) || (o.hd & 0xFFFFu) > (uint32_t)P) {
+            if (lane == 0) report(p.err, SKV_ERR_CORRUPT);
+          } else {
+            nr = min((int)(o.hd & 0xFFFFu) - a0, 16);
+          }
         }
         // (one column block: two chains of products, which halves their latency)
         float cc[NT][4] = {}, cd[NT == 1 ? 1 : NT][4] = {};
@@ -620,7 +616,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           posA = (float)(o.pos[0] - q0);
           posB = (float)(o.pos[1] - q0);
         }
-        if (ti == SKV_TIER_T1) {
+        if (nr <= 0) {
+          // nothing there
+        } else if (ti == SKV_TIER_T1) {
           const uint32_t wa[4] = {o.k[0].x, o.k[0].y, o.k[0].z, o.k[0].w};
           const uint32_t wb[4] = {o.k[1].x, o.k[1].y, o.k[1].z, o.k[1].w};
 #pragma unroll
@@ -656,6 +654,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         look(q + streams);
         raw_pos(q + streams);
         raw_keys(page, tier, at, P, g, t, o);
+        if (nr > 0) {
         uint32_t see = ~0u, w[NT][2];
         if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
         see &= (1u << (4 * NT)) - 1;
@@ -687,13 +686,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             pv<NT>(fr, 2 * k + 1, x.z & m0, x.w & m0, y.z & m1, y.w & m1, w);
           }
         }
+        }
         raw_values(page, tier, at, P, t, lane, o);
       }
     }
 
-    // (the next segment's page ids are on their way meanwhile)
-    const bool more = at_seg + 1 < nseg;
-    if (more) load_ids(f.seg[at_seg + 1], 0);
+    if (sg.dparts > 0) __syncthreads();  // (the drafted values' scratch lies where the sums go)
     // the warps' sums meet: the second half's in the first half's registers,
     // those in shared memory (a warp and the one kHalf behind it have the
     // same rows)
@@ -741,7 +739,6 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         }
       }
       __syncthreads();
-      if (half == 1 && more) make_entries(f.seg[at_seg + 1], 0);
     }
     if (tid == 0) f.bad[seg ^ 1] = 0;
     const bool bad = *(volatile int*)&f.bad[seg] != 0;
@@ -782,8 +779,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     at_seg = 0;
     nseg = f.nseg;
     if (nseg == 0) break;
-    load_ids(f.seg[0], 0);
-    make_entries(f.seg[0], 0);
+    load_ids(f.seg[0], 0, id);
+    keep_ids(seg ^ 1, id);
     __syncthreads();
   }
 }
