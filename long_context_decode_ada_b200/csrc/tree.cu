@@ -111,7 +111,7 @@ struct __align__(16) Fixed {
   uint32_t raw[kRawTiles];      // where a tile's raw bytes lie
   unsigned long long scan[kThreads / 32];
   Run run;
-  int abort;
+  int late;                     // a wait gave up
   uint32_t tmem;
   __align__(16) Tile ring[kRing];
   __align__(16) float pos[kStages][kTile];   // positions (from the unit's first q_pos)
@@ -213,24 +213,19 @@ __device__ __forceinline__ unsigned long long operand(uint32_t low) {
   return ((unsigned long long)kDescHigh << 32) | low;
 }
 
-// A bounded wait of a whole warp (about 1 s): false for all lanes when one
-// gave up.
-__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
-                                          int32_t* err) {
+// A bounded wait of a whole warp: false for all lanes after kWaits tries of at
+// most 20 us each (a wait here is on other warps of the block and takes some
+// microseconds).  Every role returns at its first wait that gave up; the error
+// is reported at the end.  Short on purpose: the code stands at some 25 places
+// of five loops that share an instruction cache.
+constexpr int kWaits = 100000;
+__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f) {
   const uint32_t a = smem_u32(&bar);
-  if (__all_sync(0xFFFFFFFFu, mbar_test_wait(a, parity))) return true;
-  const uint32_t t0 = (uint32_t)clock();
 #pragma unroll 1
-  while (!__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(a, parity, 200000u))) {
-    const bool late = (uint32_t)clock() - t0 > 2000000000u;
-    if (!__any_sync(0xFFFFFFFFu, late || *(volatile int*)&f.abort)) continue;
-    if ((threadIdx.x & 31) == 0 && !*(volatile int*)&f.abort) {
-      *(volatile int*)&f.abort = 1;
-      report(err, SKV_ERR_TIMEOUT);
-    }
-    return false;
-  }
-  return true;
+  for (int n = 0; n < kWaits; ++n)
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(a, parity, 20000u))) return true;
+  *(volatile int*)&f.late = 1;
+  return false;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -265,7 +260,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
   // (an end for each team)
   for (int batch = 0; ends < kTeams; ++batch) {
     if (batch >= 2 &&
-        !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f, p.err))
+        !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f))
       break;
     int t_unit = 0, t_n = 0, t_np = 0, t_slot = -1;
     long long t_first = 0;
@@ -386,7 +381,7 @@ __device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t b
     for (; head < t; ++head) mbar_wait_bounded(smem_u32(&f.rawfull[head & 7]), (head >> 3) & 1, &none);
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err)) {
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f)) {
       drain(t);
       return;
     }
@@ -399,7 +394,7 @@ __device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t b
       pos = 0;
     }
     while (held + need + skip > kRawSlots || t - head >= kRawTiles) {
-      if (!warp_wait(f.rawfree[head & 7], (head >> 3) & 1, f, p.err)) {
+      if (!warp_wait(f.rawfree[head & 7], (head >> 3) & 1, f)) {
         drain(t);
         return;
       }
@@ -512,7 +507,7 @@ __device__ __forceinline__ void store_keys(uint32_t page, uint32_t tier, int at0
   } else {
 #pragma unroll 1
     for (int e = 0; e < 8; ++e)
-      sts128(at[e & 1] + ((e >> 1) & 1) * kHalfDims + 1024 * (e >> 2), make_uint4(0, 0, 0, 0));
+      sts128((e & 1 ? at[1] : at[0]) + ((e >> 1) & 1) * kHalfDims + 1024 * (e >> 2), make_uint4(0, 0, 0, 0));
   }
 }
 
@@ -650,7 +645,7 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
   const int w = wd & (kTeamWarps - 1), P = p.P, T0 = 16 * w;
   int t = wd / kTeamWarps;
   uint32_t stage = t, use = 0;   // of tile t: its stage, the stage's tiles before
-  if (!warp_wait(f.dfull[0], 0, f, p.err)) return;
+  if (!warp_wait(f.dfull[0], 0, f)) return;
   for (;;) {
     Tile& d = f.ring[t & (kRing - 1)];
     const uint32_t flags = d.flags;
@@ -658,14 +653,14 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
     const Part x = d.part[w];
     const uint32_t kb = keys_at(base, stage), vb = values_at(base, stage);
     const int y = t & (kRawTiles - 1);
-    if (!warp_wait(f.rawfull[y], (t / kRawTiles) & 1, f, p.err)) return;
+    if (!warp_wait(f.rawfull[y], (t / kRawTiles) & 1, f)) return;
     const uint32_t page = f.raw[y] + x.off + kHdrBytes;
-    if (use > 0 && !warp_wait(f.kempty[stage], (use - 1) & 1, f, p.err)) return;
+    if (use > 0 && !warp_wait(f.kempty[stage], (use - 1) & 1, f)) return;
     const bool draft = (flags & kDraft) != 0;
     if (!draft) store_keys(page, x.tier, x.at, P, kb, T0, lane, base);
     if (BIAS || draft) {
       // (positions and scales are in use until the stage's values are free)
-      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, p.err)) return;
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f)) return;
       if (BIAS && lane < 16) {
         const long long b = d.unit / p.Hkv;
         const int q0 = p.q_pos[b * p.N];
@@ -685,14 +680,14 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     warp_arrive(f.kfull[stage]);
     if (!draft) {
-      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, p.err)) return;
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f)) return;
       store_values(page, x.tier, x.at, x.rows, P, vb, T0, lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     warp_arrive(f.vfull[stage]);
     if (lane == 0) mbar_arrive(smem_u32(&f.rawfree[y]));
     const int t2 = t + kTeams;
-    if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f, p.err)) return;
+    if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f)) return;
     t = t2;
     stage += kTeams;
     if (stage >= kStages) {
@@ -711,22 +706,22 @@ __device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32
   uint32_t segs = 0, stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
       return;
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
     if (flags & kFirst) {
-      if (!warp_wait(f.qfull, segs & 1, f, p.err)) return;
+      if (!warp_wait(f.qfull, segs & 1, f)) return;
       ++segs;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
       s = 0;
     }
-    if (!warp_wait(f.kfull[stage], use & 1, f, p.err)) return;
+    if (!warp_wait(f.kfull[stage], use & 1, f)) return;
     const uint32_t low = kDescKeys | (keys_at(base, stage) >> 4);
 #pragma unroll 1
     for (int y = two ? 1 : 0; y >= 0; --y) {
-      if (!warp_wait(f.sfree[s], (turn >> s) & 1, f, p.err)) return;
-      if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f, p.err)) return;
+      if (!warp_wait(f.sfree[s], (turn >> s) & 1, f)) return;
+      if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
@@ -756,7 +751,7 @@ __device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t
   uint32_t stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
       return;
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
@@ -764,11 +759,11 @@ __device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t
       add = s = 0;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
     }
-    if (!warp_wait(f.vfull[stage], use & 1, f, p.err)) return;
+    if (!warp_wait(f.vfull[stage], use & 1, f)) return;
     const uint32_t low = kDescValues | (values_at(base, stage) >> 4);
 #pragma unroll 1
     for (int y = two ? 1 : 0; y >= 0; --y) {
-      if (!warp_wait(f.pfull[s], (turn >> s) & 1, f, p.err)) return;
+      if (!warp_wait(f.pfull[s], (turn >> s) & 1, f)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
@@ -822,7 +817,7 @@ __device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, flo
     tc_st8(pa + k / 2, w);
   }
   if (r.mine > 0) {
-    if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
+    if (!warp_wait(f.odone[wg], r.turn ^ 1, f)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int k = 0; k < kHeadDim; k += 16) {
@@ -903,7 +898,7 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
       tc_ld16(sa + c + 48, s + 16);
     }
     // (the product before may still read its weights)
-    if (c == 0 && r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return false;
+    if (c == 0 && r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f)) return false;
     tc_st8(pa + c / 2, w);
     tc_st8(pa + c / 2 + 8, w + 8);
   }
@@ -928,10 +923,10 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
   unsigned long long see = 0;
   const auto meet = [&]() {
     warp_arrive(f.sync);
-    return warp_wait(f.sync, syncs++ & 1, f, p.err);
+    return warp_wait(f.sync, syncs++ & 1, f);
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, p.err))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
       return;
     const Tile& d = f.ring[t & (kRing - 1)];
     const uint32_t flags = d.flags;
@@ -1010,7 +1005,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     if (++stage == kStages) stage = 0;
     // one block: the streams take the tiles in turn; two: every tile
     if (nb == 2 || next == 0) {
-      if (!warp_wait(f.sfull[wg], r.turn, f, p.err)) return;
+      if (!warp_wait(f.sfull[wg], r.turn, f)) return;
       tc_fence_after();
       if (busy) {
         const int n = kTile * rc / 128, c0 = copy * n;
@@ -1036,7 +1031,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     if (!(flags & kLast)) continue;
     // the segment's end: the streams' and copies' sums meet, 32 dims at a time
     if (r.mine > 0) {
-      if (!warp_wait(f.odone[wg], r.turn ^ 1, f, p.err)) return;
+      if (!warp_wait(f.odone[wg], r.turn ^ 1, f)) return;
       tc_fence_after();
     }
     const bool bad = *(const volatile int*)&d.bad != 0;
@@ -1133,7 +1128,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
 
   if (tid == 0) {
-    f.abort = 0;
+    f.late = 0;
     for (int k = 0; k < kStages; ++k) {
       mbar_init(smem_u32(&f.kfull[k]), kTeamWarps);
       mbar_init(smem_u32(&f.vfull[k]), kTeamWarps);
@@ -1201,6 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && f.late) report(p.err, SKV_ERR_TIMEOUT);
   if (warp == kMmaS) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
