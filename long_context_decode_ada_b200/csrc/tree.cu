@@ -258,6 +258,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
   int2 join = make_int2(-1, 0);
   Unit x = {};
   // (an end for each team)
+#pragma unroll 1
   for (int batch = 0; ends < kTeams; ++batch) {
     if (batch >= 2 &&
         !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f))
@@ -268,6 +269,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
 #pragma unroll 1
     for (int e = 0; e < kBatch; ++e) {
       // the next unit with a part in this run
+#pragma unroll 1
       while (!open && u < U && cc < run.to) {
         x = unit_of(p, u, RowsCost());
         Share y;

@@ -161,13 +161,16 @@ __device__ __forceinline__ Unit unit_of(const TreeParams& p, int u, Cost rows_co
   Unit x;
   const long long a = max(0, p.indptr[u]), z = min((long long)p.indptr[u + 1], p.page_cap);
   const int b = u / p.Hkv;
-  x.n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
+  // (hidden from the compiler, which would make a loop for every combination)
+  const int32_t *count = p.count, *tier_indptr = p.tier_indptr;
+  const void* K = p.K;
+  asm volatile("" : "+l"(count), "+l"(tier_indptr), "+l"(K));
+  x.n = count ? min(max(count[b], 0), p.N) : p.N;
   x.first = a;
   x.np = (int)max(0ll, z - a);
   int n0 = 0, n1 = x.np;
-  if (p.tier_indptr) {
-    const int t0 = p.tier_indptr[3 * u], t1 = p.tier_indptr[3 * u + 1],
-              t2 = p.tier_indptr[3 * u + 2];
+  if (tier_indptr) {
+    const int t0 = tier_indptr[3 * u], t1 = tier_indptr[3 * u + 1], t2 = tier_indptr[3 * u + 2];
     n0 = min(max(t1 - t0, 0), x.np);
     n1 = min(max(t2 - t1, 0), x.np - n0);
   }
@@ -183,7 +186,7 @@ __device__ __forceinline__ Unit unit_of(const TreeParams& p, int u, Cost rows_co
   x.begin = 2 * Cost::kBegin / p.P;
   if (x.n == 0) {
     x.last = x.cost = 0;
-  } else if (p.K || x.np == 0) {
+  } else if (K || x.np == 0) {
     x.last = x.begin + pages;
     x.cost = x.last + (unsigned long long)(f * ipp);
   } else {
@@ -313,6 +316,7 @@ __device__ __forceinline__ void write_row(const TreeParams& p, int unit, int n, 
     unsigned long long bits = p.mask ? p.mask[tok] : (i == 63 ? ~0ull : (2ull << i) - 1);
     if (n < 64) bits &= (1ull << n) - 1;
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + tok * p.q_stride + (long long)hq * kHeadDim;
+#pragma unroll 1
     while (bits) {
       const int j = __ffsll((long long)bits) - 1;
       bits &= bits - 1;
@@ -328,6 +332,7 @@ __device__ __forceinline__ void write_row(const TreeParams& p, int unit, int n, 
           out = true;
       }
       if (!__any_sync(group, out)) continue;
+#pragma unroll 1
       for (int e = kEach * l; e < kEach * (l + 1); ++e)
         s += from16(q[e], p.q_bf16) * from16(static_cast<const uint16_t*>(p.K)[at + e], p.kv_bf16);
 #pragma unroll

@@ -465,15 +465,19 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     f.nseg = 0;
   }
   __syncthreads();
-  refill();
-  __syncthreads();
-  int at_seg = 0, nseg = f.nseg;
-  if (nseg == 0) return;
-  load_ids(f.seg[0], 0, id);
-  keep_ids(0, id);
-  __syncthreads();
-
+  int at_seg = 0, nseg = 0;
+#pragma unroll 1
   for (int seg = 0;; seg ^= 1) {
+    if (at_seg == nseg) {
+      refill();
+      __syncthreads();
+      at_seg = 0;
+      nseg = f.nseg;
+      if (nseg == 0) break;
+      load_ids(f.seg[0], 0, id);
+      keep_ids(seg, id);
+      __syncthreads();
+    }
     // (read again where it is used: registers are short)
     const Segment& sg = f.seg[at_seg];
     const int b = sg.u / p.Hkv, h = sg.u - b * p.Hkv, R = sg.n * G;
@@ -770,18 +774,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       write_row<CAP, BIAS, 32>(p, sg.u, sg.n, sg.slot, bad, r, M, L, v, 4 * lane, lane);
     }
     __syncthreads();
-    if (more) {
-      ++at_seg;
-      continue;
-    }
-    refill();
-    __syncthreads();
-    at_seg = 0;
-    nseg = f.nseg;
-    if (nseg == 0) break;
-    load_ids(f.seg[0], 0, id);
-    keep_ids(seg ^ 1, id);
-    __syncthreads();
+    ++at_seg;
   }
 }
 
