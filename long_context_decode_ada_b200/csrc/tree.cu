@@ -1023,6 +1023,9 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
           return;
       } else {
         warp_arrive(f.sfree[wg]);
+        // (not ahead of the warps that have rows: the job's weights are complete
+        // when all four have arrived)
+        if (r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f)) return;
       }
       tc_fence_before();
       warp_arrive(f.pfull[wg]);

@@ -227,6 +227,29 @@ def test_split_counts(splits, by_bytes):
     compare(cache, got, q, k=k, v=v, mask=mask)
 
 
+@pytest.mark.parametrize("N,n", [(17, 17), (20, 20), (24, 24), (40, 40), (16, 3), (40, 9)])
+def test_rows_that_leave_lanes_idle(N, n):
+    # long parts of a unit with rows for some of the warps only (68 to 96 rows of
+    # 128, 160 of 256, or few rows of a batch that is laid out for many)
+    cache, _ = make_store([9000, 2000], 1, 4, 16, seed=37, f=(0.05, 0.5, 0.4))
+    q, k, v, par = drafts(2, N, 1, 4, N + n)
+    mask = skv.tree_mask(par).cuda()
+    count = torch.tensor([n, N], dtype=torch.int32, device="cuda")
+    lse = torch.empty((2, N, 4), device="cuda")
+    for splits in (3, 40):
+        got = cache.tree_attention(q, k, v, mask=mask, count=count, lse=lse, num_splits=splits)
+        again, _ = cache.tree_attention(q, k, v, mask=mask, count=count, num_splits=splits)
+        cache.check()
+        assert torch.equal(again[0, :n], got[0][0, :n]) and torch.equal(again[1], got[0][1])
+    keep = [0, n - 1]
+    one = dict(k=k[:, :n], v=v[:, :n], mask=mask[:, :n])
+    ref = tree_reference(cache, q[:, :n].cpu(), **{a: b.cpu() for a, b in one.items()})
+    out = got[0][0].double().cpu().numpy()
+    for i in keep:
+        err = np.abs(out[i] - ref[0][0, i])
+        assert np.all(err <= ref[2][0, i]), float(np.max(err / ref[2][0, i]))
+
+
 def test_same_result_every_call_and_after_other_sizes():
     cache, _ = make_store([3000, 900], 2, 4, 64, seed=19)
     q, k, v, par = drafts(2, 24, 2, 4, 6)
