@@ -792,7 +792,7 @@ __device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t
 
 // ---------------------------------------------------------------- the softmax
 struct Row {           // a lane's row in its stream
-  float c;             // what a product is scaled by (log2 domain, before the cap)
+  float c;             // what a product is scaled by (log2 domain; capped: to x / cap)
   float cap, slope, rel;
   float m, l;
   uint32_t turn;       // parity of the stream's next job
@@ -836,6 +836,41 @@ __device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, flo
   return true;
 }
 
+// s <- cap tanh(s c / cap) (log2 domain): z = s r.c = x / cap.  Where every |z| of
+// the warp is at most 1/2 (scores are usually small beside their cap) by the
+// Taylor series of tanh up to z^13, whose rest is below 5e-8: packed products
+// instead of two of the three special functions a score takes, which are what
+// bounds a job (16 a cycle and SM).  Else by 1 - 2 / (1 + e^(2 z)).
+__device__ __forceinline__ void cap_scores(const Row& r, float (&s)[32]) {
+  float big[2] = {fabsf(s[0]), fabsf(s[1])};
+#pragma unroll
+  for (int k = 2; k < 32; ++k) big[k & 1] = fmaxf(big[k & 1], fabsf(s[k]));
+  if (!__any_sync(0xFFFFFFFFu, !(fmaxf(big[0], big[1]) * r.c <= 0.5f))) {
+    const auto both = [](float x) { return make_float2(x, x); };
+    const float2 c2 = both(r.c), a2 = both(r.cap), none = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float2 z = fma2(make_float2(s[k], s[k + 1]), c2, none), u = fma2(z, z, none);
+      float2 y = fma2(both(21844.0f / 6081075.0f), u, both(-1382.0f / 155925.0f));
+      y = fma2(y, u, both(62.0f / 2835.0f));
+      y = fma2(y, u, both(-17.0f / 315.0f));
+      y = fma2(y, u, both(2.0f / 15.0f));
+      y = fma2(y, u, both(-1.0f / 3.0f));
+      const float2 az = fma2(a2, z, none);
+      y = fma2(fma2(y, u, none), az, az);
+      s[k] = y.x;
+      s[k + 1] = y.y;
+    }
+  } else {
+    const float c = r.c * (2.0f * 1.4426950408889634f);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float e = ex2f(s[k] * c);
+      s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
+    }
+  }
+}
+
 // n columns (32 or 64) of a job, 32 at a time: scores (at sa) to weights (at
 // pa); bits: the columns this row sees.
 template <bool CAP, bool BIAS>
@@ -857,17 +892,11 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
 #pragma unroll
       for (int k = 0; k < 32; ++k) s[k] *= cs[c + k];
     }
-    if (CAP || BIAS) {
+    if (CAP) cap_scores(r, s);
+    if (BIAS) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        if (CAP) {
-          const float e = ex2f(s[k] * r.c);
-          s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
-        } else {
-          s[k] *= r.c;
-        }
-        if (BIAS) s[k] = fmaf(r.slope, pos[c + k] - r.rel, s[k]);
-      }
+      for (int k = 0; k < 32; ++k)
+        s[k] = fmaf(r.slope, pos[c + k] - r.rel, CAP ? s[k] : s[k] * r.c);
     }
     const uint32_t see = (uint32_t)(bits >> c);
     if (see != 0xFFFFFFFFu) {
@@ -986,7 +1015,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       const float log2e = 1.4426950408889634f;
       const float c = p.qk_scale * pow2i(-e);
       if (CAP) {
-        r.c = c * (2.0f * log2e / p.softcap);   // exp2 of it is e^(2 x / cap)
+        r.c = c / p.softcap;
         r.cap = p.softcap * log2e;
       } else {
         r.c = c * log2e;
