@@ -492,9 +492,13 @@ int skv_decode_attention_static(skv_ctx* ctx, const void* q, int q_dtype, int B,
    pos_t the position of a resident token (by row_of) or q_pos[b][j] of a
    drafted one.  A row that sees nothing gives out 0 and lse -inf; rows
    i >= count[b] are left as they were.  Keys and values that a row's mask
-   hides never reach it, whatever they hold (infinities, NaN).  Sums and
-   softmax statistics are fp32; store keys (as decoded), store values and
-   softmax weights enter the tensor cores as fp16. */
+   hides never reach it, whatever they hold (infinities, NaN).  Sums
+   and softmax statistics are fp32; queries, keys (the store's as decoded),
+   values and softmax weights enter the tensor cores as fp16.  Queries and
+   drafted keys are scaled to its range by a power of two a row (bf16 enters
+   exactly, but for elements below 2^-38 of their row's largest); drafted
+   values that fp16 does not hold are added in fp32, those below 2^-25 count
+   as zero. */
 typedef struct skv_tree {
   int32_t N;              /* drafted tokens a sequence, 1..64 */
   int32_t kv_dtype;       /* SKV_Q_FP16 / SKV_Q_BF16: type of K and V */
@@ -525,8 +529,9 @@ int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, i
                             int positions, int num_splits, size_t* bytes);
 /* q, out: [B][N][Hq][128] in q_dtype (out dense); lse: fp32 [B][N][Hq] or
    NULL; score: NULL for plain scores.  Hq/Hkv in {1, 2, 4}.  page_tier_indptr
-   may be NULL.  q, K, V and out must be 16-byte aligned.  The workspace needs
-   no initialisation; calls that overlap in time must not share one.  Stream
+   may be NULL.  num_splits: runs the page list is cut into, 0 (the number of
+   SMs) to 65535.  q, K, V and out must be 16-byte aligned.  The workspace
+   needs no initialisation; calls that overlap in time must not share one.  Stream
    order: as any kernel launch (no early start).  A context with t0_bf16 is
    refused.  Device errors: SKV_ERR_CORRUPT (bad page id, header or row: the
    page or row is skipped), SKV_ERR_TIMEOUT. */
@@ -563,7 +568,8 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
      tier_out, row_of_out, page_indptr_out, page_tier_indptr_out (or NULL),
      page_ids_out (capacity out_cap)   the store after the call; must not
                 overlap the store's own arrays
-     workspace  skv_evict_workspace_size bytes
+     workspace  skv_evict_workspace_size bytes; calls that overlap in time must
+                not share one
    Tmax is at most 2^20.  Device errors: SKV_ERR_POOL (free list or page
    capacity exhausted; the outputs are then unspecified, the old store is
    intact), SKV_ERR_CORRUPT (a kept token's row lies outside the store; its

@@ -1027,7 +1027,7 @@ static bool tree_sizes_ok(int B, int N, int Hq, int Hkv, int64_t page_cap) {
 int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, int64_t page_cap,
                             int positions, int num_splits, size_t* bytes) {
   if (!ctx || !bytes) return fail(SKV_ERR_ARG, "skv_tree_workspace_size: null argument");
-  if (!tree_sizes_ok(B, N, Hq, Hkv, page_cap) || num_splits < 0)
+  if (!tree_sizes_ok(B, N, Hq, Hkv, page_cap) || num_splits < 0 || num_splits > 65535)
     return fail(SKV_ERR_ARG, "skv_tree_workspace_size: bad sizes");
   *bytes = skv::tree_workspace_bytes(page_cap, ctx->P, positions, decode_splits(ctx, num_splits), N,
                                      Hq / Hkv, nullptr, nullptr);
@@ -1043,10 +1043,10 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
   const char* name = "skv_tree_attention";
   if (!ctx || !tree) return fail(SKV_ERR_ARG, "%s: null argument", name);
   if (ctx->t0_bf16) return fail(SKV_ERR_ARG, "%s: not for bf16 T0 pages", name);
-  if (!tree_sizes_ok(B, tree->N, Hq, Hkv, page_cap) || num_splits < 0)
+  if (!tree_sizes_ok(B, tree->N, Hq, Hkv, page_cap) || num_splits < 0 || num_splits > 65535)
     return fail(SKV_ERR_ARG,
                 "%s: need B >= 0, 1 <= N <= 64, Hq/Hkv in {1, 2, 4}, B * Hkv <= 2^20, "
-                "0 <= page_cap <= 2^25, num_splits >= 0",
+                "0 <= page_cap <= 2^25, 0 <= num_splits <= 65535",
                 name);
   if ((q_dtype != SKV_Q_BF16 && q_dtype != SKV_Q_FP16) ||
       (tree->kv_dtype != SKV_Q_BF16 && tree->kv_dtype != SKV_Q_FP16))

@@ -32,16 +32,22 @@
 //                      memory, running maximum and sum, weights back as fp16
 //
 // The two streams have accumulators of their own.  With at most 128 rows they
-// take the tiles in turn, and with at most 64 rows the rows are entered twice, each copy handling half of a job's columns: every lane of
-// tensor memory then has work, and the copies' sums meet at the segment's
-// end.  With more than 128 rows stream b has the rows
-// 128 b .. 128 b + 127 of every tile.  The running maximum is raised (and O
-// rescaled) only when a score passes it by more than 2^8, so weights stay
-// within fp16.
+// take the tiles in turn, and with at most 64 rows the rows are entered twice,
+// each copy handling half of a job's columns: every lane of tensor memory then
+// has work, and the copies' sums meet at the segment's end.  With more than
+// 128 rows stream b has the rows 128 b .. 128 b + 127 of every tile.  The
+// running maximum is raised (and O rescaled) only when a score passes it by
+// more than 2^8, so weights stay within fp16.
 //
-// What costs here is not the products but the instructions around them: the
-// roles' loops are kept short (32 columns of softmax at a time), since straight-line code for four roles starves the
-// schedulers of instructions.
+// What bounds it is neither the products (tensor cores 17% busy) nor HBM but
+// the conversion and the softmax around them: instruction issue, 49% busy at
+// 128 rows, with five roles' loops sharing one instruction cache.  Measured
+// over the 128K store (1.05 M token-heads): 32 tokens (128 rows) 171 us with
+// short waits, 209 us with waits of 35 instructions at their 25 places
+// (instruction cache misses 3.6 M against 0.7 M a launch); pages loaded by the
+// decode warps themselves instead of by bulk copies 231 us; tiles of 64 tokens
+// with one warp issuing both products 274 us.  Three decode teams instead of
+// two change nothing (175 us).
 //
 // Tensor memory (512 columns): Q 0-63 (and 64-127 for the second block), P of
 // the streams at 64 and 96 (over S with two blocks), S at 128 and 192, O at

@@ -13,7 +13,18 @@
 // gather costs less than the products).
 //
 // The loads of a warp's next 16 tokens are issued as soon as the registers
-// of the present ones are free; pages are asked for in L2 some tiles ahead.
+// of the present ones are free.  Shared memory stays at 128 KB: loads in
+// flight pass through the L1, and with 28 KB of it (shared memory full) the
+// ragged batch of 64 with 8 tokens took 487 us against 415.
+//
+// What bounds it: instruction issue (41 to 45% busy with three warps a
+// scheduler; registers allow no more) and the latency behind it; HBM 2.7 TB/s
+// on single tokens over the 128K store (78 us), tensor cores 16% busy on the
+// ragged batch (310 us; 390 us in the tensor-memory form, which wins from 33
+// rows on: its conversion costs the same for 1 row as for 64).  12 warps: 16
+// with 128 registers each spill (biased single tokens 260 us against 214), 8
+// hide less.  L2 prefetches ahead of the loads cost more than they hide (333
+// against 316 us).
 #include <algorithm>
 
 #include "tree.cuh"
@@ -659,37 +670,37 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         raw_pos(q + streams);
         raw_keys(page, tier, at, P, g, t, o);
         if (nr > 0) {
-        uint32_t see = ~0u, w[NT][2];
-        if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
-        see &= (1u << (4 * NT)) - 1;
-        if (NT == 1) {
+          uint32_t see = ~0u, w[NT][2];
+          if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
+          see &= (1u << (4 * NT)) - 1;
+          if (NT == 1) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) cc[0][e] += cd[0][e];
-        }
-        weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, posA, posB, see, w);
-        const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
-        if (ti != SKV_TIER_T0) {
-          const uint32_t s0 = o.s[0] & m0, s1 = o.s[1] & m1;
+            for (int e = 0; e < 4; ++e) cc[0][e] += cd[0][e];
+          }
+          weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, posA, posB, see, w);
+          const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
+          if (ti != SKV_TIER_T0) {
+            const uint32_t s0 = o.s[0] & m0, s1 = o.s[1] & m1;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t va[4] = {o.v[y].x, o.v[y].y, o.v[y].z, o.v[y].w};
-            const uint32_t vb[4] = {o.v[y + 2].x, o.v[y + 2].y, o.v[y + 2].z, o.v[y + 2].w};
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t va[4] = {o.v[y].x, o.v[y].y, o.v[y].z, o.v[y].w};
+              const uint32_t vb[4] = {o.v[y + 2].x, o.v[y + 2].y, o.v[y + 2].z, o.v[y + 2].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t ua = va[k] ^ 0x80808080u, ub = vb[k] ^ 0x80808080u;
+                pv<NT>(fr, 4 * y + k, scaled(ua, 0x4140, s0), scaled(ua, 0x4342, s0),
+                       scaled(ub, 0x4140, s1), scaled(ub, 0x4342, s1), w);
+              }
+            }
+          } else {
+            const uint8_t* a = pg + kHdrBytes + 256 * (P + a0) + 16 * lane;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t ua = va[k] ^ 0x80808080u, ub = vb[k] ^ 0x80808080u;
-              pv<NT>(fr, 4 * y + k, scaled(ua, 0x4140, s0), scaled(ua, 0x4342, s0),
-                     scaled(ub, 0x4140, s1), scaled(ub, 0x4342, s1), w);
+              const uint4 x = ldg128(a + 512 * k), y = ldg128(a + 2048 + 512 * k);
+              pv<NT>(fr, 2 * k, x.x & m0, x.y & m0, y.x & m1, y.y & m1, w);
+              pv<NT>(fr, 2 * k + 1, x.z & m0, x.w & m0, y.z & m1, y.w & m1, w);
             }
           }
-        } else {
-          const uint8_t* a = pg + kHdrBytes + 256 * (P + a0) + 16 * lane;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 x = ldg128(a + 512 * k), y = ldg128(a + 2048 + 512 * k);
-            pv<NT>(fr, 2 * k, x.x & m0, x.y & m0, y.x & m1, y.y & m1, w);
-            pv<NT>(fr, 2 * k + 1, x.z & m0, x.w & m0, y.z & m1, y.w & m1, w);
-          }
-        }
         }
         raw_values(page, tier, at, P, t, lane, o);
       }

@@ -677,7 +677,9 @@ class PagedCache:
         int32 [B].  The result is `into` (made by spare(); a new one when
         None), a store over the same pools whose pages take free slots; this
         store stays as it is, and its pages may be reused once nothing reads
-        it.  Device errors are in the result's error word."""
+        it.  Device errors are in the result's error word.  Calls on one store
+        share its workspace: they must not overlap in time (nor must captured
+        graphs of it)."""
         n = self.B * self.Hkv * self.Tmax
         self._own(score, "score", n, torch.float32)
         self._own(seq_lens, "seq_lens", self.B, torch.int32)

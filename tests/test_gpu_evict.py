@@ -206,6 +206,31 @@ def test_several_blocks_a_unit(T):
         check_eviction(cache, new, want, dev)
 
 
+@pytest.mark.parametrize("T", [4096, 4097, 8200, 32769, 65536, 131072, 131073])
+def test_sizes_where_the_blocks_change(T):
+    # 8 or 16 positions a thread, one to sixteen blocks a sequence's head, and the
+    # first length beyond; sequences that end inside and rows off 16 bytes
+    lens = [T, T // 3 + 1]
+    cache, dev = make_store(lens, 1, 1, 64, f=(0.02, 0.3, 0.5), seed=T % 97)
+    s = scores((2, 1, T), 3, zeros=0.3)
+    s = (s * 8).round() / 8
+    keep = torch.tensor([T // 2 + 3, 40], dtype=torch.int32)
+    new = cache.evict(s.cuda(), dev["seq_lens"], keep.cuda(), sink=3, recent=33)
+    new.check()
+    tier = cache.tier.cpu()
+    want = torch.full_like(tier, 3)
+    pos = torch.arange(T)
+    for b, L in enumerate(lens):
+        res = (tier[b, 0] < 3) & (pos < L)
+        held = res & ((pos < 3) | (pos >= L - 33))
+        key = torch.where(res & ~held, s[b, 0], torch.full((T,), -1.0))
+        order = torch.argsort(key, descending=True, stable=True)[:max(0, int(keep[b]) - int(held.sum()))]
+        stay = held.clone()
+        stay[order[key[order] >= 0]] = True
+        want[b, 0] = torch.where(stay, tier[b, 0], want[b, 0])
+    check_eviction(cache, new, want.numpy(), dev)
+
+
 def test_long_store_without_cached_keys():
     # 2^20 positions: the scores are read again for every digit
     T = 1 << 20

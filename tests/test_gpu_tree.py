@@ -104,6 +104,27 @@ def test_code_variants(kw):
     compare(cache, cache.tree_attention(q, k, v), q, k=k, v=v, **v2)
 
 
+@pytest.mark.parametrize("kw", [dict(ctx_kw=dict(t1_angle_bits=5)), dict(ctx_kw=dict(share_grid=1))])
+@pytest.mark.parametrize("N", [1, 12, 36])
+def test_code_variants_at_other_row_counts(kw, N):
+    cache, _ = make_store([260, 33], 2, 4, 32, seed=45, **kw)
+    q, k, v, _ = drafts(2, N, 2, 4, 19)
+    v2 = dict(t1_53="t1_angle_bits" in kw["ctx_kw"], lloyd="share_grid" in kw["ctx_kw"])
+    compare(cache, cache.tree_attention(q, k, v), q, k=k, v=v, **v2)
+
+
+@pytest.mark.parametrize("N", [2, 40])
+def test_caps_that_some_scores_reach(N):
+    # scores far above the cap beside small ones: both ways of the tanh
+    cache, _ = make_store([1500], 1, 4, 64, seed=47, k_scale=4.0)
+    q, k, v, _ = drafts(1, N, 1, 4, 23)
+    q[:, :, 0] *= 8
+    lse = torch.empty((1, N, 4), device="cuda")
+    for cap in (2.0, 20.0, 500.0):
+        got = cache.tree_attention(q, k, v, softcap=cap, lse=lse)
+        compare(cache, got, q, k=k, v=v, softcap=cap)
+
+
 @pytest.mark.parametrize("N,softcap,bias", [(1, 30.0, False), (7, 5.0, False), (1, 0.0, True),
                                             (20, 0.0, True), (33, 50.0, True)])
 def test_capped_and_biased_scores(N, softcap, bias):
@@ -248,6 +269,40 @@ def test_rows_that_leave_lanes_idle(N, n):
     for i in keep:
         err = np.abs(out[i] - ref[0][0, i])
         assert np.all(err <= ref[2][0, i]), float(np.max(err / ref[2][0, i]))
+
+
+@pytest.mark.parametrize("N", [2, 6, 20, 40])      # 8, 24, 80 and 160 rows a kv head
+def test_values_beyond_fp16(N):
+    # drafted bf16 values that fp16 does not hold: the rows that see them get
+    # them, the others the same bits as without
+    cache, _ = make_store([700, 90], 2, 4, 16, seed=41)
+    q, k, v, _ = drafts(2, N, 2, 4, 5, torch.bfloat16, torch.bfloat16)
+    mask = torch.ones((2, N), dtype=torch.int64)
+    mask[:, N - 1] = (1 << N) - 1                    # the last one sees all, the others token 0
+    clean, _ = cache.tree_attention(q, k, v, mask=mask.cuda())
+    v2 = v.clone()
+    v2[0, 1, 0, 5], v2[0, 1, 1, 127], v2[1, N - 1, 1, 64] = 1e6, -3e5, 7e7
+    lse = torch.empty((2, N, 8), device="cuda")
+    got = cache.tree_attention(q, k, v2, mask=mask.cuda(), lse=lse)
+    compare(cache, got, q, k=k, v=v2, mask=mask)
+    assert torch.equal(got[0][:, :N - 1], clean[:, :N - 1])
+    v2[0, 1, 0, 5], v2[0, 1, 0, 6] = float("inf"), float("nan")
+    out = cache.tree_attention(q, k, v2, mask=mask.cuda())[0]
+    assert torch.equal(out[:, :N - 1], clean[:, :N - 1])
+    assert torch.all(out[0, N - 1, :4, 5] == float("inf")) and torch.isnan(out[0, N - 1, :4, 6]).all()
+
+
+@pytest.mark.parametrize("N", [2, 6, 20, 40])
+def test_a_query_that_is_not_a_number_stays_in_its_row(N):
+    cache, _ = make_store([900], 2, 4, 32, seed=43)
+    q, k, v, _ = drafts(1, N, 2, 4, 15)
+    clean, _ = cache.tree_attention(q, k, v)
+    q[0, 1, 3] = float("nan")
+    lse = torch.empty((1, N, 8), device="cuda")
+    out, _ = cache.tree_attention(q, k, v, lse=lse)
+    assert torch.isnan(out[0, 1, 3]).all() and torch.isnan(lse[0, 1, 3])
+    out[0, 1, 3] = clean[0, 1, 3]
+    assert torch.equal(out, clean)
 
 
 def test_same_result_every_call_and_after_other_sizes():
