@@ -6,7 +6,8 @@
 // enter mma.sync (m16n8k16, A = 16 keys, B = 8 rows of Q) as they come, the
 // weights are transposed between the products by movmatrix, and the values
 // (A = V^T, in the pages' fragment order) go from global memory through the
-// int8 -> fp16 conversion straight into the second product.  No barrier lies
+// int8 -> fp16 conversion (exact) straight into the second product; their scales
+// go with the weights, which enter as two fp16 parts.  No barrier lies
 // between a warp's loads and its sums; the warps' sums meet once per segment
 // in shared memory.  Up to 8 rows a warp has one column block, up to 16 two;
 // with 17 to 32 rows two warps share the tokens, 16 rows each (the second
@@ -84,8 +85,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
-// Lane 4 g + t: rows g, g + 8 of the 16 tokens for keys; rows 2 t, 2 t + 1 of
-// both halves for values.
+// Lane 4 g + t: rows g, g + 8 of the 16 tokens for keys and scales; rows 2 t,
+// 2 t + 1 of both halves for values.
 struct Raw {
   uint4 k[2], v[4];
   uint32_t r[2], s[2];
@@ -118,11 +119,11 @@ __device__ __forceinline__ void raw_keys(const uint8_t* page, uint32_t tier, int
   }
 }
 __device__ __forceinline__ void raw_values(const uint8_t* page, uint32_t tier, int at, int P,
-                                           int t, int lane, Raw& o) {
+                                           int g, int lane, Raw& o) {
   if (tier == SKV_TIER_T1 || tier == SKV_TIER_T2) {
     const uint8_t* a = page + kHdrBytes + (tier == SKV_TIER_T1 ? 66 : 50) * P;
-    o.s[0] = *reinterpret_cast<const uint32_t*>(a + 2 * at + 4 * t);
-    o.s[1] = *reinterpret_cast<const uint32_t*>(a + 2 * at + 4 * t + 16);
+    o.s[0] = *reinterpret_cast<const uint16_t*>(a + 2 * (at + g));
+    o.s[1] = *reinterpret_cast<const uint16_t*>(a + 2 * (at + g) + 16);
     a += 2 * P + 128 * at + 16 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.v[i] = ldg128(a + 512 * i);
@@ -175,13 +176,34 @@ struct Score {
   float slope[NT][2], rel[NT][2];
 };
 
+// Weights (2^4 at most above 1, see kRise) times a value scale (515 at most, as
+// fp16 values have it) times kGain stay within fp16, and small ones stay
+// normal numbers further down.
+constexpr float kRise = 4.0f, kGain = 4.0f;
+
+// Weights as B fragments: each is the sum of two fp16 numbers, so that nothing
+// is lost to their rounding (the products for it cost less than scaling the
+// values, which would round them: one fp16 store 0.0002 off, as its output's
+// rounding alone, against 0.00034).
+template <int NT>
+struct Weights {
+  uint32_t hi[NT][2], lo[NT][2];
+};
+
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = transposed(*reinterpret_cast<const uint32_t*>(&h));
+  lo = transposed(pack_f16x2(x - f.x, y - f.y));
+}
+
 // Scores to weights: c holds the products of tokens g, g + 8, rA / rB what
-// the keys are scaled by; bit 4 n + e of `see`: the score counts.  The
-// weights leave as B fragments (fp16; sums are taken before the rounding).
+// the keys are scaled by, vA / vB what the values are; bit 4 n + e of `see`:
+// the score counts.
 template <int NT, bool CAP, bool BIAS>
 __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float (&c)[NT][4],
-                                        float rA, float rB, float posA, float posB, uint32_t see,
-                                        uint32_t (&b)[NT][2]) {
+                                        float rA, float rB, float vA, float vB, float posA,
+                                        float posB, uint32_t see, Weights<NT>& b) {
   constexpr uint32_t kAll = (1u << (4 * NT)) - 1;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -200,7 +222,7 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
     for (int k = 0; k < 4 * NT; ++k)
       if (!((see >> k) & 1)) c[k >> 2][k & 3] = -INFINITY;
   }
-  // z = score - maximum; above kRaise (or without a maximum: not a number or
+  // z = score - maximum; above kRise (or without a maximum: not a number or
   // infinite) the maximum rises first
   float z[NT][4], top = -INFINITY;
   const auto less = [&](int n, int e, float m) {
@@ -213,7 +235,7 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
       z[n][e] = less(n, e, f.m[n][e & 1]);
       top = fmaxf(top, z[n][e]);
     }
-  if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
+  if (__any_sync(0xFFFFFFFFu, top > kRise)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float a[2];
@@ -223,7 +245,7 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
         x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-        x = x > f.m[n][j] + kRaise ? x : f.m[n][j];
+        x = x > f.m[n][j] + kRise ? x : f.m[n][j];
         a[j] = x == f.m[n][j] ? 1.0f : ex2f(f.m[n][j] - x);
         f.m[n][j] = x;
         f.l[n][j] *= a[j];
@@ -254,16 +276,18 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
     const float w0 = ex2f(z[n][0]), w1 = ex2f(z[n][1]), w2 = ex2f(z[n][2]), w3 = ex2f(z[n][3]);
     f.l[n][0] += w0 + w2;
     f.l[n][1] += w1 + w3;
-    b[n][0] = transposed(pack_f16x2(w0, w1));
-    b[n][1] = transposed(pack_f16x2(w2, w3));
+    split(w0 * vA, w1 * vA, b.hi[n][0], b.lo[n][0]);
+    split(w2 * vB, w3 * vB, b.hi[n][1], b.lo[n][1]);
   }
 }
 
 template <int NT>
 __device__ __forceinline__ void pv(Frag<NT>& f, int mt, uint32_t a0, uint32_t a1, uint32_t a2,
-                                   uint32_t a3, const uint32_t (&b)[NT][2]) {
+                                   uint32_t a3, const Weights<NT>& b) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) mma_16816k16_f16(f.acc[n][mt], a0, a1, a2, a3, b[n][0], b[n][1]);
+  for (int n = 0; n < NT; ++n) mma_16816k16_f16(f.acc[n][mt], a0, a1, a2, a3, b.lo[n][0], b.lo[n][1]);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mma_16816k16_f16(f.acc[n][mt], a0, a1, a2, a3, b.hi[n][0], b.hi[n][1]);
 }
 
 // both halves of a mask of rows 2 t, 2 t + 1 that lie below `rows`
@@ -271,13 +295,12 @@ __device__ __forceinline__ uint32_t pair_mask(int row, int rows) {
   return (row < rows ? 0xFFFFu : 0u) | (row + 1 < rows ? 0xFFFF0000u : 0u);
 }
 
-// int8 values (two words of a tile row) to fp16, times the rows' scales: v + 128
-// as the low byte of 1024 + x, less 1152 (exact), then one rounding
-__device__ __forceinline__ uint32_t scaled(uint32_t u, uint32_t sel, uint32_t s) {
+// int8 values to fp16: v + 128 as the low byte of 1024 + x, less 1152 (exact)
+__device__ __forceinline__ uint32_t whole(uint32_t u, uint32_t sel) {
   const uint32_t x = __byte_perm(u, 0x64646464u, sel);
   const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
-  return hmul2(*reinterpret_cast<const uint32_t*>(&h), s);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // 16 drafted tokens from j0 on (scratch: 2 KB of shared memory of the warp).
@@ -332,7 +355,8 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
         mma_16816k16_f16(c[NT - 1], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], q.z, q.w);
     }
   }
-  uint32_t see = 0, w[NT][2];
+  uint32_t see = 0;
+  Weights<NT> w;
 #pragma unroll 1
   for (int e = 0; e < 4 * NT; ++e) {
     const int r = row0 + 8 * (e >> 2) + 2 * t + (e & 1), j = j0 + g + 8 * ((e >> 1) & 1);
@@ -341,7 +365,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
       if (p.mask ? (p.mask[tok0 + i] >> j) & 1 : j <= i) see |= 1u << e;
     }
   }
-  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], pos[0], pos[1], see, w);
+  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], kGain, kGain, pos[0], pos[1], see, w);
   // values: 64 dims at a time as fp16 rows of 128 bytes (16-byte chunks permuted
   // by the token's low bits), read back transposed.  A value that fp16 does
   // not hold enters as 0 and is added by write_row.
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         // (one column block: two chains of products, which halves their latency)
         float cc[NT][4] = {}, cd[NT == 1 ? 1 : NT][4] = {};
         float(&co)[NT][4] = NT == 1 ? cd : cc;
-        float rA = 1.0f, rB = 1.0f, posA = 0.0f, posB = 0.0f;
+        float rA = 1.0f, rB = 1.0f, vA = kGain, vB = kGain, posA = 0.0f, posB = 0.0f;
         if (BIAS) {
           posA = (float)(o.pos[0] - q0);
           posB = (float)(o.pos[1] - q0);
@@ -665,22 +689,24 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         if (ti != SKV_TIER_T0) {
           rA = __half2float(__ushort_as_half((uint16_t)o.r[0]));
           rB = __half2float(__ushort_as_half((uint16_t)o.r[1]));
+          // (rows that are not there may hold anything)
+          vA = g < nr ? kGain * __half2float(__ushort_as_half((uint16_t)o.s[0])) : 0.0f;
+          vB = g + 8 < nr ? kGain * __half2float(__ushort_as_half((uint16_t)o.s[1])) : 0.0f;
         }
         look(q + streams);
         raw_pos(q + streams);
         raw_keys(page, tier, at, P, g, t, o);
         if (nr > 0) {
-          uint32_t see = ~0u, w[NT][2];
+          uint32_t see = ~0u;
+          Weights<NT> w;
           if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
           see &= (1u << (4 * NT)) - 1;
           if (NT == 1) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) cc[0][e] += cd[0][e];
           }
-          weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, posA, posB, see, w);
-          const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
+          weights<NT, CAP, BIAS>(fr, sc, cc, rA, rB, vA, vB, posA, posB, see, w);
           if (ti != SKV_TIER_T0) {
-            const uint32_t s0 = o.s[0] & m0, s1 = o.s[1] & m1;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint32_t va[4] = {o.v[y].x, o.v[y].y, o.v[y].z, o.v[y].w};
@@ -688,11 +714,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t ua = va[k] ^ 0x80808080u, ub = vb[k] ^ 0x80808080u;
-                pv<NT>(fr, 4 * y + k, scaled(ua, 0x4140, s0), scaled(ua, 0x4342, s0),
-                       scaled(ub, 0x4140, s1), scaled(ub, 0x4342, s1), w);
+                pv<NT>(fr, 4 * y + k, whole(ua, 0x4140), whole(ua, 0x4342), whole(ub, 0x4140),
+                       whole(ub, 0x4342), w);
               }
             }
           } else {
+            const uint32_t m0 = pair_mask(2 * t, nr), m1 = pair_mask(2 * t + 8, nr);
             const uint8_t* a = pg + kHdrBytes + 256 * (P + a0) + 16 * lane;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -702,7 +729,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             }
           }
         }
-        raw_values(page, tier, at, P, t, lane, o);
+        raw_values(page, tier, at, P, g, lane, o);
       }
     }
 
@@ -775,7 +802,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int k = 0; k < S::kHalf / blocks; ++k) {
-        const float ak = __shfl_sync(0xFFFFFFFFu, a, k);
+        const float ak = __shfl_sync(0xFFFFFFFFu, a, k) * (1.0f / kGain);
         const float4 x = *reinterpret_cast<const float4*>(&f.o[blocks * k + blk][lr][4 * lane]);
         v[0] += ak * x.x;
         v[1] += ak * x.y;
