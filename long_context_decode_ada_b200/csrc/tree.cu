@@ -49,6 +49,13 @@
 // with one warp issuing both products 274 us.  Three decode teams instead of
 // two change nothing (175 us).
 //
+// Roundings: a coded key is a table entry times its radius (two fp16
+// roundings), a value an int8 times its scale (one), a weight one; each is
+// 2^-11 of its number at most.  Together they put an output about 0.0004 of
+// its size off; bf16 outputs are rounded by 0.0017 anyway, fp16 ones by 0.0002.
+// Exact values and split weights, as in the form for few rows, would double
+// the second product and need 64 columns of tensor memory that are not there.
+//
 // Tensor memory (512 columns): Q 0-63 (and 64-127 for the second block), P of
 // the streams at 64 and 96 (over S with two blocks), S at 128 and 192, O at
 // 256 and 384.

@@ -6,8 +6,8 @@
 // enter mma.sync (m16n8k16, A = 16 keys, B = 8 rows of Q) as they come, the
 // weights are transposed between the products by movmatrix, and the values
 // (A = V^T, in the pages' fragment order) go from global memory through the
-// int8 -> fp16 conversion (exact) straight into the second product; their scales
-// go with the weights, which enter as two fp16 parts.  No barrier lies
+// int8 -> fp16 conversion (exact) straight into the second product; their
+// scales go with the weights, which enter as two fp16 parts.  No barrier lies
 // between a warp's loads and its sums; the warps' sums meet once per segment
 // in shared memory.  Up to 8 rows a warp has one column block, up to 16 two;
 // with 17 to 32 rows two warps share the tokens, 16 rows each (the second
@@ -21,7 +21,7 @@
 // What bounds it: instruction issue (41 to 45% busy with three warps a
 // scheduler; registers allow no more) and the latency behind it; HBM 2.7 TB/s
 // on single tokens over the 128K store (78 us), tensor cores 16% busy on the
-// ragged batch (310 us; 390 us in the tensor-memory form, which wins from 33
+// ragged batch (323 us; 390 us in the tensor-memory form, which wins from 33
 // rows on: its conversion costs the same for 1 row as for 64).  12 warps: 16
 // with 128 registers each spill (biased single tokens 260 us against 214), 8
 // hide less.  L2 prefetches ahead of the loads cost more than they hide (333

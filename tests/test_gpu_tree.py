@@ -271,6 +271,51 @@ def test_rows_that_leave_lanes_idle(N, n):
         assert np.all(err <= ref[2][0, i]), float(np.max(err / ref[2][0, i]))
 
 
+@pytest.mark.parametrize("N", [2, 5, 12, 33])
+def test_long_runs(N):
+    # one run with more pages of a unit than are held at once and more units than
+    # are looked up at once, some of them empty or without drafted tokens
+    lens = [9100] + [(37 * b) % 150 for b in range(21)]
+    cache, _ = make_store(lens, 2, 4, 16, seed=49, f=(0.1, 0.5, 0.4))
+    B = len(lens)
+    q, k, v, _ = drafts(B, N, 2, 4, 27)
+    count = torch.tensor([N if b % 4 != 2 else 0 for b in range(B)], dtype=torch.int32)
+    lse = torch.empty((B, N, 8), device="cuda")
+    outs = []
+    for splits in (1, 3, 0):
+        out, _ = cache.tree_attention(q, k, v, count=count.cuda(), lse=lse, num_splits=splits)
+        outs.append(out)
+    cache.check()
+    # other runs round other sums: half a bf16 step and the weights' roundings apart
+    for out in outs[:2]:
+        assert torch.all((out.float() - outs[2].float()).abs() <= 2.0 ** -7 * outs[2].float().abs() + 4e-3)
+    few = [0, 1, 2, 3, 21]
+    sub = [x[few] for x in (q, k, v)]
+    ref = tree_reference(_Part(cache, few), sub[0].cpu(), k=sub[1].cpu(), v=sub[2].cpu(), count=count[few])
+    got = outs[0][few].double().cpu().numpy()
+    for i, b in enumerate(few):
+        n = int(count[b])
+        assert np.all(np.abs(got[i, :n] - ref[0][i, :n]) <= ref[2][i, :n])
+        assert torch.all(outs[0][b, n:] == 0)
+
+
+class _Part:
+    """Some sequences of a store, as tree_reference reads one."""
+
+    def __init__(self, cache, seqs):
+        self.ctx, self.Hkv, self.B = cache.ctx, cache.Hkv, len(seqs)
+        self.pools, self.stride, self.payload = cache.pools, cache.stride, cache.payload
+        ptr = cache.page_indptr.cpu()
+        ids, to = [], [0]
+        for b in seqs:
+            for h in range(cache.Hkv):
+                a, z = int(ptr[b * cache.Hkv + h]), int(ptr[b * cache.Hkv + h + 1])
+                ids.append(cache.page_ids[a:z].cpu())
+                to.append(to[-1] + z - a)
+        self.page_indptr, self.page_ids = torch.tensor(to), torch.cat(ids)
+        self.row_of = cache.row_of[seqs]
+
+
 @pytest.mark.parametrize("N", [2, 6, 20, 40])      # 8, 24, 80 and 160 rows a kv head
 def test_values_beyond_fp16(N):
     # drafted bf16 values that fp16 does not hold: the rows that see them get
