@@ -530,8 +530,8 @@ int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, i
 /* q, out: [B][N][Hq][128] in q_dtype (out dense); lse: fp32 [B][N][Hq] or
    NULL; score: NULL for plain scores.  Hq/Hkv in {1, 2, 4}.  page_tier_indptr
    may be NULL.  num_splits: runs the page list is cut into, 0 (the number of
-   SMs) to 65535.  q, K, V and out must be 16-byte aligned.  The workspace
-   needs no initialisation; calls that overlap in time must not share one.  Stream
+   SMs) to 65535.  q, K, V and out must be 16-byte aligned, and out must
+   not overlap the others.  The workspace needs no initialisation; calls that overlap in time must not share one.  Stream
    order: as any kernel launch (no early start).  A context with t0_bf16 is
    refused.  Device errors: SKV_ERR_CORRUPT (bad page id, header or row: the
    page or row is skipped), SKV_ERR_TIMEOUT. */
@@ -564,6 +564,7 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
      tier ... page_ids, page_cap  the store (page_cap: capacity of page_ids)
      free, free_cursor  device free lists and int32 [3] cursors (read only);
                 free_cursor_out: int32 [3] device or NULL, the cursors after the call
+                (not free_cursor itself)
      pools      holds the old and the new pages
      tier_out, row_of_out, page_indptr_out, page_tier_indptr_out (or NULL),
      page_ids_out (capacity out_cap)   the store after the call; must not

@@ -1071,6 +1071,8 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(tree->K) | reinterpret_cast<uintptr_t>(tree->V)) & 15)
     return fail(SKV_ERR_ARG, "%s: q, K, V and out must be 16-byte aligned", name);
+  if (out == q || out == tree->K || out == tree->V)
+    return fail(SKV_ERR_ARG, "%s: out must not be q, K or V", name);
   size_t need = 0;
   const int rc = skv_tree_workspace_size(ctx, B, tree->N, Hq, Hkv, page_cap, bias, num_splits, &need);
   if (rc != SKV_OK) return rc;
@@ -1168,9 +1170,12 @@ int skv_evict(skv_ctx* ctx, int B, int Hkv, int64_t Tmax, const int32_t* seq_len
       (Tmax > 0 && (!score || !tier || !row_of || !tier_out || !row_of_out)) ||
       (page_cap > 0 && !page_ids) || (out_cap > 0 && !page_ids_out))
     return fail(SKV_ERR_ARG, "%s: null argument", name);
-  if (tier == tier_out || row_of == row_of_out || page_indptr == page_indptr_out ||
-      page_ids == page_ids_out)
+  // (an empty store's arrays may all be NULL)
+  if ((tier && tier == tier_out) || (row_of && row_of == row_of_out) ||
+      page_indptr == page_indptr_out || (page_ids && page_ids == page_ids_out))
     return fail(SKV_ERR_ARG, "%s: the new store's arrays must not be the old one's", name);
+  if (free_cursor == free_cursor_out)
+    return fail(SKV_ERR_ARG, "%s: free_cursor_out must not be free_cursor", name);
   const size_t need = skv::evict_workspace_bytes(B, Hkv, Tmax, ctx->P);
   if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15))
     return fail(SKV_ERR_ARG, "%s: a 16-byte aligned workspace of %zu bytes needed", name, need);

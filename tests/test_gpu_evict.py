@@ -1,6 +1,8 @@
 """Eviction on the GPU: the kept set against a plain sort, tables and page
 bytes exact, ties, held tokens, odd sizes, several blocks per unit, refusals,
 and a run with the decode, the tree attention and the append around it."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -267,6 +269,26 @@ def test_pool_and_row_errors():
     with pytest.raises(skv.SkvError) as e:
         new.check()
     assert e.value.code == skv.SKV_ERR_CORRUPT
+
+
+def test_a_store_without_tokens():
+    ctx = skv.Context(16)
+    fl, pools = skv.SkvFreeLists(), skv.SkvPools()
+    i32 = lambda n, x: torch.full((n,), x, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, keep, err, cursor, old = i32(2, 0), i32(2, 5), i32(1, 0), i32(3, 0), i32(7, 0)
+    after, new, tiers = i32(3, -1), i32(7, -1), i32(19, -1)
+    size = C.c_size_t()
+    assert skv.lib().skv_evict_workspace_size(ctx.handle, 2, 3, 0, C.byref(size)) == skv.SKV_OK
+    ws = torch.empty(max(size.value, 16), dtype=torch.uint8, device="cuda")
+    at = lambda t: C.c_void_p(t.data_ptr())  # noqa: E731
+    rc = skv.lib().skv_evict(
+        ctx.handle, 2, 3, 0, at(lens), None, None, at(keep), 1, 1, None, None, at(old), None, 0,
+        C.byref(fl), at(cursor), C.byref(pools), None, None, at(new), at(tiers), None, 0, at(after),
+        at(err), at(ws), ws.numel(), C.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == skv.SKV_OK, skv.lib().skv_last_error()
+    torch.cuda.synchronize()
+    assert new.eq(0).all() and tiers.eq(0).all() and int(err) == 0
+    assert after.eq(0).all()
 
 
 def test_refusals():

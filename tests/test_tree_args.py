@@ -53,6 +53,18 @@ def test_calls_are_refused_before_the_gpu(bad):
     assert len(skv.lib().skv_last_error()) > 10
 
 
+def test_out_over_its_inputs_is_refused():
+    for K, V, out in ((0, 0, 16), (32, 64, 32), (32, 64, 64)):
+        t = skv.SkvTree(N=4, kv_dtype=skv.Q_FP16)
+        t.K, t.V = K or None, V or None
+        pools = skv.SkvPools()
+        # (neither a workspace nor anything to read: the call cannot get past its checks)
+        rc = skv.lib().skv_tree_attention(
+            skv.Context(16).handle, 16, skv.Q_BF16, 2, 8, 2, C.byref(t), None, 128, None, None, 0,
+            C.byref(pools), out, None, 128, None, 0, 0, None)
+        assert rc == skv.SKV_ERR_ARG and b"out must not be" in skv.lib().skv_last_error()
+
+
 def test_a_batch_of_none_and_bf16_stores():
     assert call(skv.Context(16), B=0) == skv.SKV_OK
     assert call(skv.Context(16, t0_bf16=True), B=0) == skv.SKV_ERR_ARG
@@ -74,3 +86,21 @@ def test_evict_sizes():
     assert f(ctx.handle, 2, 8, 1000, C.byref(n)) == skv.SKV_OK and n.value >= 4 * 16 * 1000
     for B, H, T in ((-1, 8, 10), (1, 0, 10), (1, 8, -1), (1, 8, (1 << 20) + 1), (1 << 20, 8, 10)):
         assert f(ctx.handle, B, H, T, C.byref(n)) == skv.SKV_ERR_ARG
+
+
+def evict_call(indptr=16, ids=None, indptr_out=32, ids_out=None, cursor=48, cursor_out=None):
+    """A store without tokens; no workspace: the call cannot get past its checks."""
+    fl, pools = skv.SkvFreeLists(), skv.SkvPools()
+    rc = skv.lib().skv_evict(
+        skv.Context(16).handle, 1, 2, 0, 64, None, None, 80, 0, 0, None, None, indptr, ids, 0,
+        C.byref(fl), cursor, C.byref(pools), None, None, indptr_out, None, ids_out, 0, cursor_out,
+        96, None, 0, None)
+    assert rc == skv.SKV_ERR_ARG
+    return skv.lib().skv_last_error()
+
+
+def test_evict_arrays_of_their_own():
+    assert b"cursor" in evict_call(cursor_out=48)
+    assert b"the old one's" in evict_call(indptr_out=16)
+    assert b"the old one's" in evict_call(ids=128, ids_out=128)
+    assert b"workspace" in evict_call(cursor_out=112)            # an empty store's NULLs are no overlap
