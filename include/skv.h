@@ -514,7 +514,7 @@ typedef struct skv_tree {
 } skv_tree;
 
 typedef struct skv_score {
-  float softcap;            /* finite, >= 0 (0: none) */
+  float softcap;            /* 0 (none) or 2^-40 to 2^40 */
   int32_t reserved;         /* zero */
   const float* slopes;      /* fp32 [Hq] device, or NULL: no bias; the rest is then unused */
   const int32_t* q_pos;     /* int32 [B][N] device: positions of the drafted tokens */

@@ -1058,8 +1058,8 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
       qs > (1LL << 31) || ks > (1LL << 31))
     return fail(SKV_ERR_ARG, "%s: strides must cover a token and be multiples of 8", name);
   const float cap = score ? score->softcap : 0.0f;
-  if (!(cap >= 0.0f) || std::isinf(cap))
-    return fail(SKV_ERR_ARG, "%s: softcap must be finite and not negative", name);
+  if (cap != 0.0f && !(cap >= std::ldexp(1.0f, -40) && cap <= std::ldexp(1.0f, 40)))
+    return fail(SKV_ERR_ARG, "%s: softcap must be 0 (none) or lie within 2^-40 and 2^40", name);
   const bool bias = score && score->slopes;
   if (bias && (!score->q_pos || !score->row_of || !score->seq_lens || score->Tmax < 0 ||
                score->Tmax > (1LL << 23)))

@@ -855,9 +855,9 @@ __device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, flo
 
 // s <- cap tanh(s c / cap) (log2 domain): z = s r.c = x / cap.  Where every |z| of
 // the warp is at most 1/2 (scores are usually small beside their cap) by the
-// Taylor series of tanh up to z^13, whose rest is below 5e-8: packed products
-// instead of two of the three special functions a score takes, which are what
-// bounds a job (16 a cycle and SM).  Else by 1 - 2 / (1 + e^(2 z)).
+// series of cap_series: packed products instead of two of the three special
+// functions a score takes, which are what bounds a job (16 a cycle and SM).
+// Else by 1 - 2 / (1 + e^(2 z)), with a high cap score by score (cap_any).
 __device__ __forceinline__ void cap_scores(const Row& r, float (&s)[32]) {
   float big[2] = {fabsf(s[0]), fabsf(s[1])};
 #pragma unroll
@@ -878,13 +878,16 @@ __device__ __forceinline__ void cap_scores(const Row& r, float (&s)[32]) {
       s[k] = y.x;
       s[k + 1] = y.y;
     }
-  } else {
-    const float c = r.c * (2.0f * 1.4426950408889634f);
+  } else if (r.cap <= kLowCap * 1.4426950408889634f) {
+    const float c = fminf(r.c * (2.0f * 1.4426950408889634f), 3.0e38f);
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float e = ex2f(s[k] * c);
       s[k] = fmaf(-2.0f * r.cap, rcpf(1.0f + e), r.cap);
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[k] = cap_any(s[k] * r.c, r.cap);
   }
 }
 
@@ -1032,7 +1035,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       const float log2e = 1.4426950408889634f;
       const float c = p.qk_scale * pow2i(-e);
       if (CAP) {
-        r.c = c / p.softcap;
+        r.c = fminf(c / p.softcap, 3.0e38f);   // (0 times it stays 0)
         r.cap = p.softcap * log2e;
       } else {
         r.c = c * log2e;

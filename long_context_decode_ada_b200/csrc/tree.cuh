@@ -142,6 +142,26 @@ __device__ __forceinline__ void prefetch_page(const uint8_t* a, int P, int tier)
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(bytes) : "memory");
 }
 
+// cap tanh(z) for |z| at most 1/2: the Taylor series up to z^13, whose rest is
+// below 5e-8.  (1 - 2 / (1 + e^(2 z)) is off by some 3e-7 whatever z: with a cap
+// far above the scores, by more than the scores.)
+__device__ __forceinline__ float cap_series(float z, float cap) {
+  const float u = z * z, az = cap * z;
+  float y = fmaf(21844.0f / 6081075.0f, u, -1382.0f / 155925.0f);
+  y = fmaf(y, u, 62.0f / 2835.0f);
+  y = fmaf(y, u, -17.0f / 315.0f);
+  y = fmaf(y, u, 2.0f / 15.0f);
+  y = fmaf(y, u, -1.0f / 3.0f);
+  return fmaf(y * u, az, az);
+}
+// Caps up to which 1 - 2 / (1 + e^(2 z)) serves for every z: it is then off by at
+// most 6e-5 of a weight (an fp16 result's rounding is 5e-4).
+constexpr float kLowCap = 128.0f;
+__device__ __forceinline__ float cap_any(float z, float cap) {
+  const float x = fmaf(-2.0f * cap, rcpf(1.0f + ex2f(z * (2.0f * 1.4426950408889634f))), cap);
+  return fabsf(z) <= 0.5f ? cap_series(z, cap) : x;
+}
+
 // ------------------------------------------------------------------ the split
 // Pages of a unit by tier and their costs.  A dense page's bytes take 2.6
 // times a coded one's, but its conversion less: it counts twice.  A unit's

@@ -170,10 +170,13 @@ __device__ __forceinline__ uint32_t tbl2(const uint4& w, int j, uint32_t tb) {
   return lds32((xn & 0xF00u) | (xc & 0x3000u) | tb);
 }
 
+// CAP: 0 none, 1 up to kLowCap, 2 above it by cap_any (one capped token over the
+// 128K context: 87 us with it, 81 without).
+
 // What a warp knows of its rows' scores (columns 2 t, 2 t + 1 of block n).
 template <int NT>
 struct Score {
-  float c[NT][2];         // what a product is scaled by (log2 domain, before the cap)
+  float c[NT][2];         // what a product is scaled by: to the log2 domain, or to parts of the cap
   float cap;
   float slope[NT][2], rel[NT][2];
 };
@@ -202,7 +205,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& 
 // Scores to weights: c holds the products of tokens g, g + 8, rA / rB what
 // the keys are scaled by, vA / vB what the values are; bit 4 n + e of `see`:
 // the score counts.
-template <int NT, bool CAP, bool BIAS>
+template <int NT, int CAP, bool BIAS>
 __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float (&c)[NT][4],
                                         float rA, float rB, float vA, float vB, float posA,
                                         float posB, uint32_t see, Weights<NT>& b) {
@@ -214,7 +217,8 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
       const int j = e & 1;
       float x = c[n][e] * (e < 2 ? rA : rB);
       if (CAP || BIAS) x *= sc.c[n][j];
-      if (CAP) x = fmaf(-2.0f * sc.cap, rcpf(1.0f + ex2f(x)), sc.cap);
+      if (CAP == 1) x = fmaf(-2.0f * sc.cap, rcpf(1.0f + ex2f(x)), sc.cap);
+      if (CAP == 2) x = cap_any(x, sc.cap);
       if (BIAS) x = fmaf(sc.slope[n][j], (e < 2 ? posA : posB) - sc.rel[n][j], x);
       c[n][e] = x;
     }
@@ -307,7 +311,7 @@ __device__ __forceinline__ uint32_t whole(uint32_t u, uint32_t sel) {
 
 // 16 drafted tokens from j0 on (scratch: 2 KB of shared memory of the warp).
 // Rolled loops: a unit's drafted tokens are few, their code should be too.
-template <int NT, bool CAP, bool BIAS>
+template <int NT, int CAP, bool BIAS>
 __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, const Score<NT>& sc,
                                              const Segment& sg, int j0, int row0, int G, int lane,
                                              uint32_t scratch, int* bad) {
@@ -412,7 +416,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
   if (out) *(volatile int*)bad = 1;
 }
 
-template <int NT, bool CAP, bool BIAS>
+template <int NT, int CAP, bool BIAS>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     tree_rows_kernel(const __grid_constant__ TreeParams p) {
   using S = Shape<NT>;
@@ -565,8 +569,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         }
       }
       // of the lane's two score columns
-      const float scale = p.qk_scale * pow2i(-e) * 1.4426950408889634f *
-                          (CAP ? 2.0f / sc.cap * 1.4426950408889634f : 1.0f);
+      float scale = p.qk_scale * pow2i(-e);
+      if (CAP)   // (0 times it stays 0)
+        scale = fminf(scale * (CAP == 1 ? 2.0f * 1.4426950408889634f : 1.0f) / p.softcap, 3.0e38f);
+      else
+        scale *= 1.4426950408889634f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         sc.c[k][j] = __shfl_sync(0xFFFFFFFFu, scale, 8 * t + 4 * j);
@@ -811,14 +818,14 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         v[2] += ak * x.z;
         v[3] += ak * x.w;
       }
-      write_row<CAP, BIAS, 32>(p, sg.u, sg.n, sg.slot, bad, r, M, L, v, 4 * lane, lane);
+      write_row<CAP != 0, BIAS, 32>(p, sg.u, sg.n, sg.slot, bad, r, M, L, v, 4 * lane, lane);
     }
     __syncthreads();
     ++at_seg;
   }
 }
 
-template <int NT, bool CAP, bool BIAS>
+template <int NT, int CAP, bool BIAS>
 cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(tree_rows_kernel<NT, CAP, BIAS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -831,9 +838,11 @@ cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
 
 template <int NT>
 cudaError_t launch_score(const TreeParams& p, cudaStream_t stream) {
+  if (p.softcap > kLowCap)
+    return p.slopes ? launch<NT, 2, true>(p, stream) : launch<NT, 2, false>(p, stream);
   if (p.softcap > 0.0f)
-    return p.slopes ? launch<NT, true, true>(p, stream) : launch<NT, true, false>(p, stream);
-  return p.slopes ? launch<NT, false, true>(p, stream) : launch<NT, false, false>(p, stream);
+    return p.slopes ? launch<NT, 1, true>(p, stream) : launch<NT, 1, false>(p, stream);
+  return p.slopes ? launch<NT, 0, true>(p, stream) : launch<NT, 0, false>(p, stream);
 }
 
 }  // namespace

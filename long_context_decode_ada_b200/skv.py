@@ -584,7 +584,7 @@ class PagedCache:
           mask   int64 [B][N], bit j of row i: token i sees drafted token j;
                  None: a chain (tree_mask() makes one from parents)
           count  int32 [B] drafted tokens of each sequence, None: N
-          softcap  0 or c: scores c tanh(x / c)
+          softcap  0 or c (2^-40 to 2^40): scores c tanh(x / c)
           slopes fp32 [Hq]: scores less slopes[h] times the distance; needs
                  q_pos int32 [B][N] and seq_lens int32 [B]
         Rows i >= count[b] of out and lse are left as they were (an `out` made

@@ -125,6 +125,30 @@ def test_caps_that_some_scores_reach(N):
         compare(cache, got, q, k=k, v=v, softcap=cap)
 
 
+@pytest.mark.parametrize("N", [1, 4, 40])
+@pytest.mark.parametrize("cap", [1e4, 1e8, 2.0 ** 40])
+def test_caps_far_above_the_scores(N, cap):
+    cache, _ = make_store([700], 1, 4, 32, seed=53)
+    q, k, v, _ = drafts(1, N, 1, 4, 29)
+    lse = torch.empty((1, N, 4), device="cuda")
+    compare(cache, cache.tree_attention(q, k, v, softcap=cap, lse=lse), q, k=k, v=v, softcap=cap)
+
+
+@pytest.mark.parametrize("N", [2, 7, 40])
+def test_a_row_beyond_the_cap_leaves_the_others(N):
+    # the first token's scores pass a cap far above those of the others
+    cache, _ = make_store([700], 1, 4, 32, seed=59)
+    q, k, v, _ = drafts(1, N, 1, 4, 31)
+    far = q.clone()
+    far[:, 0] *= 2.0 ** 20
+    lse, lse_far = (torch.empty((1, N, 4), device="cuda") for _ in range(2))
+    got, _ = cache.tree_attention(q, k, v, softcap=1e5, lse=lse)
+    got_far, _ = cache.tree_attention(far, k, v, softcap=1e5, lse=lse_far)
+    assert torch.isfinite(got_far).all()
+    got_far[:, 0], lse_far[:, 0] = got[:, 0], lse[:, 0]
+    compare(cache, (got_far, lse_far), q, k=k, v=v, softcap=1e5)
+
+
 @pytest.mark.parametrize("N,softcap,bias", [(1, 30.0, False), (7, 5.0, False), (1, 0.0, True),
                                             (20, 0.0, True), (33, 50.0, True)])
 def test_capped_and_biased_scores(N, softcap, bias):

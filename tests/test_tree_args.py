@@ -53,6 +53,12 @@ def test_calls_are_refused_before_the_gpu(bad):
     assert len(skv.lib().skv_last_error()) > 10
 
 
+@pytest.mark.parametrize("cap", [2.0 ** -41, 1e-45, 2.0 ** 41, 3e38])
+def test_caps_outside_the_range_are_refused(cap):
+    assert call(skv.Context(16), B=0, cap=cap) == skv.SKV_ERR_ARG
+    assert call(skv.Context(16), B=0, cap=2.0 ** -40) == call(skv.Context(16), B=0, cap=2.0 ** 40) == skv.SKV_OK
+
+
 def test_out_over_its_inputs_is_refused():
     for K, V, out in ((0, 0, 16), (32, 64, 32), (32, 64, 64)):
         t = skv.SkvTree(N=4, kv_dtype=skv.Q_FP16)
