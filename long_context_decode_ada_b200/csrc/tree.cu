@@ -42,8 +42,8 @@
 // What bounds it is neither the products (tensor cores 17% busy) nor HBM but
 // the conversion and the softmax around them: instruction issue, 49% busy at
 // 128 rows, with five roles' loops sharing one instruction cache.  Measured
-// over the 128K store (1.05 M token-heads): 32 tokens (128 rows) 171 us with
-// short waits, 209 us with waits of 35 instructions at their 25 places
+// over the 128K store (1.05 M token-heads): 32 tokens (128 rows) 169 us; 171 us
+// before units' take-up was weighed as it is, 209 us with waits of 35 instructions at their 25 places
 // (instruction cache misses 3.6 M against 0.7 M a launch); pages loaded by the
 // decode warps themselves instead of by bulk copies 231 us; tiles of 64 tokens
 // with one warp issuing both products 274 us.  Three decode teams instead of

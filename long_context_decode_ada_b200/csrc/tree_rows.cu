@@ -21,7 +21,7 @@
 // What bounds it: instruction issue (41 to 45% busy with three warps a
 // scheduler; registers allow no more) and the latency behind it; HBM 2.7 TB/s
 // on single tokens over the 128K store (78 us), tensor cores 16% busy on the
-// ragged batch (323 us; 390 us in the tensor-memory form, which wins from 33
+// ragged batch (308 us; 364 us in the tensor-memory form, which wins from 33
 // rows on: its conversion costs the same for 1 row as for 64).  12 warps: 16
 // with 128 registers each spill (biased single tokens 260 us against 214), 8
 // hide less.  L2 prefetches ahead of the loads cost more than they hide (333
