@@ -593,6 +593,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     }
 
     if (more) keep_ids(seg ^ 1, id);
+    // the rows' fragments in shared memory are there (one column block: only the
+    // drafted tokens read them)
+    if (NT == 2 || sg.dparts > 0) __syncthreads();
     for (int w0 = 0; w0 < sg.pages || w0 == 0; w0 += kWindow) {
       const int held = min(kWindow, sg.pages - w0);
       if (w0 > 0) {
