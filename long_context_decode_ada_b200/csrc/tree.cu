@@ -1163,7 +1163,9 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
         write_row<CAP, BIAS, 8>(p, d.unit, d.n, d.slot, bad, nb == 1 ? x : 128 * s + x, Mx, Lx, v, d0,
                                 lane);
       }
-      if (step < 7 && !meet()) return;
+      // (behind the last step too: a stream without a tile in the next segment
+      // waits for nothing there before it writes its sums)
+      if (!meet()) return;
     }
   }
 }

@@ -30,3 +30,22 @@ def test_queries_of_the_unit_itself(G, N, lens):
     for splits in (1, 4):
         got = cache.tree_attention(q, k, v, lse=lse, num_splits=splits)
         compare(cache, got, q, k=k, v=v)
+
+
+@pytest.mark.parametrize("n", [9, 16, 20, 32])             # 36 to 128 rows a kv head
+@pytest.mark.parametrize("drafted", [False, True])
+def test_units_of_one_tile_behind_longer_ones(n, drafted):
+    # one tile: the second stream has nothing to do in the unit.  Units of more
+    # than 128 rows, of several tiles and of other sizes lie between
+    lens = [300, 5, 40, 64, 0, 9, 700, 1, 60, 33, 128, 20]
+    N = 64 if drafted else n
+    cache, _ = make_store(lens, 2, 4, 64, f=(0.0, 0.5, 0.5), seed=71)
+    B = len(lens)
+    q, k, v, _ = drafts(B, N, 2, 4, 37)
+    q = unlike_queries(q)
+    count = torch.tensor([N if b % 5 == 0 else n for b in range(B)], dtype=torch.int32)
+    kw = dict(k=k, v=v) if drafted else {}
+    lse = torch.empty((B, N, 8), device="cuda")
+    for splits in (1, 3):
+        got = cache.tree_attention(q, count=count.cuda(), lse=lse, num_splits=splits, **kw)
+        compare(cache, got, q, count=count, **kw)
