@@ -1088,10 +1088,11 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
       if (!warp_wait(f.odone[wg], r.turn ^ 1, f)) return;
       tc_fence_after();
     }
-    const bool bad = *(const volatile int*)&d.bad != 0;
     sum.m[wg][tl] = r.m;
     sum.l[wg][tl] = r.l;
     if (!meet()) return;
+    // (now: only the stream that had the drafted tile has waited for its decode)
+    const bool bad = *(const volatile int*)&d.bad != 0;
     float* const mine = buf + tl * kBufRow;
     const int copies = 128 / rc, sub = tl & (rc - 1);
     float a = 1.0f;

@@ -49,3 +49,21 @@ def test_units_of_one_tile_behind_longer_ones(n, drafted):
     for splits in (1, 3):
         got = cache.tree_attention(q, count=count.cuda(), lse=lse, num_splits=splits, **kw)
         compare(cache, got, q, count=count, **kw)
+
+
+@pytest.mark.parametrize("N", [9, 12, 16, 17, 25, 32])     # 36 to 128 rows a kv head
+@pytest.mark.parametrize("lens", [[0, 1], [64, 10], [128, 65], [400, 200]])
+def test_values_beyond_fp16_that_every_row_sees(N, lens):
+    # the drafted tile alone, or behind one or two or more tiles: it falls to
+    # either stream, and rows of both write what fp16 does not hold
+    cache, _ = make_store(lens, 1, 4, 16, f=(0.0, 0.6, 0.4), seed=67)
+    q, k, v, _ = drafts(2, N, 1, 4, 35, torch.bfloat16, torch.bfloat16)
+    mask = torch.full((2, N), (1 << N) - 1, dtype=torch.int64)
+    v[0, 0, 0, 3], v[0, N - 1, 0, 100], v[1, 1, 0, 77] = 2e6, -4e5, 3e8
+    lse = torch.empty((2, N, 4), device="cuda")
+    for splits in (1, 2, 0):
+        got = cache.tree_attention(q, k, v, mask=mask.cuda(), lse=lse, num_splits=splits)
+        compare(cache, got, q, k=k, v=v, mask=mask)
+    v[0, 0, 0, 3], v[0, 1, 0, 4] = float("inf"), float("nan")
+    out, _ = cache.tree_attention(q, k, v, mask=mask.cuda())
+    assert torch.all(out[0, :, :, 3] == float("inf")) and torch.isnan(out[0, :, :, 4]).all()
