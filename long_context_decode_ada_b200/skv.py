@@ -11,6 +11,7 @@ page table, tiers, row map) and wraps the allocate -> encode -> decode calls.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from typing import List, Optional, Sequence
@@ -392,6 +393,7 @@ class PagedCache:
         if getattr(self, "_cursor", None) is None:
             tip = self.page_tier_indptr
             U = self.B * self.Hkv
+            self._evict_on = set()
             self._cursor = torch.stack(
                 [(tip[t + 1:3 * U + 1:3] - tip[t:3 * U:3]).sum() for t in range(3)]
             ).to(torch.int32)
@@ -557,8 +559,17 @@ class PagedCache:
                                         f"{self.pools[0].device}")
 
     def _own_stream(self, stream=None):
-        s = stream if stream is not None else torch.cuda.current_stream(self.pools[0].device)
+        dev = self.pools[0].device
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        if s.device != dev:
+            raise SkvError(SKV_ERR_ARG, f"stream: on {s.device}, the store is on {dev}")
         return C.c_void_p(s.cuda_stream)
+
+    @staticmethod
+    def _under(stream):
+        """Buffers made inside are allocated and filled on the call's stream:
+        in order with its kernels, and not handed out again before they end."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
     def tree_workspace(self, N: int, Hq: int, positions: bool = False,
                        num_splits: int = 0) -> torch.Tensor:
@@ -588,7 +599,7 @@ class PagedCache:
           slopes fp32 [Hq]: scores less slopes[h] times the distance; needs
                  q_pos int32 [B][N] and seq_lens int32 [B]
         Rows i >= count[b] of out and lse are left as they were (an `out` made
-        here is zero there)."""
+        here is zero there).  An `out` made here belongs to the call's stream."""
         dev = self.pools[0].device
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise SkvError(SKV_ERR_ARG, "q: a tensor [B][N][Hq][128] is required")
@@ -620,19 +631,21 @@ class PagedCache:
             sc.slopes, sc.q_pos = slopes.data_ptr(), q_pos.data_ptr()
             sc.row_of, sc.seq_lens = self.row_of.data_ptr(), seq_lens.data_ptr()
             sc.Tmax = self.Tmax
-        if out is None:
-            out = torch.zeros((self.B, N, Hq, self.ctx.d), dtype=q.dtype, device=dev)
+        to = self._own_stream(stream)
+        with self._under(stream):
+            if out is None:
+                out = torch.zeros((self.B, N, Hq, self.ctx.d), dtype=q.dtype, device=dev)
+            if workspace is None:
+                workspace = self.tree_workspace(N, Hq, slopes is not None, num_splits)
         self._own(out, "out", self.B * N * Hq * self.ctx.d, q.dtype)
         self._own(lse, "lse", self.B * N * Hq, torch.float32)
-        if workspace is None:
-            workspace = self.tree_workspace(N, Hq, slopes is not None, num_splits)
         self._own(workspace, "workspace", workspace.numel(), torch.uint8)
         _check(lib().skv_tree_attention(
             self.ctx.handle, _ptr(q), _Q_TYPES[q.dtype], self.B, Hq, self.Hkv, C.byref(t),
             C.byref(sc), _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None, _ptr(self.page_ids),
             self.page_cap, C.byref(self._pools_c), _ptr(out), _ptr(lse), _ptr(self.err),
-            _ptr(workspace), workspace.numel(), num_splits, self._own_stream(stream)))
+            _ptr(workspace), workspace.numel(), num_splits, to))
         return out, lse
 
     def set_free_lists(self, free_lists, cursor=None):
@@ -652,14 +665,15 @@ class PagedCache:
             self._own(cursor, "cursor", 3, torch.int32)
             cursor = cursor.clone()
         self._cursor = cursor
+        self._evict_on = set()
 
     def spare(self) -> "PagedCache":
         """An empty store over the same pools and free lists: the `into` of
         evict()."""
         s = PagedCache.__new__(PagedCache)
         s.__dict__.update({k: x for k, x in self.__dict__.items()
-                           if k not in ("_ws_append", "_ws_retier", "_ws_evict", "released",
-                                        "n_released")})
+                           if k not in ("_ws_append", "_ws_retier", "_ws_evict", "_evict_on",
+                                        "released", "n_released")})
         for name in ("tier", "row_of", "page_indptr", "page_tier_indptr", "page_ids", "err"):
             setattr(s, name, torch.zeros_like(getattr(self, name)))
         s.tier.fill_(TIER_DROP)
@@ -685,8 +699,10 @@ class PagedCache:
         self._own(seq_lens, "seq_lens", self.B, torch.int32)
         self._own(keep, "keep", self.B, torch.int32)
         self._own(protect, "protect", n, torch.uint8)
+        to = self._own_stream(stream)
         if into is None:
-            into = self.spare()
+            with self._under(stream):
+                into = self.spare()
         if into is self or into.tier is self.tier:
             raise SkvError(SKV_ERR_ARG, "evict: into must be another store (see spare())")
         if into.pools is not self.pools or into.tier.shape != self.tier.shape:
@@ -694,13 +710,24 @@ class PagedCache:
         if getattr(self, "_free_c", None) is None:
             raise SkvError(SKV_ERR_ARG, "evict: the store has no free lists (set_free_lists)")
         into._free, into._free_c = self._free, self._free_c
-        cursor = self.free_cursor()
-        if getattr(self, "_ws_evict", None) is None:
-            size = C.c_size_t()
-            _check(lib().skv_evict_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
-                                                  C.byref(size)))
-            self._ws_evict = torch.empty(max(size.value, 1), dtype=torch.uint8,
-                                         device=self.device)
+        with self._under(stream):
+            cursor = self.free_cursor()
+            if getattr(self, "_ws_evict", None) is None:
+                size = C.c_size_t()
+                _check(lib().skv_evict_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
+                                                      C.byref(size)))
+                self._ws_evict = torch.empty(max(size.value, 1), dtype=torch.uint8,
+                                             device=self.device)
+        if getattr(self, "_evict_on", None) is None:
+            self._evict_on = set()
+        if to.value not in self._evict_on:
+            # (the caller may drop this store before the call's kernels end; once a
+            # stream is enough)
+            on = stream if stream is not None else torch.cuda.current_stream(self.pools[0].device)
+            for t in (self.tier, self.row_of, self.page_indptr, self.page_ids, cursor,
+                      self._ws_evict):
+                t.record_stream(on)
+            self._evict_on.add(to.value)
         _check(lib().skv_evict(
             self.ctx.handle, self.B, self.Hkv, self.Tmax, _ptr(seq_lens), _ptr(score),
             _ptr(protect), _ptr(keep), int(sink), int(recent), _ptr(self.tier),
@@ -708,7 +735,7 @@ class PagedCache:
             C.byref(self._free_c), _ptr(cursor), C.byref(self._pools_c), _ptr(into.tier),
             _ptr(into.row_of), _ptr(into.page_indptr), _ptr(into.page_tier_indptr),
             _ptr(into.page_ids), into.page_cap, _ptr(into._cursor), _ptr(into.err),
-            _ptr(self._ws_evict), self._ws_evict.numel(), self._own_stream(stream)))
+            _ptr(self._ws_evict), self._ws_evict.numel(), to))
         return into
 
     def check(self, stream=None):
