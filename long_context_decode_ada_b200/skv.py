@@ -577,7 +577,7 @@ class PagedCache:
         _check(lib().skv_tree_workspace_size(self.ctx.handle, self.B, N, Hq, self.Hkv,
                                              self.page_cap, 1 if positions else 0, num_splits,
                                              C.byref(n)))
-        return torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.device)
+        return torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.pools[0].device)
 
     def tree_attention(self, q: torch.Tensor, k: Optional[torch.Tensor] = None,
                        v: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
@@ -681,6 +681,12 @@ class PagedCache:
         s._cursor = torch.zeros(3, dtype=torch.int32, device=self.pools[0].device)
         return s
 
+    def _evict_workspace(self) -> torch.Tensor:
+        n = C.c_size_t()
+        _check(lib().skv_evict_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
+                                              C.byref(n)))
+        return torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.pools[0].device)
+
     def evict(self, score: torch.Tensor, seq_lens: torch.Tensor, keep: torch.Tensor,
               sink: int = 0, recent: int = 0, protect: Optional[torch.Tensor] = None,
               into: Optional["PagedCache"] = None, stream=None) -> "PagedCache":
@@ -713,11 +719,7 @@ class PagedCache:
         with self._under(stream):
             cursor = self.free_cursor()
             if getattr(self, "_ws_evict", None) is None:
-                size = C.c_size_t()
-                _check(lib().skv_evict_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
-                                                      C.byref(size)))
-                self._ws_evict = torch.empty(max(size.value, 1), dtype=torch.uint8,
-                                             device=self.device)
+                self._ws_evict = self._evict_workspace()
         if getattr(self, "_evict_on", None) is None:
             self._evict_on = set()
         if to.value not in self._evict_on:
