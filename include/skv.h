@@ -533,7 +533,8 @@ int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, i
    SMs) to 65535.  q, K, V and out must be 16-byte aligned, and out must
    not overlap the others.  The workspace needs no initialisation; calls that overlap in time must not share one.  Stream
    order: as any kernel launch (no early start).  A context with t0_bf16 is
-   refused.  Device errors: SKV_ERR_CORRUPT (bad page id, header or row: the
+   refused.  Device errors: SKV_ERR_CORRUPT (bad page id, header or row, and
+   with slopes a resident row that row_of names for no t < seq_lens[b]: the
    page or row is skipped), SKV_ERR_TIMEOUT. */
 int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, int Hkv,
                        const skv_tree* tree, const skv_score* score, const int32_t* page_indptr,

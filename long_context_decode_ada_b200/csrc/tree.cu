@@ -688,6 +688,11 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
           if (T0 + lane < d.n) q = p.q_pos[b * p.N + T0 + lane];
         } else if (lane < x.rows) {
           q = p.row_pos[(long long)d.first * P + T0 + lane];  // (a tile's pages follow each other)
+          if (q < 0) {
+            // no position names the row: its column holds no token
+            report(p.err, SKV_ERR_CORRUPT);
+            atomicAnd(&d.valid, ~(1ull << (T0 + lane)));
+          }
         }
         f.pos[stage][T0 + lane] = (float)(q - q0);
       }
@@ -1322,6 +1327,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     p.lse[tok * p.Hq + hq] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// No positions yet (rows that no position below seq_lens names stay at -1): the
+// listed pages only, a capacity may be far larger.
+__global__ void __launch_bounds__(256) tree_unplaced_kernel(const __grid_constant__ TreeParams p) {
+  const long long pages = min((long long)p.indptr[p.B * p.Hkv], p.page_cap), words = pages * p.P / 4;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < words;
+       i += (long long)gridDim.x * blockDim.x)
+    reinterpret_cast<int4*>(p.row_pos)[i] = make_int4(-1, -1, -1, -1);
+}
+
 // Positions of the store's rows: row_pos[page * P + row] = t, by the row map.
 __global__ void __launch_bounds__(256) tree_positions_kernel(const __grid_constant__ TreeParams p) {
   const long long U = (long long)p.B * p.Hkv;
@@ -1371,6 +1385,12 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
   const long long U = (long long)p.B * p.Hkv;
   if (U == 0) return cudaSuccess;
   cudaError_t e;
+  if (p.slopes && p.page_cap > 0) {
+    const long long words = p.page_cap * p.P / 4;
+    tree_unplaced_kernel<<<(unsigned)std::min<long long>((words + 255) / 256, 1184), 256, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (p.slopes && p.Tmax > 0) {
     const long long bx = std::min<long long>((p.Tmax + 255) / 256, std::max<long long>(1, 1184 / U));
     tree_positions_kernel<<<dim3((unsigned)bx, (unsigned)std::min<long long>(U, 65535)), 256, 0,

@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       const auto raw_pos = [&](int q) {
         if (BIAS && q < store) {
           const int32_t* a = p.row_pos + ((sg.first + w0 + (q >> lgp)) * P + at + g);
-          o.pos[0] = a[0];   // (of a row that is not there: unused)
+          o.pos[0] = a[0];   // (below 0: no position names the row)
           o.pos[1] = a[8];
         }
       };
@@ -663,9 +663,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         float cc[NT][4] = {}, cd[NT == 1 ? 1 : NT][4] = {};
         float(&co)[NT][4] = NT == 1 ? cd : cc;
         float rA = 1.0f, rB = 1.0f, vA = kGain, vB = kGain, posA = 0.0f, posB = 0.0f;
+        uint32_t placed = ~0u;
         if (BIAS) {
           posA = (float)(o.pos[0] - q0);
           posB = (float)(o.pos[1] - q0);
+          if (o.pos[0] < 0) placed &= 0xCCCCCCCCu;
+          if (o.pos[1] < 0) placed &= 0x33333333u;
         }
         if (nr <= 0) {
           // nothing there
@@ -712,6 +715,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           uint32_t see = ~0u;
           Weights<NT> w;
           if (nr < 16) see = (g < nr ? 0x33333333u : 0u) | (g + 8 < nr ? 0xCCCCCCCCu : 0u);
+          if (BIAS && (see & ~placed)) {
+            report(p.err, SKV_ERR_CORRUPT);
+            see &= placed;
+          }
           see &= (1u << (4 * NT)) - 1;
           if (NT == 1) {
 #pragma unroll
