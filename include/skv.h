@@ -617,7 +617,9 @@ int skv_set_profile_event(skv_ctx* ctx, void* event);
    reports SKV_ERR_TIMEOUT in err_word; later calls work normally.  0 (the
    default) means about one second.  A short limit exists to exercise that
    error path: before the CTA leaves, every page copy it started is waited
-   for with the one-second limit, whatever `cycles` is. */
+   for with the one-second limit, whatever `cycles` is.  The waits of
+   skv_tree_attention (more than 32 rows a kv head) keep to about the same
+   limit, up to two seconds (their default). */
 int skv_set_wait_limit(skv_ctx* ctx, int64_t cycles);
 
 /* Synchronise `stream`, read the device error word, reset it to 0 and return

@@ -1101,6 +1101,12 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
     p.seq_lens = score->seq_lens;
     p.Tmax = score->Tmax;
   }
+  if (ctx->wait_limit > 0) {
+    // tries, and ns each (a short one takes about a microsecond all the same), of
+    // clocks at some 2 GHz
+    const double ns = std::min(0.5 * (double)ctx->wait_limit, 2e9);
+    p.wait_limit = (uint32_t)std::max(1.0, ns < 1e6 ? ns / 1000 : std::sqrt(ns));
+  }
   p.S = decode_splits(ctx, num_splits);
   skv::tree_workspace_bytes(page_cap, ctx->P, bias, p.S, p.N, Hq / Hkv, &p, workspace);
   p.indptr = page_indptr;

@@ -288,6 +288,7 @@ struct TreeParams {
   int t1_scheme;
   float rho[4];               // decoded 2-bit shares
   float cos6[64], sin6[64], cos4[16], sin4[16], cos5[32], sin5[32];
+  uint32_t wait_limit;        // a wait between a block's warps: so many tries of so many ns (0: the default)
   int S;                      // runs (CTAs)
   int2* join;                 // workspace: per run the unit it starts and shares (-1: none), its last run
   float* part;                // workspace: partial O [2S][N * G][128]

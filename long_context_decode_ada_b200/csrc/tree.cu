@@ -226,17 +226,34 @@ __device__ __forceinline__ unsigned long long operand(uint32_t low) {
   return ((unsigned long long)kDescHigh << 32) | low;
 }
 
-// A bounded wait of a whole warp: false for all lanes after kWaits tries of at
-// most 20 us each (a wait here is on other warps of the block and takes some
-// microseconds).  Every role returns at its first wait that gave up; the error
-// is reported at the end.  Short on purpose: the code stands at some 25 places
-// of five loops that share an instruction cache.
-constexpr int kWaits = 100000;
-__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f) {
+// How long a wait may take: tries, and ns that one may sleep.  The default stands in
+// the code (the limit in a register of every role costs the prompt batch 3%, read
+// from the parameters at every wait 6%), a limit set by the caller has instances
+// of its own.
+struct DefaultLimit {
+  __device__ __forceinline__ DefaultLimit(const TreeParams&) {}
+  __device__ __forceinline__ uint32_t tries() const { return 100000u; }
+  __device__ __forceinline__ uint32_t ns() const { return 20000u; }
+};
+struct SetLimit {
+  uint32_t lim;
+  __device__ __forceinline__ SetLimit(const TreeParams& p) : lim(p.wait_limit) {}
+  __device__ __forceinline__ uint32_t tries() const { return lim; }
+  __device__ __forceinline__ uint32_t ns() const { return lim; }
+};
+
+// A bounded wait of a whole warp: false for all lanes after the limit's tries (a
+// wait here is on other warps of the block and takes some microseconds).  Every
+// role returns at its first wait that gave up, once what it has in flight
+// itself has landed; the error is reported at the end.  Short on purpose: the
+// code stands at some 25 places of five loops that share an instruction cache.
+template <class Limit>
+__device__ __forceinline__ bool warp_wait(unsigned long long& bar, uint32_t parity, Fixed& f,
+                                          Limit lim) {
   const uint32_t a = smem_u32(&bar);
 #pragma unroll 1
-  for (int n = 0; n < kWaits; ++n)
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(a, parity, 20000u))) return true;
+  for (uint32_t n = 0; n < lim.tries(); ++n)
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_sleep(a, parity, lim.ns()))) return true;
   *(volatile int*)&f.late = 1;
   return false;
 }
@@ -264,7 +281,9 @@ struct RowsCost {
 static_assert(RowsCost::kTile == kTile, "tiles");
 
 // ---------------------------------------------------------------- the planner
-__device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int lane) {
+template <class Limit>
+__device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, int lane,
+                                        Limit lim) {
   const int U = p.B * p.Hkv, ipp = kTile / p.P, lgP = __ffs(p.P) - 1;
   const int mine = lane >> 2, part = lane & 3;      // the lane's tile of a batch, its 16 rows
   const int pg = 16 * part >> lgP, at = 16 * part & (p.P - 1);
@@ -278,7 +297,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
 #pragma unroll 1
   for (int batch = 0; ends < kTeams; ++batch) {
     if (batch >= 2 &&
-        !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f))
+        !warp_wait(f.rfree[(batch - 2) & 3], ((batch - 2) >> 2) & 1, f, lim))
       break;
     int t_unit = 0, t_n = 0, t_np = 0, t_slot = -1;
     long long t_first = 0;
@@ -391,7 +410,9 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
 // ----------------------------------------------------------------- the copier
 // Brings the tiles' pages into the raw slots by bulk copies, whole pages in
 // the order of the tiles.
-__device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t base, int lane) {
+template <class Limit>
+__device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t base, int lane,
+                                       Limit lim) {
   uint32_t used = 0;                 // slots of the last 8 tiles, 4 bits each
   int head = 0, held = 0, pos = 0;   // first tile not given back, slots in use, next slot
   // the copies in flight end before the block does
@@ -400,12 +421,15 @@ __device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t b
     for (; head < t; ++head) mbar_wait_bounded(smem_u32(&f.rawfull[head & 7]), (head >> 3) & 1, &none);
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f)) {
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, lim)) {
       drain(t);
       return;
     }
     const Tile& d = f.ring[t & (kRing - 1)];
-    if (d.flags & kEnd) return;
+    if (d.flags & kEnd) {
+      drain(t);   // (a decode warp that gave up has not waited for them)
+      return;
+    }
     const uint32_t bytes = d.bytes;
     int need = (int)((bytes + kRawSlot - 1) / kRawSlot), skip = 0;
     if (pos + need > kRawSlots) {
@@ -413,7 +437,7 @@ __device__ __forceinline__ void copier(const TreeParams& p, Fixed& f, uint32_t b
       pos = 0;
     }
     while (held + need + skip > kRawSlots || t - head >= kRawTiles) {
-      if (!warp_wait(f.rawfree[head & 7], (head >> 3) & 1, f)) {
+      if (!warp_wait(f.rawfree[head & 7], (head >> 3) & 1, f, lim)) {
         drain(t);
         return;
       }
@@ -658,13 +682,13 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
   if (out) *(volatile int*)bad = 1;
 }
 
-template <bool BIAS>
+template <bool BIAS, class Limit>
 __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint32_t base, int wd,
-                                            int lane) {
+                                            int lane, Limit lim) {
   const int w = wd & (kTeamWarps - 1), P = p.P, T0 = 16 * w;
   int t = wd / kTeamWarps;
   uint32_t stage = t, use = 0;   // of tile t: its stage, the stage's tiles before
-  if (!warp_wait(f.dfull[0], 0, f)) return;
+  if (!warp_wait(f.dfull[0], 0, f, lim)) return;
   for (;;) {
     Tile& d = f.ring[t & (kRing - 1)];
     const uint32_t flags = d.flags;
@@ -672,14 +696,14 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
     const Part x = d.part[w];
     const uint32_t kb = keys_at(base, stage), vb = values_at(base, stage);
     const int y = t & (kRawTiles - 1);
-    if (!warp_wait(f.rawfull[y], (t / kRawTiles) & 1, f)) return;
+    if (!warp_wait(f.rawfull[y], (t / kRawTiles) & 1, f, lim)) return;
     const uint32_t page = f.raw[y] + x.off + kHdrBytes;
-    if (use > 0 && !warp_wait(f.kempty[stage], (use - 1) & 1, f)) return;
+    if (use > 0 && !warp_wait(f.kempty[stage], (use - 1) & 1, f, lim)) return;
     const bool draft = (flags & kDraft) != 0;
     if (!draft) store_keys(page, x.tier, x.at, P, kb, T0, lane, base);
     if (BIAS || draft) {
       // (positions and scales are in use until the stage's values are free)
-      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f)) return;
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, lim)) return;
       if (BIAS && lane < 16) {
         const long long b = d.unit / p.Hkv;
         const int q0 = p.q_pos[b * p.N];
@@ -704,14 +728,14 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     warp_arrive(f.kfull[stage]);
     if (!draft) {
-      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f)) return;
+      if (use > 0 && !warp_wait(f.vempty[stage], (use - 1) & 1, f, lim)) return;
       store_values(page, x.tier, x.at, x.rows, P, vb, T0, lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     warp_arrive(f.vfull[stage]);
     if (lane == 0) mbar_arrive(smem_u32(&f.rawfree[y]));
     const int t2 = t + kTeams;
-    if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f)) return;
+    if ((t2 ^ t) & kBatch && !warp_wait(f.dfull[(t2 / kBatch) & 3], (t2 / kRing) & 1, f, lim)) return;
     t = t2;
     stage += kTeams;
     if (stage >= kStages) {
@@ -724,28 +748,30 @@ __device__ __forceinline__ void decode_role(const TreeParams& p, Fixed& f, uint3
 // ------------------------------------------------------------------- the MMAs
 // S = Q K^T of every job, as soon as the keys are there and the stream's
 // scores are read (two blocks: its weights used).
-__device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
+template <class Limit>
+__device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm,
+                                           Limit lim) {
   const int most = 128 * p.Hkv;       // n * Hq above it: two blocks
   uint32_t turn = 3;                  // bit s: parity of stream s's job before
   uint32_t segs = 0, stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, lim))
       return;
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
     if (flags & kFirst) {
-      if (!warp_wait(f.qfull, segs & 1, f)) return;
+      if (!warp_wait(f.qfull, segs & 1, f, lim)) return;
       ++segs;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
       s = 0;
     }
-    if (!warp_wait(f.kfull[stage], use & 1, f)) return;
+    if (!warp_wait(f.kfull[stage], use & 1, f, lim)) return;
     const uint32_t low = kDescKeys | (keys_at(base, stage) >> 4);
 #pragma unroll 1
     for (int y = two ? 1 : 0; y >= 0; --y) {
-      if (!warp_wait(f.sfree[s], (turn >> s) & 1, f)) return;
-      if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f)) return;
+      if (!warp_wait(f.sfree[s], (turn >> s) & 1, f, lim)) return;
+      if (two && !warp_wait(f.odone[s], (turn >> s) & 1, f, lim)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
@@ -768,14 +794,16 @@ __device__ __forceinline__ void mma_scores(const TreeParams& p, Fixed& f, uint32
 }
 
 // O += P V of every job, as soon as its weights are there.
-__device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm) {
+template <class Limit>
+__device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t base, uint32_t tm,
+                                         Limit lim) {
   const int most = 128 * p.Hkv;
   uint32_t turn = 0;                  // bit s: parity of stream s's job
   uint32_t add = 0;                   // bit s: stream s has had a job in the segment
   uint32_t stage = 0, use = 0, s = 0;
   bool two = false;
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, lim))
       return;
     const uint32_t flags = f.ring[t & (kRing - 1)].flags;
     if (flags & kEnd) return;
@@ -783,11 +811,11 @@ __device__ __forceinline__ void mma_sums(const TreeParams& p, Fixed& f, uint32_t
       add = s = 0;
       two = f.ring[t & (kRing - 1)].n * p.Hq > most;
     }
-    if (!warp_wait(f.vfull[stage], use & 1, f)) return;
+    if (!warp_wait(f.vfull[stage], use & 1, f, lim)) return;
     const uint32_t low = kDescValues | (values_at(base, stage) >> 4);
 #pragma unroll 1
     for (int y = two ? 1 : 0; y >= 0; --y) {
-      if (!warp_wait(f.pfull[s], (turn >> s) & 1, f)) return;
+      if (!warp_wait(f.pfull[s], (turn >> s) & 1, f, lim)) return;
       turn ^= 1u << s;
       tc_fence_after();
       if (elect_one()) {
@@ -823,8 +851,9 @@ struct Row {           // a lane's row in its stream
 
 // The maximum of the lanes that need it rises to `top`: their sums, O and the
 // weights of the job's columns before `done` (at pa) follow.
-__device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, float top, uint32_t pa,
-                                      int done, uint32_t oa, int wg) {
+template <class Limit>
+__device__ __forceinline__ bool raise(Fixed& f, Row& r, float top, uint32_t pa, int done,
+                                      uint32_t oa, int wg, Limit lim) {
   const float m = top > r.m + kRaise ? top : r.m;
   const float a = m == r.m ? 1.0f : ex2f(r.m - m);
   r.l *= a;
@@ -841,7 +870,7 @@ __device__ __forceinline__ bool raise(const TreeParams& p, Fixed& f, Row& r, flo
     tc_st8(pa + k / 2, w);
   }
   if (r.mine > 0) {
-    if (!warp_wait(f.odone[wg], r.turn ^ 1, f)) return false;
+    if (!warp_wait(f.odone[wg], r.turn ^ 1, f, lim)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int k = 0; k < kHeadDim; k += 16) {
@@ -898,11 +927,10 @@ __device__ __forceinline__ void cap_scores(const Row& r, float (&s)[32]) {
 
 // n columns (32 or 64) of a job, 32 at a time: scores (at sa) to weights (at
 // pa); bits: the columns this row sees.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& r, uint32_t sa,
-                                            uint32_t pa, uint32_t oa, int wg, int n,
-                                            unsigned long long bits, const float* cs,
-                                            const float* pos) {
+template <bool CAP, bool BIAS, class Limit>
+__device__ __forceinline__ bool softmax_job(Fixed& f, Row& r, uint32_t sa, uint32_t pa,
+                                            uint32_t oa, int wg, int n, unsigned long long bits,
+                                            const float* cs, const float* pos, Limit lim) {
   float s[32];
   tc_ld16(sa, s);
   tc_ld16(sa + 16, s + 16);
@@ -934,7 +962,7 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
     for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
     float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     if (!(CAP || BIAS)) top *= r.c;
-    if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise) && !raise(p, f, r, top, pa, c, oa, wg)) return false;
+    if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise) && !raise(f, r, top, pa, c, oa, wg, lim)) return false;
     const float m = r.m == -INFINITY ? 0.0f : r.m;
     const float2 c2 = make_float2(r.c, r.c), m2 = make_float2(-m, -m);
     float2 l2 = make_float2(r.l, 0.0f);
@@ -954,7 +982,12 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
       tc_ld16(sa + c + 48, s + 16);
     }
     // (the product before may still read its weights)
-    if (c == 0 && r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f)) return false;
+    if (c == 0 && r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f, lim)) {
+      tc_wait_ld();   // the next columns arrive in their registers first
+#pragma unroll
+      for (int k = 0; k < 32; ++k) asm volatile("" : "+f"(s[k]));
+      return false;
+    }
     tc_st8(pa + c / 2, w);
     tc_st8(pa + c / 2 + 8, w + 8);
   }
@@ -962,9 +995,9 @@ __device__ __forceinline__ bool softmax_job(const TreeParams& p, Fixed& f, Row& 
   return true;
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, class Limit>
 __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, float* buf, Sums& sum,
-                                             uint32_t tm0, int warp, int lane) {
+                                             uint32_t tm0, int warp, int lane, Limit lim) {
   const int G = p.Hq / p.Hkv;
   const int wg = warp >> 2, part = warp & 3, tl = 32 * part + lane;
   const uint32_t tm = tm0 + ((uint32_t)(32 * part) << 16);
@@ -979,10 +1012,10 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
   unsigned long long see = 0;
   const auto meet = [&]() {
     warp_arrive(f.sync);
-    return warp_wait(f.sync, syncs++ & 1, f);
+    return warp_wait(f.sync, syncs++ & 1, f, lim);
   };
   for (int t = 0;; ++t) {
-    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f))
+    if ((t & (kBatch - 1)) == 0 && !warp_wait(f.dfull[(t / kBatch) & 3], (t / kRing) & 1, f, lim))
       return;
     const Tile& d = f.ring[t & (kRing - 1)];
     const uint32_t flags = d.flags;
@@ -1061,7 +1094,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     if (++stage == kStages) stage = 0;
     // one block: the streams take the tiles in turn; two: every tile
     if (nb == 2 || next == 0) {
-      if (!warp_wait(f.sfull[wg], r.turn, f)) return;
+      if (!warp_wait(f.sfull[wg], r.turn, f, lim)) return;
       tc_fence_after();
       if (busy) {
         const int n = kTile * rc / 128, c0 = copy * n;
@@ -1073,13 +1106,14 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
         }
         const uint32_t sa = tm + kColS + 64 * wg + c0;
         const uint32_t pa = nb == 2 ? sa : tm + kColP + 32 * wg + c0 / 2;
-        if (!softmax_job<CAP, BIAS>(p, f, r, sa, pa, oa, wg, n, bits >> c0, cs, f.pos[stage] + c0))
+        if (!softmax_job<CAP, BIAS>(f, r, sa, pa, oa, wg, n, bits >> c0, cs, f.pos[stage] + c0,
+                                    lim))
           return;
       } else {
         warp_arrive(f.sfree[wg]);
         // (not ahead of the warps that have rows: the job's weights are complete
         // when all four have arrived)
-        if (r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f)) return;
+        if (r.mine > 0 && !warp_wait(f.odone[wg], r.turn ^ 1, f, lim)) return;
       }
       tc_fence_before();
       warp_arrive(f.pfull[wg]);
@@ -1090,7 +1124,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     if (!(flags & kLast)) continue;
     // the segment's end: the streams' and copies' sums meet, 32 dims at a time
     if (r.mine > 0) {
-      if (!warp_wait(f.odone[wg], r.turn ^ 1, f)) return;
+      if (!warp_wait(f.odone[wg], r.turn ^ 1, f, lim)) return;
       tc_fence_after();
     }
     sum.m[wg][tl] = r.m;
@@ -1176,7 +1210,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
   }
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, class Limit>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   Fixed& f = *reinterpret_cast<Fixed*>(raw);
@@ -1228,25 +1262,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
   find_run<kThreads>(p, blockIdx.x, f.scan, &f.run, RowsCost());  // (block-wide barriers)
   tc_fence_after();
   const uint32_t tm = *(volatile uint32_t*)&f.tmem;
+  const Limit lim(p);
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     softmax_role<CAP, BIAS>(p, f, reinterpret_cast<float*>(mem + kAtBuf),
-                            *reinterpret_cast<Sums*>(mem + kAtSums), tm, warp, lane);
+                            *reinterpret_cast<Sums*>(mem + kAtSums), tm, warp, lane, lim);
+    tc_wait_st();   // (a role that gave up leaves stores in flight)
   } else if (warp < kPlanner) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
-    decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane);
+    decode_role<BIAS>(p, f, base, warp - kSoftWarps, lane, lim);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsHelp));
     if (warp == kPlanner) {
-      planner(p, f, blockIdx.x, lane);
+      planner(p, f, blockIdx.x, lane, lim);
     } else if (warp == kCopier) {
-      copier(p, f, base, lane);
+      copier(p, f, base, lane, lim);
     } else {
       if (warp == kMmaS)
-        mma_scores(p, f, base, tm);
+        mma_scores(p, f, base, tm, lim);
       else
-        mma_sums(p, f, base, tm);
+        mma_sums(p, f, base, tm, lim);
       // nothing in flight when tensor memory is given back
       unsigned long long& fin = f.fin[warp - kMmaS];
       if (elect_one()) tc_commit(smem_u32(&fin));
@@ -1356,10 +1392,12 @@ __global__ void __launch_bounds__(256) tree_positions_kernel(const __grid_consta
 
 template <bool CAP, bool BIAS>
 cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
+  const auto kernel = p.wait_limit ? tree_kernel<CAP, BIAS, SetLimit>
+                                   : tree_kernel<CAP, BIAS, DefaultLimit>;
   const cudaError_t e = cudaFuncSetAttribute(
-      tree_kernel<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  tree_kernel<CAP, BIAS><<<(unsigned)p.S, kThreads, kSmemBytes, stream>>>(p);
+  kernel<<<(unsigned)p.S, kThreads, kSmemBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
