@@ -142,8 +142,9 @@ template <int NT>
 struct Frag {
   uint32_t q[16];         // B fragments of the rows (one column block; two: from qs)
   uint32_t qs;            // the same in shared memory
-  float acc[NT][8][4];    // O^T: dims 16 mt + g (+ 8), rows 2 t, 2 t + 1
+  float acc[NT][8][4];    // O^T times gain: dims 16 mt + g (+ 8), rows 2 t, 2 t + 1
   float m[NT][2], l[NT][2];
+  float gain;             // of the weights, a power of two
 };
 
 // S^T += keys (A: two registers a row) x rows for k-step s
@@ -181,15 +182,17 @@ struct Score {
   float slope[NT][2], rel[NT][2];
 };
 
-// Weights (2^4 at most above 1, see kRise) times a value scale (515 at most, as
-// fp16 values have it) times kGain stay within fp16, and small ones stay
-// normal numbers further down.
-constexpr float kRise = 4.0f, kGain = 4.0f;
+// Weights (2^4 at most above 1, see kRise) times a value scale times the warp's
+// gain stay within fp16: scale times gain is at most kTop.  The gain starts high
+// and is lowered (with the sums: powers of two, exact) when a value scale
+// asks for it, so that small weights of small values stay normal numbers: with a
+// gain of 4 for all, weights of 2^-12 were lost where values are below 0.01.
+constexpr float kRise = 4.0f, kTop = 4094.0f, kFirstGain = 68719476736.0f;   // 2^36: any scale's
 
 // Weights as B fragments: each is the sum of two fp16 numbers, so that nothing
-// is lost to their rounding (the products for it cost less than scaling the
-// values, which would round them: one fp16 store 0.0002 off, as its output's
-// rounding alone, against 0.00034).
+// of a weight above some 2^-36 is lost to their rounding (the products for it
+// cost less than scaling the values, which would round them: one fp16 store
+// 0.0002 off, as its output's rounding alone, against 0.00034).
 template <int NT>
 struct Weights {
   uint32_t hi[NT][2], lo[NT][2];
@@ -229,7 +232,7 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
       if (!((see >> k) & 1)) c[k >> 2][k & 3] = -INFINITY;
   }
   // z = score - maximum; above kRise (or without a maximum: not a number or
-  // infinite) the maximum rises first
+  // infinite) the maximum rises first.  Value scales above kTop lower the gain
   float z[NT][4], top = -INFINITY;
   const auto less = [&](int n, int e, float m) {
     return CAP || BIAS ? c[n][e] - m : fmaf(c[n][e], sc.c[n][e & 1], -m);
@@ -241,7 +244,17 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
       z[n][e] = less(n, e, f.m[n][e & 1]);
       top = fmaxf(top, z[n][e]);
     }
-  if (__any_sync(0xFFFFFFFFu, top > kRise)) {
+  const float big = fmaxf(fabsf(vA), fabsf(vB));
+  if (__any_sync(0xFFFFFFFFu, top > kRise || big > kTop)) {
+    float v = big;
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+    // (v d in [2^11, 2^12))
+    const float d = v > kTop ? __uint_as_float((265u - (__float_as_uint(v) >> 23)) << 23) : 1.0f;
+    f.gain *= d;
+    vA *= d;
+    vB *= d;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float a[2];
@@ -255,6 +268,7 @@ __device__ __forceinline__ void weights(Frag<NT>& f, const Score<NT>& sc, float 
         a[j] = x == f.m[n][j] ? 1.0f : ex2f(f.m[n][j] - x);
         f.m[n][j] = x;
         f.l[n][j] *= a[j];
+        a[j] *= d;
       }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
@@ -371,7 +385,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
       if (p.mask ? (p.mask[tok0 + i] >> j) & 1 : j <= i) see |= 1u << e;
     }
   }
-  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], kGain, kGain, pos[0], pos[1], see, w);
+  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], f.gain, f.gain, pos[0], pos[1], see, w);
   // values: 64 dims at a time as fp16 rows of 128 bytes (16-byte chunks permuted
   // by the token's low bits), read back transposed.  A value that fp16 does
   // not hold enters as 0 and is added by write_row.
@@ -591,6 +605,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       for (int mt = 0; mt < 8; ++mt)
         fr.acc[k][mt][0] = fr.acc[k][mt][1] = fr.acc[k][mt][2] = fr.acc[k][mt][3] = 0.0f;
     }
+    fr.gain = kFirstGain;
 
     if (more) keep_ids(seg ^ 1, id);
     // the rows' fragments in shared memory are there (one column block: only the
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
         // (one column block: two chains of products, which halves their latency)
         float cc[NT][4] = {}, cd[NT == 1 ? 1 : NT][4] = {};
         float(&co)[NT][4] = NT == 1 ? cd : cc;
-        float rA = 1.0f, rB = 1.0f, vA = kGain, vB = kGain, posA = 0.0f, posB = 0.0f;
+        float rA = 1.0f, rB = 1.0f, vA = fr.gain, vB = fr.gain, posA = 0.0f, posB = 0.0f;
         uint32_t placed = ~0u;
         if (BIAS) {
           posA = (float)(o.pos[0] - q0);
@@ -705,8 +720,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           rA = __half2float(__ushort_as_half((uint16_t)o.r[0]));
           rB = __half2float(__ushort_as_half((uint16_t)o.r[1]));
           // (rows that are not there may hold anything)
-          vA = g < nr ? kGain * __half2float(__ushort_as_half((uint16_t)o.s[0])) : 0.0f;
-          vB = g + 8 < nr ? kGain * __half2float(__ushort_as_half((uint16_t)o.s[1])) : 0.0f;
+          vA = g < nr ? fr.gain * __half2float(__ushort_as_half((uint16_t)o.s[0])) : 0.0f;
+          vB = g + 8 < nr ? fr.gain * __half2float(__ushort_as_half((uint16_t)o.s[1])) : 0.0f;
         }
         look(q + streams);
         raw_pos(q + streams);
@@ -766,6 +781,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       }
     }
     const int slot0 = warp < S::kHalf ? warp : warp - S::kHalf;
+    const float off = 1.0f / fr.gain;   // (exact)
     for (int half = 1; half >= 0; --half) {
       if (warp / S::kHalf == half) {
 #pragma unroll
@@ -782,8 +798,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
               fr.l[k][j] = fr.l[k][j] * a0 + l1 * a1;
 #pragma unroll
               for (int mt = 0; mt < 8; ++mt) {
-                fr.acc[k][mt][j] = fr.acc[k][mt][j] * a0 + to[16 * mt] * a1;
-                fr.acc[k][mt][j + 2] = fr.acc[k][mt][j + 2] * a0 + to[16 * mt + 8] * a1;
+                fr.acc[k][mt][j] = fr.acc[k][mt][j] * (a0 * off) + to[16 * mt] * a1;
+                fr.acc[k][mt][j + 2] = fr.acc[k][mt][j + 2] * (a0 * off) + to[16 * mt + 8] * a1;
               }
               __syncwarp();   // (every lane has read the row's m and l)
             }
@@ -791,10 +807,11 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
               f.m[slot0][r] = fr.m[k][j];
               f.l[slot0][r] = fr.l[k][j];
             }
+            const float o = half == 0 ? 1.0f : off;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
-              to[16 * mt] = fr.acc[k][mt][j];
-              to[16 * mt + 8] = fr.acc[k][mt][j + 2];
+              to[16 * mt] = fr.acc[k][mt][j] * o;
+              to[16 * mt + 8] = fr.acc[k][mt][j + 2] * o;
             }
           }
         }
@@ -821,7 +838,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, k);
       float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int k = 0; k < S::kHalf / blocks; ++k) {
-        const float ak = __shfl_sync(0xFFFFFFFFu, a, k) * (1.0f / kGain);
+        const float ak = __shfl_sync(0xFFFFFFFFu, a, k);
         const float4 x = *reinterpret_cast<const float4*>(&f.o[blocks * k + blk][lr][4 * lane]);
         v[0] += ak * x.x;
         v[1] += ak * x.y;
