@@ -496,9 +496,10 @@ int skv_decode_attention_static(skv_ctx* ctx, const void* q, int q_dtype, int B,
    and softmax statistics are fp32; queries, keys (the store's as decoded),
    values and softmax weights enter the tensor cores as fp16.  Queries and
    drafted keys are scaled to its range by a power of two a row (bf16 enters
-   exactly, but for elements below 2^-38 of their row's largest); drafted
-   values that fp16 does not hold are added in fp32, those below 2^-25 count
-   as zero. */
+   exactly, but for elements below 2^-38 of their row's largest), drafted bf16
+   values by one that their largest of the sequence and kv head asks for (what
+   fp16 loses of them lies below 2^-19 of that); those above fp16's range are
+   added in fp32. */
 typedef struct skv_tree {
   int32_t N;              /* drafted tokens a sequence, 1..64 */
   int32_t kv_dtype;       /* SKV_Q_FP16 / SKV_Q_BF16: type of K and V */

@@ -1029,8 +1029,8 @@ int skv_tree_workspace_size(const skv_ctx* ctx, int B, int N, int Hq, int Hkv, i
   if (!ctx || !bytes) return fail(SKV_ERR_ARG, "skv_tree_workspace_size: null argument");
   if (!tree_sizes_ok(B, N, Hq, Hkv, page_cap) || num_splits < 0 || num_splits > 65535)
     return fail(SKV_ERR_ARG, "skv_tree_workspace_size: bad sizes");
-  *bytes = skv::tree_workspace_bytes(page_cap, ctx->P, positions, decode_splits(ctx, num_splits), N,
-                                     Hq / Hkv, nullptr, nullptr);
+  *bytes = skv::tree_workspace_bytes(page_cap, ctx->P, positions, decode_splits(ctx, num_splits),
+                                     B * Hkv, N, Hq / Hkv, nullptr, nullptr);
   return ok();
 }
 
@@ -1108,7 +1108,7 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
     p.wait_limit = (uint32_t)std::max(1.0, ns < 1e6 ? ns / 1000 : std::sqrt(ns));
   }
   p.S = decode_splits(ctx, num_splits);
-  skv::tree_workspace_bytes(page_cap, ctx->P, bias, p.S, p.N, Hq / Hkv, &p, workspace);
+  skv::tree_workspace_bytes(page_cap, ctx->P, bias, p.S, B * Hkv, p.N, Hq / Hkv, &p, workspace);
   p.indptr = page_indptr;
   p.tier_indptr = page_tier_indptr;
   p.ids = page_ids;

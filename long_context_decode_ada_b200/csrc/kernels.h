@@ -291,12 +291,13 @@ struct TreeParams {
   uint32_t wait_limit;        // a wait between a block's warps: so many tries of so many ns (0: the default)
   int S;                      // runs (CTAs)
   int2* join;                 // workspace: per run the unit it starts and shares (-1: none), its last run
+  int32_t* shift;             // workspace: per unit what its drafted values are scaled by, or NULL
   float* part;                // workspace: partial O [2S][N * G][128]
   float2* part_ml;            // workspace: their (m, l), log2 domain
 };
 // Bytes of workspace; with p, its pointers into ws are set.
-size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int N, int G,
-                            TreeParams* p, void* ws);
+size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int units, int N,
+                            int G, TreeParams* p, void* ws);
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream);
 // The form for few rows (tree_rows.cu): N * Hq / Hkv up to kTreeRows.
 constexpr int kTreeRows = 32;

@@ -113,6 +113,7 @@ struct __align__(16) Tile {
   int slot;                     // partial slot, -1: the unit lies in this run
   int bad;                      // a drafted value lies outside fp16
   uint32_t bytes;               // raw bytes
+  int shift;                    // drafted values enter times 2^shift
 };
 
 struct __align__(16) Fixed {
@@ -293,6 +294,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
   unsigned long long cc = run.before;
   int2 join = make_int2(-1, 0);
   Unit x = {};
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the shifts)
   // (an end for each team)
 #pragma unroll 1
   for (int batch = 0; ends < kTeams; ++batch) {
@@ -401,6 +403,7 @@ __device__ __forceinline__ void planner(const TreeParams& p, Fixed& f, int c, in
       d.slot = t_slot;
       d.bad = 0;
       d.bytes = sum;
+      d.shift = (t_flags & kDraft) && p.shift ? p.shift[t_unit] : 0;
     }
     warp_arrive(f.dfull[batch & 3]);
   }
@@ -657,8 +660,9 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
     sts128(row + (i >> 1) * kHalfDims + (((4 * (i & 1) + g) ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
   if (g == 0) cs[j] = pow2i(-e);
+  const float vup = pow2i(d.shift);
   bool out = false;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int hf = c >> 1, gg = g + 4 * (c & 1);
     uint32_t w[4];
@@ -675,7 +679,7 @@ __device__ __forceinline__ void store_draft(const TreeParams& p, const Tile& d, 
           out = true;
         }
       }
-      w[m] = pack_f16x2(y[0], y[1]);
+      w[m] = pack_f16x2(y[0] * vup, y[1] * vup);
     }
     sts128(vb + (uint32_t)j * 128 + hf * kHalfDims + ((gg ^ t) << 4), make_uint4(w[0], w[1], w[2], w[3]));
   }
@@ -853,7 +857,7 @@ struct Row {           // a lane's row in its stream
 // weights of the job's columns before `done` (at pa) follow.
 template <class Limit>
 __device__ __forceinline__ bool raise(Fixed& f, Row& r, float top, uint32_t pa, int done,
-                                      uint32_t oa, int wg, Limit lim) {
+                                      uint32_t oa, int wg, float up, Limit lim) {
   const float m = top > r.m + kRaise ? top : r.m;
   const float a = m == r.m ? 1.0f : ex2f(r.m - m);
   r.l *= a;
@@ -872,13 +876,14 @@ __device__ __forceinline__ bool raise(Fixed& f, Row& r, float top, uint32_t pa, 
   if (r.mine > 0) {
     if (!warp_wait(f.odone[wg], r.turn ^ 1, f, lim)) return false;
     tc_fence_after();
+    const float au = a * up;
 #pragma unroll 1
     for (int k = 0; k < kHeadDim; k += 16) {
       float o[16];
       tc_ld16(oa + k, o);
       tc_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] *= a;
+      for (int e = 0; e < 16; ++e) o[e] *= au;
       tc_st8(oa + k, reinterpret_cast<const uint32_t*>(o));
       tc_st8(oa + k + 8, reinterpret_cast<const uint32_t*>(o) + 8);
     }
@@ -930,7 +935,8 @@ __device__ __forceinline__ void cap_scores(const Row& r, float (&s)[32]) {
 template <bool CAP, bool BIAS, class Limit>
 __device__ __forceinline__ bool softmax_job(Fixed& f, Row& r, uint32_t sa, uint32_t pa,
                                             uint32_t oa, int wg, int n, unsigned long long bits,
-                                            const float* cs, const float* pos, Limit lim) {
+                                            const float* cs, const float* pos, int shift,
+                                            Limit lim) {
   float s[32];
   tc_ld16(sa, s);
   tc_ld16(sa + 16, s + 16);
@@ -962,7 +968,9 @@ __device__ __forceinline__ bool softmax_job(Fixed& f, Row& r, uint32_t sa, uint3
     for (int k = 4; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
     float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     if (!(CAP || BIAS)) top *= r.c;
-    if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise) && !raise(f, r, top, pa, c, oa, wg, lim)) return false;
+    if (__any_sync(0xFFFFFFFFu, top > r.m + kRaise || (c == 0 && shift != 0))) {
+      if (!raise(f, r, top, pa, c, oa, wg, c == 0 ? pow2i(shift) : 1.0f, lim)) return false;
+    }
     const float m = r.m == -INFINITY ? 0.0f : r.m;
     const float2 c2 = make_float2(r.c, r.c), m2 = make_float2(-m, -m);
     float2 l2 = make_float2(r.l, 0.0f);
@@ -1107,7 +1115,7 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
         const uint32_t sa = tm + kColS + 64 * wg + c0;
         const uint32_t pa = nb == 2 ? sa : tm + kColP + 32 * wg + c0 / 2;
         if (!softmax_job<CAP, BIAS>(f, r, sa, pa, oa, wg, n, bits >> c0, cs, f.pos[stage] + c0,
-                                    lim))
+                                    flags & kDraft ? d.shift : 0, lim))
           return;
       } else {
         warp_arrive(f.sfree[wg]);
@@ -1134,12 +1142,13 @@ __device__ __forceinline__ void softmax_role(const TreeParams& p, Fixed& f, floa
     const bool bad = *(const volatile int*)&d.bad != 0;
     float* const mine = buf + tl * kBufRow;
     const int copies = 128 / rc, sub = tl & (rc - 1);
-    float a = 1.0f;
+    // (the drafted tile is the segment's last: this stream's?)
+    float a = (flags & kDraft) && (nb == 2 || next == 1) ? pow2i(-d.shift) : 1.0f;
     if (nb == 1) {
       float M = -INFINITY;
       for (int k = 0; k < copies; ++k)
         M = fmaxf(M, fmaxf(sum.m[0][sub + rc * k], sum.m[1][sub + rc * k]));
-      a = r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
+      a *= r.m == -INFINITY ? 0.0f : ex2f(r.m - M);
     }
 #pragma unroll 1
     for (int step = 0; step < 8; ++step) {
@@ -1390,6 +1399,30 @@ __global__ void __launch_bounds__(256) tree_positions_kernel(const __grid_consta
   }
 }
 
+// Drafted bf16 values that are all small enter times a power of two (their
+// largest between 1 and 2; the sums before them follow, see raise): fp16 holds
+// all bits of those above 2^-14 only.  At 2^-6 and above what is lost lies 2^-19
+// below the largest.  A warp per unit; the kernel that reads the shifts starts
+// beside this one.  (Inside it, in any role, the few instructions cost 2 to 28%
+// of the prompt batch by where they put the others' loops.)
+__global__ void __launch_bounds__(256) tree_shift_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int u = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (u >= p.B * p.Hkv) return;
+  const int b = u / p.Hkv, h = u - b * p.Hkv;
+  const int n = p.count ? min(max(p.count[b], 0), p.N) : p.N;
+  const uint16_t* V = static_cast<const uint16_t*>(p.V) + (long long)b * p.N * p.kv_stride +
+                      (long long)h * kHeadDim + 8 * (lane & 15);
+  uint32_t mx = 0;
+#pragma unroll 8
+  for (int j = lane >> 4; j < n; j += 2) {
+    const uint4 x = *reinterpret_cast<const uint4*>(V + j * p.kv_stride);
+    mx = held_bits(held_bits(held_bits(held_bits(mx, x.x), x.y), x.z), x.w);
+  }
+  const int e = scale_exp(__reduce_max_sync(0xFFFFFFFFu, mx), 1) - 14;
+  if (lane == 0) p.shift[u] = e > 6 ? min(e, 60) : 0;
+}
+
 template <bool CAP, bool BIAS>
 cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
   const auto kernel = p.wait_limit ? tree_kernel<CAP, BIAS, SetLimit>
@@ -1397,26 +1430,43 @@ cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)p.S, kThreads, kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  if (p.shift) {
+    tree_shift_kernel<<<(unsigned)(((long long)p.B * p.Hkv + 7) / 8), 256, 0, stream>>>(p);
+    const cudaError_t s = cudaGetLastError();
+    if (s != cudaSuccess) return s;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.S);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.shift ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
-// Workspace: the positions, then the joins, then the parts of two slots a run.
-size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int N, int G,
-                            TreeParams* p, void* ws) {
+// Workspace: the positions, then the joins, the units' shifts, then the parts of
+// two slots a run.
+size_t tree_workspace_bytes(long long page_cap, int P, int positions, int S, int units, int N,
+                            int G, TreeParams* p, void* ws) {
   const size_t pos = positions ? ((size_t)page_cap * P * 4 + 127) / 128 * 128 : 0;
   const size_t join = ((size_t)S * 8 + 127) / 128 * 128;
+  const size_t shift = N * G > kTreeRows ? ((size_t)units * 4 + 127) / 128 * 128 : 0;
   const size_t rows = 2ull * S * N * G;
   if (p) {
     uint8_t* w = static_cast<uint8_t*>(ws);
     p->row_pos = reinterpret_cast<int32_t*>(w);
     p->join = reinterpret_cast<int2*>(w + pos);
-    p->part = reinterpret_cast<float*>(w + pos + join);
-    p->part_ml = reinterpret_cast<float2*>(w + pos + join + rows * kHeadDim * 4);
+    p->shift = shift && p->V && p->kv_bf16 ? reinterpret_cast<int32_t*>(w + pos + join) : nullptr;
+    p->part = reinterpret_cast<float*>(w + pos + join + shift);
+    p->part_ml = reinterpret_cast<float2*>(w + pos + join + shift + rows * kHeadDim * 4);
   }
-  return pos + join + rows * (kHeadDim * 4 + 8);
+  return pos + join + shift + rows * (kHeadDim * 4 + 8);
 }
 
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {

@@ -101,6 +101,11 @@ __device__ __forceinline__ float2 from16x2(uint32_t x, int bf16) {
 __device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t x) {
   return max(m, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
 }
+// the same over bf16 halves that fp16's range holds (up to 65280)
+__device__ __forceinline__ uint32_t held_bits(uint32_t m, uint32_t x) {
+  const uint32_t a = x & 0x7FFFu, b = (x >> 16) & 0x7FFFu;
+  return max(m, max(a <= 0x477Fu ? a : 0u, b <= 0x477Fu ? b : 0u));
+}
 // e with 2^e |x| in [2^14, 2^15) for the largest |x| (bit pattern m)
 __device__ __forceinline__ int scale_exp(uint32_t m, int bf16) {
   if (m == 0) return 0;

@@ -187,7 +187,7 @@ struct Score {
 // and is lowered (with the sums: powers of two, exact) when a value scale
 // asks for it, so that small weights of small values stay normal numbers: with a
 // gain of 4 for all, weights of 2^-12 were lost where values are below 0.01.
-constexpr float kRise = 4.0f, kTop = 4094.0f, kFirstGain = 68719476736.0f;   // 2^36: any scale's
+constexpr float kRise = 4.0f, kTop = 4094.0f, kFirstGain = 0x1p100f;
 
 // Weights as B fragments: each is the sum of two fp16 numbers, so that nothing
 // of a weight above some 2^-36 is lost to their rounding (the products for it
@@ -375,6 +375,23 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
         mma_16816k16_f16(c[NT - 1], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], q.z, q.w);
     }
   }
+  // bf16 values are scaled to fp16's range by a power of two, the weights back
+  const int tok = lane >> 1;
+  const uint16_t* V = static_cast<const uint16_t*>(p.V) + (tok0 + j0 + tok) * p.kv_stride + off;
+  float vup = 1.0f, vdown = f.gain;
+  if (p.kv_bf16) {
+    uint32_t mx = 0;
+    if (j0 + tok < n) {
+#pragma unroll 4
+      for (int k = lane & 1; k < 16; k += 2) {
+        const uint4 x = *reinterpret_cast<const uint4*>(V + 8 * k);
+        mx = held_bits(held_bits(held_bits(held_bits(mx, x.x), x.y), x.z), x.w);
+      }
+    }
+    const int e = scale_exp(__reduce_max_sync(0xFFFFFFFFu, mx), 1);
+    vup = pow2i(e);
+    vdown *= pow2i(-e);
+  }
   uint32_t see = 0;
   Weights<NT> w;
 #pragma unroll 1
@@ -385,21 +402,19 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
       if (p.mask ? (p.mask[tok0 + i] >> j) & 1 : j <= i) see |= 1u << e;
     }
   }
-  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], f.gain, f.gain, pos[0], pos[1], see, w);
+  weights<NT, CAP, BIAS>(f, sc, c, down[0], down[1], vdown, vdown, pos[0], pos[1], see, w);
   // values: 64 dims at a time as fp16 rows of 128 bytes (16-byte chunks permuted
   // by the token's low bits), read back transposed.  A value that fp16 does
   // not hold enters as 0 and is added by write_row.
   bool out = false;
-  const int tok = lane >> 1, m = lane >> 3, from = (lane & 7) + 8 * (m >> 1);
+  const int m = lane >> 3, from = (lane & 7) + 8 * (m >> 1);
 #pragma unroll
   for (int hv = 0; hv < 2; ++hv) {
     __syncwarp();
 #pragma unroll 1
     for (int k = 4 * (lane & 1); k < 4 * (lane & 1) + 4; ++k) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (j0 + tok < n)
-        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.V) +
-                                            (tok0 + j0 + tok) * p.kv_stride + off + 64 * hv + 8 * k);
+      if (j0 + tok < n) x = *reinterpret_cast<const uint4*>(V + 64 * hv + 8 * k);
       uint32_t z[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -412,7 +427,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
           y.y = 0.0f;
           out = true;
         }
-        z[e] = pack_f16x2(y.x, y.y);
+        z[e] = pack_f16x2(y.x * vup, y.y * vup);
       }
       sts128(scratch + 128 * tok + ((k ^ (tok & 7)) << 4), make_uint4(z[0], z[1], z[2], z[3]));
     }
@@ -430,7 +445,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
   if (out) *(volatile int*)bad = 1;
 }
 
-template <int NT, int CAP, bool BIAS>
+template <int NT, int CAP, bool BIAS, bool DRAFT>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     tree_rows_kernel(const __grid_constant__ TreeParams p) {
   using S = Shape<NT>;
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     if (more) keep_ids(seg ^ 1, id);
     // the rows' fragments in shared memory are there (one column block: only the
     // drafted tokens read them)
-    if (NT == 2 || sg.dparts > 0) __syncthreads();
+    if (NT == 2 || (DRAFT && sg.dparts > 0)) __syncthreads();
     for (int w0 = 0; w0 < sg.pages || w0 == 0; w0 += kWindow) {
       const int held = min(kWindow, sg.pages - w0);
       if (w0 > 0) {
@@ -657,7 +672,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       // (the first turn only loads)
 #pragma unroll 1
       for (int q = stream - streams; q < total; q += streams) {
-        if (q >= store) {
+        if (DRAFT && q >= store) {
           draft_tokens<NT, CAP, BIAS>(p, fr, sc, sg, 16 * (q - store), row0, G, lane,
                                       smem_u32(&f.o[0][0][0]) + warp * kScratch,
                                       &f.bad[seg]);
@@ -767,7 +782,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       }
     }
 
-    if (sg.dparts > 0) __syncthreads();  // (the drafted values' scratch lies where the sums go)
+    if (DRAFT && sg.dparts > 0) __syncthreads();  // (the drafted values' scratch lies where the sums go)
     // the warps' sums meet: the second half's in the first half's registers,
     // those in shared memory (a warp and the one kHalf behind it have the
     // same rows)
@@ -819,7 +834,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       __syncthreads();
     }
     if (tid == 0) f.bad[seg ^ 1] = 0;
-    const bool bad = *(volatile int*)&f.bad[seg] != 0;
+    const bool bad = DRAFT && *(volatile int*)&f.bad[seg] != 0;
     for (int r = warp; r < sg.n * G; r += S::kWarps) {
       const int blk = r >= S::kRows ? 1 : 0, lr = r - S::kRows * blk;
       float m = -INFINITY, l = 0.0f;
@@ -854,12 +869,15 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 
 template <int NT, int CAP, bool BIAS>
 cudaError_t launch(const TreeParams& p, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(tree_rows_kernel<NT, CAP, BIAS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // few rows over the store alone: the drafted tokens' code in the loop costs them
+  // registers (one capped token over the 128K context: 76 us with it, 73 without,
+  // 64 sequences with one biased token 238 and 221)
+  const auto kernel = NT == 1 && !p.K ? tree_rows_kernel<NT, CAP, BIAS, NT != 1>
+                                      : tree_rows_kernel<NT, CAP, BIAS, true>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kRowsSmem);
   if (e != cudaSuccess) return e;
-  tree_rows_kernel<NT, CAP, BIAS>
-      <<<(unsigned)p.S, Shape<NT>::kThreads, kRowsSmem, stream>>>(p);
+  kernel<<<(unsigned)p.S, Shape<NT>::kThreads, kRowsSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
