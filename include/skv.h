@@ -499,7 +499,8 @@ int skv_decode_attention_static(skv_ctx* ctx, const void* q, int q_dtype, int B,
    exactly, but for elements below 2^-38 of their row's largest), drafted bf16
    values by one that their largest of the sequence and kv head asks for (what
    fp16 loses of them lies below 2^-19 of that); those above fp16's range are
-   added in fp32. */
+   added in fp32.  (Keys of 2^105 and above may overflow a score that tiny
+   queries would bring back into range.) */
 typedef struct skv_tree {
   int32_t N;              /* drafted tokens a sequence, 1..64 */
   int32_t kv_dtype;       /* SKV_Q_FP16 / SKV_Q_BF16: type of K and V */
@@ -557,7 +558,9 @@ int skv_tree_attention(skv_ctx* ctx, const void* q, int q_dtype, int B, int Hq, 
    skv_allocate: per unit the T0, T1, T2 pages, rows in position order, in
    slots free->ids[t][free_cursor[t] + k] (k in unit order).  The store before
    the call is only read, so all its pages may go back to the caller's free
-   lists once nothing reads it any more.
+   lists once nothing reads it any more.  free_cursor is only read too: two
+   evictions from one cursor, or an append to the old store after one, would
+   take the same slots.
      seq_lens   int32 [B] device
      score      fp32 [B][Hkv][Tmax] device (skv_decode_utility's utility)
      protect    uint8 [B][Hkv][Tmax] device or NULL

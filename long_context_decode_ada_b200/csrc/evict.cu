@@ -16,7 +16,10 @@
 // What bounds it: the move, by DRAM traffic and its latency.  The pages keep
 // two rows' values in every 16 bytes, so that a kept row brings its
 // neighbours' bytes along: 518 MB read and 232 MB written on the ragged batch
-// (175 us, 4.3 TB/s), against 2 x 130 MB of kept rows.
+// (175 us, 4.3 TB/s) for some 255 MB of kept rows; at 6.5 TB/s those bytes would
+// take 118 us.  The rest of its 224 us is the select, with DRAM idle (on the 128K
+// context some 50 of 128).  The register selects spill 60 (8 positions a thread)
+// and 128 bytes (16).
 #include <cooperative_groups.h>
 
 #include <algorithm>

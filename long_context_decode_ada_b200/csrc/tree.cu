@@ -39,22 +39,27 @@
 // running maximum is raised (and O rescaled) only when a score passes it by
 // more than 2^8, so weights stay within fp16.
 //
-// What bounds it is neither the products (tensor cores 17% busy) nor HBM but
-// the conversion and the softmax around them: instruction issue, 49% busy at
-// 128 rows, with five roles' loops sharing one instruction cache.  Measured
-// over the 128K store (1.05 M token-heads): 32 tokens (128 rows) 169 us; 171 us
-// before units' take-up was weighed as it is, 209 us with waits of 35 instructions at their 25 places
-// (instruction cache misses 3.6 M against 0.7 M a launch); pages loaded by the
+// What bounds it is neither the products (tensor cores 21% busy) nor HBM nor
+// instruction issue (49% busy at 128 rows) but the hand-overs between the roles
+// and the ends of segments: from a segment's last tile to the next one's first
+// product pass 47,000 to 60,000 cycles, in which the pipe drains, the sums are
+// written in eight steps and the next queries are read.  Five roles' loops
+// share one instruction cache: a few instructions more in a cold branch have
+// moved the prompt batch (265 us) by 2 to 28%.  Measured over the 128K store
+// (1.05 M token-heads): 32 tokens (128 rows) 166 us; 171 us before units' take-up
+// was weighed as it is, 209 us with waits of 35 instructions at their 25 places
+// (instruction cache misses 3.6 M against 0.6 M a launch); pages loaded by the
 // decode warps themselves instead of by bulk copies 231 us; tiles of 64 tokens
 // with one warp issuing both products 274 us.  Three decode teams instead of
-// two change nothing (175 us).
+// two change nothing (175 us against 171).  Spills: up to 20 bytes a thread.
 //
 // Roundings: a coded key is a table entry times its radius (two fp16
 // roundings), a value an int8 times its scale (one), a weight one; each is
 // 2^-11 of its number at most.  Together they put an output about 0.0004 of
 // its size off; bf16 outputs are rounded by 0.0017 anyway, fp16 ones by 0.0002.
 // Exact values and split weights, as in the form for few rows, would double
-// the second product and need 64 columns of tensor memory that are not there.
+// the second product and need 64 columns of tensor memory: with one block's
+// queries in shared memory they would be there, which is not tried.
 //
 // Tensor memory (512 columns): Q 0-63 (and 64-127 for the second block), P of
 // the streams at 64 and 96 (over S with two blocks), S at 128 and 192, O at

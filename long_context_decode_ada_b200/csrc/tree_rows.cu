@@ -18,14 +18,16 @@
 // flight pass through the L1, and with 28 KB of it (shared memory full) the
 // ragged batch of 64 with 8 tokens took 487 us against 415.
 //
-// What bounds it: instruction issue (41 to 45% busy with three warps a
-// scheduler; registers allow no more) and the latency behind it; HBM 2.7 TB/s
-// on single tokens over the 128K store (78 us), tensor cores 16% busy on the
-// ragged batch (308 us; 364 us in the tensor-memory form, which wins from 33
-// rows on: its conversion costs the same for 1 row as for 64).  12 warps: 16
-// with 128 registers each spill (biased single tokens 260 us against 214), 8
-// hide less.  L2 prefetches ahead of the loads cost more than they hide (333
-// against 316 us).
+// What bounds it: latency.  Instruction issue is 39 to 42% busy with three warps
+// a scheduler (registers allow no more), HBM gives 2.9 TB/s on single tokens
+// over the 128K store (74 us), tensor cores are 23% busy on the ragged batch
+// (309 us, of which 3.6 segments a block cost some 10 us each to take up and to
+// put down behind block-wide barriers; 364 us in the tensor-memory form, which
+// wins from 33 rows on: its conversion costs the same for 1 row as for 64).
+// 12 warps: 16 with 128 registers each spill (biased single tokens 260 us
+// against 214), 8 hide less.  L2 prefetches ahead of the loads cost more than they
+// hide (333 against 316 us).  Two column blocks spill 48 bytes a thread (136 with
+// a bias), one up to 24.
 #include <algorithm>
 
 #include "tree.cuh"
@@ -192,7 +194,9 @@ constexpr float kRise = 4.0f, kTop = 4094.0f, kFirstGain = 0x1p100f;
 // Weights as B fragments: each is the sum of two fp16 numbers, so that nothing
 // of a weight above some 2^-36 is lost to their rounding (the products for it
 // cost less than scaling the values, which would round them: one fp16 store
-// 0.0002 off, as its output's rounding alone, against 0.00034).
+// 0.0002 off, as its output's rounding alone, against 0.00034).  bf16 results
+// would not show it: they take the same path, 17 us of the ragged batch's 309,
+// rather than instances of their own.
 template <int NT>
 struct Weights {
   uint32_t hi[NT][2], lo[NT][2];

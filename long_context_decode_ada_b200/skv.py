@@ -695,11 +695,14 @@ class PagedCache:
         positions, the last `recent` and the protected ones.  score fp32
         [B][Hkv][Tmax] (the utility that decode_utility accumulates), keep
         int32 [B].  The result is `into` (made by spare(); a new one when
-        None), a store over the same pools whose pages take free slots; this
-        store stays as it is, and its pages may be reused once nothing reads
-        it.  Device errors are in the result's error word.  Calls on one store
-        share its workspace: they must not overlap in time (nor must captured
-        graphs of it)."""
+        None), a store over the same pools whose pages take the free slots from
+        this store's cursor on; this store stays as it is, its cursor included:
+        appended to, retiered or evicted once more it would take the same slots
+        as the result.  Its own pages (page_ids up to page_indptr[-1]) may go
+        into new free lists (set_free_lists) once nothing reads it.  Device
+        errors are in the result's error word.  Calls on one store share its
+        workspace: they must not overlap in time (nor must captured graphs of
+        it)."""
         n = self.B * self.Hkv * self.Tmax
         self._own(score, "score", n, torch.float32)
         self._own(seq_lens, "seq_lens", self.B, torch.int32)
