@@ -379,7 +379,8 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
         mma_16816k16_f16(c[NT - 1], a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1], q.z, q.w);
     }
   }
-  // bf16 values are scaled to fp16's range by a power of two, the weights back
+  // small bf16 values enter times a power of two, their largest between 1 and 2,
+  // the weights back (further up the weights would lose what the values gain)
   const int tok = lane >> 1;
   const uint16_t* V = static_cast<const uint16_t*>(p.V) + (tok0 + j0 + tok) * p.kv_stride + off;
   float vup = 1.0f, vdown = f.gain;
@@ -392,7 +393,7 @@ __device__ __forceinline__ void draft_tokens(const TreeParams& p, Frag<NT>& f, c
         mx = held_bits(held_bits(held_bits(held_bits(mx, x.x), x.y), x.z), x.w);
       }
     }
-    const int e = scale_exp(__reduce_max_sync(0xFFFFFFFFu, mx), 1);
+    const int e = max(0, scale_exp(__reduce_max_sync(0xFFFFFFFFu, mx), 1) - 14);
     vup = pow2i(e);
     vdown *= pow2i(-e);
   }
