@@ -237,6 +237,12 @@ def _token_stride(t: torch.Tensor, name: str, shape, device) -> int:
     return sn
 
 
+def _under(stream):
+    """Buffers made inside are allocated and filled on the call's stream: in
+    order with its kernels, and not handed out again before they end."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
@@ -375,10 +381,11 @@ class PagedCache:
         _expect(K_new, "K_new", self.B * self.Hkv * self.ctx.d, 2)
         _expect(V_new, "V_new", self.B * self.Hkv * self.ctx.d, 2)
         _expect(seq_lens, "seq_lens", self.B, 4, torch.int32)
-        cursor = self.free_cursor()
-        if getattr(self, "_ws_append", None) is None:
-            n = self.ctx.workspace_size(WS_APPEND, self.B, self.Hkv, 0, self.page_cap)
-            self._ws_append = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        with _under(stream):
+            cursor = self.free_cursor()
+            if getattr(self, "_ws_append", None) is None:
+                n = self.ctx.workspace_size(WS_APPEND, self.B, self.Hkv, 0, self.page_cap)
+                self._ws_append = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
         free0 = self._free[0]
         _check(lib().skv_append(
             self.ctx.handle, _ptr(K_new), _ptr(V_new), self.B, self.Hkv, self.Tmax, _ptr(seq_lens),
@@ -409,15 +416,16 @@ class PagedCache:
         _check_ingest(self.B, self.Hkv, self.Tmax, self.ctx.d, seq_lens=seq_lens,
                       utility=utility, budget=budget)
         _expect(demote, "demote", self.B * self.Hkv * self.Tmax, 1)
-        cursor = self.free_cursor()
-        if getattr(self, "_ws_retier", None) is None:
-            n = C.c_size_t()
-            _check(lib().skv_retier_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
-                                                   self.page_cap, C.byref(n)))
-            self._ws_retier = torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.device)
-            self.released = torch.zeros(max(1, self.page_cap), dtype=torch.int32,
-                                         device=self.device)
-            self.n_released = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with _under(stream):
+            cursor = self.free_cursor()
+            if getattr(self, "_ws_retier", None) is None:
+                n = C.c_size_t()
+                _check(lib().skv_retier_workspace_size(self.ctx.handle, self.B, self.Hkv, self.Tmax,
+                                                       self.page_cap, C.byref(n)))
+                self._ws_retier = torch.empty(max(n.value, 1), dtype=torch.uint8, device=self.device)
+                self.released = torch.zeros(max(1, self.page_cap), dtype=torch.int32,
+                                             device=self.device)
+                self.n_released = torch.zeros(1, dtype=torch.int32, device=self.device)
         _check(lib().skv_retier(
             self.ctx.handle, self.B, self.Hkv, self.Tmax, _ptr(seq_lens), _ptr(utility),
             _ptr(demote), _ptr(budget), C.byref(self._free_c), _ptr(cursor),
@@ -440,9 +448,10 @@ class PagedCache:
 
     def decode(self, q: torch.Tensor, q_dtype: int, Hq: int, out=None, lse=None,
                workspace=None, num_splits: int = 0, stream=None):
-        out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
-        if workspace is None:
-            workspace = self.workspace(Hq, num_splits)
+        with _under(stream):
+            out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
+            if workspace is None:
+                workspace = self.workspace(Hq, num_splits)
         _check(lib().skv_decode_attention(
             self.ctx.handle, _ptr(q), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None,
@@ -463,9 +472,10 @@ class PagedCache:
         if utility.dtype != torch.float32 or tuple(utility.shape) != (self.B, self.Hkv, self.Tmax) \
                 or not utility.is_contiguous():
             raise SkvError(SKV_ERR_ARG, "utility must be contiguous fp32 [B][Hkv][Tmax]")
-        out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
-        if workspace is None:
-            workspace = self.utility_workspace(Hq, num_splits)
+        with _under(stream):
+            out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
+            if workspace is None:
+                workspace = self.utility_workspace(Hq, num_splits)
         _check(lib().skv_decode_utility(
             self.ctx.handle, _ptr(q), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None,
@@ -501,7 +511,8 @@ class PagedCache:
             for t, name in ((lse_host, "lse_host"), (lse_dev, "lse_dev")):
                 _expect(t, name, self.B * Hq, 4, torch.float32, cuda=False)
         if workspace is None:
-            workspace = self.workspace(Hq, num_splits)
+            with _under(stream):
+                workspace = self.workspace(Hq, num_splits)
         _check(lib().skv_decode_attention_host(
             self.ctx.handle, _ptr(q_host), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None,
@@ -530,7 +541,8 @@ class PagedCache:
         _expect(res_host, "res_host", n + self.B * Hq, 4, torch.float32, cuda=False)
         _expect(res_dev, "res_dev", 2 * (n + self.B * Hq), 4, torch.float32, cuda=False)
         if workspace is None:
-            workspace = self.workspace(Hq, num_splits)
+            with _under(stream):
+                workspace = self.workspace(Hq, num_splits)
         _check(lib().skv_decode_attention_host_pipelined(
             self.ctx.handle, _ptr(q_host), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None, _ptr(self.page_ids),
@@ -541,7 +553,8 @@ class PagedCache:
                       num_splits: int = 0, stream=None):
         """decode() with the library's fixed scratch instead of a workspace
         (skv_decode_attention_static: calls must not overlap in time)."""
-        out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
+        with _under(stream):
+            out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
         _check(lib().skv_decode_attention_static(
             self.ctx.handle, _ptr(q), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_tier_indptr) if self.split_by_bytes else None,
@@ -564,12 +577,6 @@ class PagedCache:
         if s.device != dev:
             raise SkvError(SKV_ERR_ARG, f"stream: on {s.device}, the store is on {dev}")
         return C.c_void_p(s.cuda_stream)
-
-    @staticmethod
-    def _under(stream):
-        """Buffers made inside are allocated and filled on the call's stream:
-        in order with its kernels, and not handed out again before they end."""
-        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
     def tree_workspace(self, N: int, Hq: int, positions: bool = False,
                        num_splits: int = 0) -> torch.Tensor:
@@ -632,7 +639,7 @@ class PagedCache:
             sc.row_of, sc.seq_lens = self.row_of.data_ptr(), seq_lens.data_ptr()
             sc.Tmax = self.Tmax
         to = self._own_stream(stream)
-        with self._under(stream):
+        with _under(stream):
             if out is None:
                 out = torch.zeros((self.B, N, Hq, self.ctx.d), dtype=q.dtype, device=dev)
             if workspace is None:
@@ -710,7 +717,7 @@ class PagedCache:
         self._own(protect, "protect", n, torch.uint8)
         to = self._own_stream(stream)
         if into is None:
-            with self._under(stream):
+            with _under(stream):
                 into = self.spare()
         if into is self or into.tier is self.tier:
             raise SkvError(SKV_ERR_ARG, "evict: into must be another store (see spare())")
@@ -719,7 +726,7 @@ class PagedCache:
         if getattr(self, "_free_c", None) is None:
             raise SkvError(SKV_ERR_ARG, "evict: the store has no free lists (set_free_lists)")
         into._free, into._free_c = self._free, self._free_c
-        with self._under(stream):
+        with _under(stream):
             cursor = self.free_cursor()
             if getattr(self, "_ws_evict", None) is None:
                 self._ws_evict = self._evict_workspace()
@@ -787,9 +794,10 @@ class DenseCache:
 
     def decode(self, q, q_dtype, Hq, out=None, lse=None, workspace=None, num_splits=0,
                stream=None):
-        out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
-        if workspace is None:
-            workspace = self.workspace(Hq, num_splits)
+        with _under(stream):
+            out, lse = _decode_buffers(self.B, Hq, self.ctx.d, q, out, lse, self.device)
+            if workspace is None:
+                workspace = self.workspace(Hq, num_splits)
         _check(lib().skv_dense_decode_bf16(
             self.ctx.handle, _ptr(q), q_dtype, self.B, Hq, self.Hkv, _ptr(self.page_indptr),
             _ptr(self.page_ids), _ptr(self.pool), self.pool_slots, _ptr(out), _ptr(lse),
